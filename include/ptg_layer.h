@@ -1,0 +1,250 @@
+/*
+ * ptg_layer.h - C ABI of the layer operators around the persistent tiled GEMM
+ * (MI355X, gfx950): the RMS norm with the residual's addition, the matrix
+ * product with bias, activation and residual in its epilogue, and the
+ * gradients of both. Together they are a pre-norm feed-forward layer:
+ *
+ *   layer_rmsnorm              s = x + residual, y = s / rms(s) * weight, bf16, fp32 or
+ *                              e4m3 with one scale a row (the next product's operand)
+ *   layer_linear               out = act(x . w^T + bias) + residual
+ *   layer_activation_backward  dpre = dout * act'(pre), dbias
+ *   layer_linear_backward      dx = dpre . w, dw = dpre^T . x
+ *   layer_rmsnorm_backward     dx (of x and of residual alike), dweight
+ *
+ * Layouts. Matrices are row-major with a row stride in elements (ld*), rows
+ * dense; a weight is n x k as a linear layer keeps it. Device pointers only,
+ * 16-byte aligned. Row lengths and strides are multiples of 8 elements (16 for
+ * e4m3 operands of a product); the number of rows m is arbitrary, 0 included.
+ * A stride is at least the row's length; with m <= 1, or rows of no elements, it is
+ * not looked at.
+ *
+ * Types. Stream and operand types are named per argument. Sums, norms,
+ * products and activations are held in fp32; each output is rounded once, to
+ * the nearest value of its type, from the fp32 result.
+ *
+ * Ownership, streams, errors. As in ptg_gemm.h: the caller owns every tensor
+ * and keeps it alive until the stream has passed the call; calls are
+ * asynchronous and stream-ordered and allocate nothing; arguments are checked
+ * before anything is enqueued. The plan (layer_cfg) owns the scratch: the tile
+ * schedulers' state, the split products' partial sums and the partial column
+ * sums. Calls of one plan on different streams are ordered on the device (a
+ * call waits for the plan's previous stream), so that stream must stay valid
+ * until the plan's next call, layer_sync or layer_destroy. A plan is not
+ * thread-safe. layer_rmsnorm needs no plan.
+ *
+ * Graph capture. Every call may be captured once the plan's last call was made
+ * on the capture stream (a call on a new stream waits with an event for the
+ * previous one, which a capture refuses). A replay uses the plan's scratch like
+ * a call: order replays and other calls of the same plan on one stream.
+ *
+ * No result depends on the order in which workgroups run: sums that several
+ * workgroups share are written as partial sums and added in a fixed order.
+ */
+#ifndef PTG_LAYER_H
+#define PTG_LAYER_H
+
+#include "ptg_gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types. */
+#define LAYER_F32 0
+#define LAYER_BF16 1
+#define LAYER_E4M3 2 /* 8 bits, 4 exponent and 3 mantissa bits, largest value 448, no infinities */
+
+/*
+ * Activations of a pre-activation z:
+ *   NONE z;  RELU max(z, 0) (gradient 0 at z = 0; NaN stays NaN);
+ *   GELU z (1 + erf(z / sqrt 2)) / 2;
+ *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2;
+ *   SILU z / (1 + exp(-z)).
+ */
+#define LAYER_ACT_NONE 0
+#define LAYER_ACT_RELU 1
+#define LAYER_ACT_GELU 2
+#define LAYER_ACT_GELU_TANH 3
+#define LAYER_ACT_SILU 4
+
+/* Size limits (GEMM_E_SHAPE beyond them). */
+#define LAYER_MAX_ROWS (1 << 30)
+#define LAYER_MAX_COLS (1 << 20)     /* n, k and row strides */
+#define LAYER_MAX_NORM_COLS (1 << 15) /* n of the norm: a row is held in one workgroup's registers */
+
+/* Opaque plan: owns all scratch. */
+typedef struct layer_plan *layer_cfg;
+
+/*
+ * Build a plan on `device`, which must be the current device and gfx950. All
+ * allocation happens here (about 100 MiB: the split products' partial sums for
+ * both tile sizes, which the column sums share). Errors: GEMM_E_INVALID_ARG
+ * (out NULL, no such device), GEMM_E_UNSUPPORTED, GEMM_E_DEVICE, GEMM_E_NOMEM,
+ * GEMM_E_HIP.
+ */
+gemm_status layer_create(layer_cfg *out, int32_t device);
+
+/* Release the plan (synchronises its last stream first). NULL is a no-op. */
+gemm_status layer_destroy(layer_cfg cfg);
+
+/*
+ * Synchronise the plan's last stream and return (then clear) the device-side
+ * status of its products, as gemm_sync does. GEMM_OK before the first call.
+ */
+gemm_status layer_sync(layer_cfg cfg);
+
+/* Text of the last HIP error seen by this plan ("" if none). */
+const char *layer_last_hip_error(layer_cfg cfg);
+
+/*
+ * s = x + residual (residual NULL: s = x); r = 1 / sqrt(mean_j s_j^2 + eps);
+ * y_j = s_j r weight_j. The sum enters the norm unrounded; sum_out (NULL: not
+ * kept) receives it rounded to `type`, and may be x or residual itself (same
+ * pointer and stride: the residual stream updated in place).
+ *
+ * out_type LAYER_E4M3: `scale` receives one fp32 value a row, max_j |y_j| / 448
+ * (at least 2^-126; 1 where the row's y is all zeros), and out the codes
+ * y_j / scale. The scale's reader multiplies: y is about code * scale. A row
+ * whose y holds a NaN or an infinity gets a NaN scale and NaN codes. scale must
+ * be NULL for the other types.
+ *
+ * Squares are summed in fp32: a row whose sum of squares passes 3.4e38
+ * (values of about 1e18 and more) has r = 0.
+ * weight may be NULL (all ones). weight_type: LAYER_F32 or LAYER_BF16.
+ * One launch. m == 0 or n == 0 enqueues nothing.
+ * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, an unknown type, a
+ * scale where there is none to write or none where there is, eps negative or
+ * NaN), GEMM_E_SHAPE (negative, not a multiple of 8, over a limit, a stride
+ * shorter than the row), GEMM_E_UNSUPPORTED (current device not gfx950), GEMM_E_HIP.
+ */
+typedef struct layer_rmsnorm_args {
+  const void *x;        /* m x n, type */
+  const void *residual; /* m x n, type, or NULL */
+  const void *weight;   /* n, weight_type, or NULL */
+  void *sum_out;        /* m x n, type, or NULL */
+  void *out;            /* m x n, out_type */
+  float *scale;         /* m, e4m3 outputs only */
+  int64_t m, n;
+  int64_t ldx, ldr, lds, ldo;
+  int32_t type;         /* LAYER_F32 or LAYER_BF16: x, residual, sum_out */
+  int32_t weight_type;
+  int32_t out_type;     /* LAYER_F32, LAYER_BF16 or LAYER_E4M3 */
+  float eps;
+} layer_rmsnorm_args;
+
+gemm_status layer_rmsnorm(const layer_rmsnorm_args *args, void *stream);
+
+/*
+ * The gradient at a given s (the forward pass's sum_out, or x without a
+ * residual): with r as above (computed again from s), h = s r and
+ * g = dy weight,
+ *   dx_j = r (g_j - h_j mean_i(g_i h_i)) + dsum_j     (the gradient of x and of residual)
+ *   dweight_j = sum_m dy_mj h_mj                       (+ dweight_j with `accumulate`)
+ * dsum: the gradient that reaches sum_out from the rest of the network (NULL:
+ * none). dx (NULL: not wanted) may be dsum itself (same pointer and stride).
+ * dweight (fp32, NULL: not wanted). With m == 0 dweight is zeroed (unless
+ * accumulate is set). Errors as layer_rmsnorm, and GEMM_E_DEVICE.
+ */
+typedef struct layer_rmsnorm_grad_args {
+  const void *dy;     /* m x n, dy_type */
+  const void *s;      /* m x n, type */
+  const void *weight; /* n, weight_type, or NULL (all ones) */
+  const void *dsum;   /* m x n, type, or NULL */
+  void *dx;           /* m x n, type, or NULL */
+  float *dweight;     /* n, or NULL */
+  int64_t m, n;
+  int64_t lddy, lds, lddsum, lddx;
+  int32_t type;       /* LAYER_F32 or LAYER_BF16: s, dsum, dx */
+  int32_t dy_type;    /* LAYER_F32 or LAYER_BF16 */
+  int32_t weight_type;
+  int32_t accumulate; /* 1: add to dweight instead of overwriting it */
+  float eps;
+} layer_rmsnorm_grad_args;
+
+gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *args, layer_cfg cfg, void *stream);
+
+/*
+ * z_mn = x_scale_m w_scale_n sum_k x_mk w_nk + bias_n;  pre = z;
+ * out = act(z) + residual.
+ * in_type LAYER_BF16: x and w are bf16, x_scale and w_scale NULL.
+ * in_type LAYER_E4M3: x and w are e4m3; x_scale (m, fp32; NULL: 1) and w_scale
+ * (n, fp32; NULL: 1) are their row scales. k is then a multiple of 16.
+ * pre (bf16, NULL: not kept) receives z for layer_activation_backward. The
+ * activation is taken of the unrounded z. residual may be out itself (same
+ * pointer, stride and type). k == 0 gives z = bias. m == 0 or n == 0 enqueues
+ * nothing.
+ * Few rows (a decode step) read every weight once and split k over the machine
+ * when n alone does not fill it; many rows run as tiles under the dynamic tile
+ * scheduler. One launch either way.
+ * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, an unknown type or
+ * activation, a scale with bf16 operands), GEMM_E_SHAPE, GEMM_E_DEVICE,
+ * GEMM_E_HIP.
+ */
+typedef struct layer_linear_args {
+  const void *x;         /* m x k, in_type */
+  const void *w;         /* n x k, in_type */
+  const float *x_scale;  /* m, or NULL */
+  const float *w_scale;  /* n, or NULL */
+  const void *bias;      /* n, bias_type, or NULL */
+  const void *residual;  /* m x n, residual_type, or NULL */
+  void *pre;             /* m x n, bf16, or NULL */
+  void *out;             /* m x n, out_type */
+  int64_t m, n, k;
+  int64_t ldx, ldw, ldr, ldp, ldo;
+  int32_t in_type;       /* LAYER_BF16 or LAYER_E4M3 */
+  int32_t bias_type;     /* LAYER_F32 or LAYER_BF16 */
+  int32_t residual_type; /* LAYER_F32 or LAYER_BF16 */
+  int32_t out_type;      /* LAYER_F32 or LAYER_BF16 */
+  int32_t activation;
+  int32_t pad;
+} layer_linear_args;
+
+gemm_status layer_linear(const layer_linear_args *args, layer_cfg cfg, void *stream);
+
+/*
+ * dpre_mn = dout_mn act'(pre_mn), rounded to bf16, and dbias_n = sum_m of it
+ * before that rounding (fp32; + dbias_n with `accumulate`). dpre or dbias may be
+ * NULL (not wanted); dpre may be dout or pre itself (same stride). pre is not
+ * read with LAYER_ACT_NONE and may be NULL then. With m == 0 dbias is zeroed
+ * (unless accumulate is set). Errors as layer_linear.
+ */
+typedef struct layer_activation_grad_args {
+  const void *dout; /* m x n, bf16 */
+  const void *pre;  /* m x n, bf16 */
+  void *dpre;       /* m x n, bf16, or NULL */
+  float *dbias;     /* n, or NULL */
+  int64_t m, n;
+  int64_t lddo, ldp, lddp;
+  int32_t activation;
+  int32_t accumulate;
+} layer_activation_grad_args;
+
+gemm_status layer_activation_backward(const layer_activation_grad_args *args, layer_cfg cfg, void *stream);
+
+/*
+ * dx_mk = sum_n dpre_mn w_nk and dw_nk = sum_m dpre_mn x_mk (+ dw_nk with
+ * `accumulate`, read in dw's type). dpre, x and w are bf16; dx and dw (NULL: not wanted)
+ * fp32 or bf16. x is only read for dw, w only for dx. One launch each. With
+ * m == 0 dw is zeroed (unless accumulate is set). Errors as layer_linear.
+ */
+typedef struct layer_linear_grad_args {
+  const void *dpre; /* m x n */
+  const void *x;    /* m x k */
+  const void *w;    /* n x k */
+  void *dx;         /* m x k, dx_type, or NULL */
+  void *dw;         /* n x k, dw_type, or NULL */
+  int64_t m, n, k;
+  int64_t lddp, ldx, ldw, lddx, lddw;
+  int32_t dx_type;  /* LAYER_F32 or LAYER_BF16 */
+  int32_t dw_type;  /* LAYER_F32 or LAYER_BF16 */
+  int32_t accumulate;
+  int32_t pad;
+} layer_linear_grad_args;
+
+gemm_status layer_linear_backward(const layer_linear_grad_args *args, layer_cfg cfg, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PTG_LAYER_H */

@@ -447,3 +447,7 @@ def matmul(A, B, mode="dynamic", plan: Optional[Plan] = None, stream=None):
         if own:
             plan.destroy()
     return C
+
+
+from .layer import (ACTIVATIONS, LAYER_ABI_FUNCTIONS, LayerPlan, layer_activation_backward, layer_create, layer_destroy,  # noqa: E402,F401
+                    layer_last_hip_error, layer_linear, layer_linear_backward, layer_rmsnorm, layer_rmsnorm_backward, layer_sync)

@@ -8,15 +8,19 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO, "include")
+JOBS = 4  # compilers at a time
 LIB_NAME = "libptg_gemm.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
-SOURCES = ["gemm_kernel.hip", "spoiler.hip", "mfma_probe.hip", "hbm_probe.hip", "gemm_api.hip"]
+SOURCES = ["gemm_kernel.hip", "spoiler.hip", "mfma_probe.hip", "hbm_probe.hip", "gemm_api.hip",
+           "layer_api.hip", "norm_kernel.hip", "act_kernel.hip", "product_simple.hip"]
 
 # gfx950 only. Packed-fp32 VALU forms are disabled (hipcc makes them from plain
 # float code; some of their forms have produced wrong results on this part).
@@ -40,19 +44,27 @@ def hipcc() -> str:
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into LIB_PATH; return its path. Always rebuilds."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, *srcs, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    flags = [*HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC]
     # the host pass does not know the packed-fp32 target feature; that warning is harmless
     noise = "'-packed-fp32-ops' is not a recognized feature"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    with tempfile.TemporaryDirectory(prefix="ptg_build_") as objs, ThreadPoolExecutor(JOBS) as pool:
+        out = {s: os.path.join(objs, s + ".o") for s in SOURCES}
+        # one compiler per source, a few at a time, then one link
+        list(pool.map(lambda s: run([hipcc(), *(f for f in flags if f != "-shared"), "-c", os.path.join(CSRC, s), "-o", out[s]]),
+                      SOURCES))
+        run([hipcc(), *HIPCC_FLAGS, *out.values(), "-o", tmp])
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,386 @@
+// Host side of the layer operators' C ABI (include/ptg_layer.h): argument
+// checks, the plan and its scratch, and the choice of kernel per call.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+#include <string>
+
+#include "layer_internal.hpp"
+#include "ptg_layer.h"
+
+static_assert(LAYER_F32 == ptg::kTypeF32 && LAYER_BF16 == ptg::kTypeBf16 && LAYER_E4M3 == ptg::kTypeE4m3, "types");
+static_assert(LAYER_ACT_NONE == ptg::kActNone && LAYER_ACT_RELU == ptg::kActRelu && LAYER_ACT_GELU == ptg::kActGelu &&
+                  LAYER_ACT_GELU_TANH == ptg::kActGeluTanh && LAYER_ACT_SILU == ptg::kActSilu, "activations");
+
+struct layer_plan {
+  int device = 0;
+  int cu_count = 0;
+  float *d_ws = nullptr;  // partial sums
+  hipEvent_t stream_switch = nullptr;
+  hipStream_t last_stream = nullptr;
+  bool has_run = false;
+  std::string last_error;
+};
+
+namespace {
+
+constexpr int64_t kWsFloats = 16 << 20;  // 64 MiB: 16 partial rows of the widest column sum
+
+gemm_status hip_fail(layer_plan *p, hipError_t e, const char *what) {
+  if (p) p->last_error = std::string(what) + ": " + hipGetErrorString(e);
+  return GEMM_E_HIP;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One device property read per device and process: the layer_rmsnorm call has
+// no plan to keep it in.
+gemm_status current_gfx950(int *cu_count) {
+  constexpr int kMost = 64;
+  static int cus[kMost];  // 0: not read yet; -1: another part. Every writer writes the same value.
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return GEMM_E_HIP;
+  if (dev < 0 || dev >= kMost) return GEMM_E_DEVICE;
+  int c = __atomic_load_n(&cus[dev], __ATOMIC_RELAXED);
+  if (c == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_E_HIP;
+    c = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? prop.multiProcessorCount : -1;
+    __atomic_store_n(&cus[dev], c, __ATOMIC_RELAXED);
+  }
+  if (c < 0) return GEMM_E_UNSUPPORTED;
+  *cu_count = c;
+  return GEMM_OK;
+}
+
+gemm_status check_device(layer_plan *p) {
+  int dev = -1;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(p, e, "hipGetDevice");
+  return dev == p->device ? GEMM_OK : GEMM_E_DEVICE;
+}
+
+// The plan's scratch serves one call at a time: a call on another stream than
+// the last one first waits, on the device, for what that stream holds so far.
+gemm_status order_after_last_stream(layer_plan *p, hipStream_t s) {
+  if (p->has_run && s != p->last_stream) {
+    hipError_t e = hipEventRecord(p->stream_switch, p->last_stream);
+    if (e != hipSuccess) return hip_fail(p, e, "hipEventRecord(stream switch)");
+    e = hipStreamWaitEvent(s, p->stream_switch, 0);
+    if (e != hipSuccess) return hip_fail(p, e, "hipStreamWaitEvent(stream switch)");
+  }
+  p->last_stream = s;
+  p->has_run = true;
+  return GEMM_OK;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool stream_type(int32_t t) { return t == LAYER_F32 || t == LAYER_BF16; }
+
+// Sizes of an m x n matrix whose rows are multiples of `step` elements.
+bool bad_size(int64_t m, int64_t n, int64_t step) {
+  return m < 0 || n < 0 || m > LAYER_MAX_ROWS || n > LAYER_MAX_COLS || n % step != 0;
+}
+// A row stride of a matrix with m rows of n elements (not looked at with one row, or rows of no elements).
+bool bad_stride(int64_t ld, int64_t m, int64_t n, int64_t step) {
+  return m > 1 && n > 0 && (ld < n || ld > LAYER_MAX_COLS || ld % step != 0);
+}
+
+// Partial sums of n columns over at most `wanted` rows: as many rows as the workspace holds.
+int64_t partial_rows(int64_t wanted, int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(wanted, kWsFloats / std::max<int64_t>(n, 1))); }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status layer_create(layer_cfg *out, int32_t device) {
+  if (!out) return GEMM_E_INVALID_ARG;
+  *out = nullptr;
+  int ndev = 0, cur = -1;
+  if (hipGetDeviceCount(&ndev) != hipSuccess) return GEMM_E_HIP;
+  if (device < 0 || device >= ndev) return GEMM_E_INVALID_ARG;
+  if (hipGetDevice(&cur) != hipSuccess) return GEMM_E_HIP;
+  if (cur != device) return GEMM_E_DEVICE;
+  int cus = 0;
+  gemm_status st = current_gfx950(&cus);
+  if (st != GEMM_OK) return st;
+  layer_plan *p = new (std::nothrow) layer_plan();
+  if (!p) return GEMM_E_NOMEM;
+  p->device = device;
+  p->cu_count = cus;
+  if (hipMalloc(&p->d_ws, sizeof(float) * (size_t)kWsFloats) != hipSuccess) {
+    p->d_ws = nullptr;
+    layer_destroy(p);
+    return GEMM_E_NOMEM;
+  }
+  if (hipEventCreateWithFlags(&p->stream_switch, hipEventDisableTiming) != hipSuccess) {
+    p->stream_switch = nullptr;
+    layer_destroy(p);
+    return GEMM_E_HIP;
+  }
+  *out = p;
+  return GEMM_OK;
+}
+
+gemm_status layer_destroy(layer_cfg p) {
+  if (!p) return GEMM_OK;
+  if (p->has_run) (void)hipStreamSynchronize(p->last_stream);
+  if (p->stream_switch) (void)hipEventDestroy(p->stream_switch);
+  if (p->d_ws) (void)hipFree(p->d_ws);
+  delete p;
+  return GEMM_OK;
+}
+
+gemm_status layer_sync(layer_cfg p) {
+  if (!p) return GEMM_E_INVALID_ARG;
+  if (!p->has_run) return GEMM_OK;
+  hipError_t e = hipStreamSynchronize(p->last_stream);
+  return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "hipStreamSynchronize");
+}
+
+const char *layer_last_hip_error(layer_cfg p) { return p ? p->last_error.c_str() : ""; }
+
+gemm_status layer_rmsnorm(const layer_rmsnorm_args *a, void *stream) {
+  if (!a) return GEMM_E_INVALID_ARG;
+  if (!stream_type(a->type) || (a->out_type != LAYER_E4M3 && !stream_type(a->out_type)) ||
+      (a->weight && !stream_type(a->weight_type)) || !(a->eps >= 0.0f))
+    return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || a->n > LAYER_MAX_NORM_COLS || bad_stride(a->ldx, a->m, a->n, 8) ||
+      (a->residual && bad_stride(a->ldr, a->m, a->n, 8)) || (a->sum_out && bad_stride(a->lds, a->m, a->n, 8)) ||
+      bad_stride(a->ldo, a->m, a->n, 8))
+    return GEMM_E_SHAPE;
+  if ((a->out_type == LAYER_E4M3) != (a->scale != nullptr) && (a->m > 0 || a->scale)) return GEMM_E_INVALID_ARG;
+  if (a->m == 0 || a->n == 0) return GEMM_OK;
+  if (!a->x || !a->out || !aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->sum_out) ||
+      !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->scale) & 3u))
+    return GEMM_E_INVALID_ARG;
+  int cus = 0;
+  gemm_status st = current_gfx950(&cus);
+  if (st != GEMM_OK) return st;
+  ptg::NormArgs k;
+  std::memset(&k, 0, sizeof(k));
+  k.x = a->x;
+  k.residual = a->residual;
+  k.weight = a->weight;
+  k.sum_out = a->sum_out;
+  k.out = a->out;
+  k.scale = a->scale;
+  k.ldx = a->ldx;
+  k.ldr = a->ldr;
+  k.lds = a->lds;
+  k.ldo = a->ldo;
+  k.m = (int32_t)a->m;
+  k.n = (int32_t)a->n;
+  k.type = a->type;
+  k.weight_type = a->weight_type;
+  k.out_type = a->out_type;
+  k.eps = a->eps;
+  return ptg::launch_rmsnorm(k, cus, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_OK : GEMM_E_HIP;
+}
+
+gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  if (!stream_type(a->type) || !stream_type(a->dy_type) || (a->weight && !stream_type(a->weight_type)) || !(a->eps >= 0.0f) ||
+      a->accumulate < 0 || a->accumulate > 1)
+    return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || a->n > LAYER_MAX_NORM_COLS || bad_stride(a->lddy, a->m, a->n, 8) ||
+      bad_stride(a->lds, a->m, a->n, 8) || (a->dsum && bad_stride(a->lddsum, a->m, a->n, 8)) ||
+      (a->dx && bad_stride(a->lddx, a->m, a->n, 8)))
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->dy) || !aligned16(a->s) || !aligned16(a->weight) || !aligned16(a->dsum) || !aligned16(a->dx) ||
+      !aligned16(a->dweight) || (a->m > 0 && a->n > 0 && (!a->dy || !a->s)))
+    return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK) return st;
+  if (a->n == 0 || (!a->dx && !a->dweight) || (a->m == 0 && (!a->dweight || a->accumulate))) return GEMM_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  int rows = 0;
+  hipError_t e;
+  if (a->m > 0) {
+    ptg::NormGradArgs k;
+    std::memset(&k, 0, sizeof(k));
+    k.dy = a->dy;
+    k.s = a->s;
+    k.weight = a->weight;
+    k.dsum = a->dsum;
+    k.dx = a->dx;
+    k.partial = a->dweight ? p->d_ws : nullptr;
+    k.lddy = a->lddy;
+    k.lds = a->lds;
+    k.lddsum = a->lddsum;
+    k.lddx = a->lddx;
+    k.m = (int32_t)a->m;
+    k.n = (int32_t)a->n;
+    k.type = a->type;
+    k.dy_type = a->dy_type;
+    k.weight_type = a->weight_type;
+    k.eps = a->eps;
+    // at most 8 x CUs groups of rows of at most 2048, or 2 x CUs of 8192, or CUs
+    // of 32768 elements: within the workspace
+    rows = ptg::rmsnorm_partial_rows(k.m, k.n, p->cu_count);
+    if ((int64_t)rows * a->n > kWsFloats) return GEMM_E_SHAPE;
+    e = ptg::launch_rmsnorm_backward(k, p->cu_count, s);
+    if (e != hipSuccess) return hip_fail(p, e, "rmsnorm backward");
+  }
+  if (a->dweight) {
+    e = ptg::launch_column_sum(p->d_ws, rows, (int32_t)a->n, a->dweight, a->accumulate, s);
+    if (e != hipSuccess) return hip_fail(p, e, "column sum");
+  }
+  return GEMM_OK;
+}
+
+gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  const bool e8 = a->in_type == LAYER_E4M3;
+  if ((!e8 && a->in_type != LAYER_BF16) || (a->bias && !stream_type(a->bias_type)) ||
+      (a->residual && !stream_type(a->residual_type)) || !stream_type(a->out_type) || a->activation < LAYER_ACT_NONE ||
+      a->activation > LAYER_ACT_SILU || (!e8 && (a->x_scale || a->w_scale)))
+    return GEMM_E_INVALID_ARG;
+  const int64_t step = e8 ? 16 : 8;
+  if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, step) || a->n > LAYER_MAX_COLS || bad_stride(a->ldx, a->m, a->k, step) ||
+      bad_stride(a->ldw, a->n, a->k, step) || bad_stride(a->ldo, a->m, a->n, 8) ||
+      (a->residual && bad_stride(a->ldr, a->m, a->n, 8)) || (a->pre && bad_stride(a->ldp, a->m, a->n, 8)))
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->x_scale) || !aligned16(a->w_scale) || !aligned16(a->bias) ||
+      !aligned16(a->residual) || !aligned16(a->pre) || !aligned16(a->out))
+    return GEMM_E_INVALID_ARG;
+  const bool empty = a->m == 0 || a->n == 0;
+  if (!empty && (!a->out || (a->k > 0 && (!a->x || !a->w)))) return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK || empty) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  ptg::ProductArgs k;
+  std::memset(&k, 0, sizeof(k));
+  k.a = a->x;
+  k.b = a->w;
+  k.lda = a->ldx;
+  k.ldb = a->ldw;
+  k.m = (int32_t)a->m;
+  k.n = (int32_t)a->n;
+  k.k = (int32_t)a->k;
+  k.ep.row_scale = a->x_scale;
+  k.ep.col_scale = a->w_scale;
+  k.ep.bias = a->bias;
+  k.ep.residual = a->residual;
+  k.ep.pre = a->pre;
+  k.ep.out = a->out;
+  k.ep.ldr = a->ldr;
+  k.ep.ldp = a->ldp;
+  k.ep.ldo = a->ldo;
+  k.ep.bias_type = a->bias_type;
+  k.ep.residual_type = a->residual_type;
+  k.ep.out_type = a->out_type;
+  k.ep.act = a->activation;
+  hipError_t e = ptg::launch_product_simple(k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
+  return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
+}
+
+gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  if (a->activation < LAYER_ACT_NONE || a->activation > LAYER_ACT_SILU || a->accumulate < 0 || a->accumulate > 1)
+    return GEMM_E_INVALID_ARG;
+  const bool none = a->activation == LAYER_ACT_NONE;
+  if (bad_size(a->m, a->n, 8) || bad_stride(a->lddo, a->m, a->n, 8) || (!none && a->pre && bad_stride(a->ldp, a->m, a->n, 8)) ||
+      (a->dpre && bad_stride(a->lddp, a->m, a->n, 8)))
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->dout) || (!none && !aligned16(a->pre)) || !aligned16(a->dpre) || !aligned16(a->dbias) ||
+      (a->m > 0 && a->n > 0 && (!a->dout || (!none && !a->pre))))
+    return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK) return st;
+  if (a->n == 0 || (!a->dpre && !a->dbias) || (a->m == 0 && (!a->dbias || a->accumulate))) return GEMM_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  int64_t groups = 0;
+  hipError_t e;
+  if (a->m > 0) {
+    ptg::ActGradArgs k;
+    std::memset(&k, 0, sizeof(k));
+    k.dout = a->dout;
+    k.pre = a->pre;
+    k.dpre = a->dpre;
+    k.partial = a->dbias ? p->d_ws : nullptr;
+    k.lddo = a->lddo;
+    k.ldp = a->ldp;
+    k.lddp = a->lddp;
+    k.m = (int32_t)a->m;
+    k.n = (int32_t)a->n;
+    k.act = a->activation;
+    // eight workgroups a CU, each with 16 rows at least (four a wave)
+    const int64_t strips = ceil_div(a->n, 512);
+    groups = partial_rows(std::min<int64_t>(ceil_div((int64_t)p->cu_count * 8, strips), ceil_div(a->m, 16)), a->n);
+    k.rows_per_group = (int32_t)ceil_div(a->m, groups);
+    groups = ceil_div(a->m, k.rows_per_group);
+    e = ptg::launch_activation_backward(k, (int)groups, s);
+    if (e != hipSuccess) return hip_fail(p, e, "activation backward");
+  }
+  if (a->dbias) {
+    e = ptg::launch_column_sum(p->d_ws, (int)groups, (int32_t)a->n, a->dbias, a->accumulate, s);
+    if (e != hipSuccess) return hip_fail(p, e, "column sum");
+  }
+  return GEMM_OK;
+}
+
+gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  if ((a->dx && !stream_type(a->dx_type)) || (a->dw && !stream_type(a->dw_type)) || a->accumulate < 0 || a->accumulate > 1)
+    return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || bad_size(a->m, a->k, 8) || bad_stride(a->lddp, a->m, a->n, 8) ||
+      (a->dw && bad_stride(a->ldx, a->m, a->k, 8)) || (a->dx && bad_stride(a->ldw, a->n, a->k, 8)) ||
+      (a->dx && bad_stride(a->lddx, a->m, a->k, 8)) || (a->dw && bad_stride(a->lddw, a->n, a->k, 8)))
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->dpre) || (a->dw && !aligned16(a->x)) || (a->dx && !aligned16(a->w)) || !aligned16(a->dx) || !aligned16(a->dw))
+    return GEMM_E_INVALID_ARG;
+  const bool any_dx = a->dx && a->m > 0 && a->k > 0;
+  const bool any_dw = a->dw && a->n > 0 && a->k > 0 && !(a->m == 0 && a->accumulate);
+  if ((any_dx && a->n > 0 && (!a->dpre || !a->w)) || (any_dw && a->m > 0 && (!a->dpre || !a->x))) return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK || (!any_dx && !any_dw)) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  ptg::ProductArgs k;
+  if (any_dx) {
+    std::memset(&k, 0, sizeof(k));
+    k.a = a->dpre;
+    k.b = a->w;
+    k.lda = a->lddp;
+    k.ldb = a->ldw;
+    k.m = (int32_t)a->m;
+    k.n = (int32_t)a->k;
+    k.k = (int32_t)a->n;
+    k.ep.out = a->dx;
+    k.ep.ldo = a->lddx;
+    k.ep.out_type = a->dx_type;
+    hipError_t e = ptg::launch_product_simple(k, ptg::kFormNN, s);
+    if (e != hipSuccess) return hip_fail(p, e, "linear backward, dx");
+  }
+  if (any_dw) {
+    std::memset(&k, 0, sizeof(k));
+    k.a = a->dpre;
+    k.b = a->x;
+    k.lda = a->lddp;
+    k.ldb = a->ldx;
+    k.m = (int32_t)a->n;
+    k.n = (int32_t)a->k;
+    k.k = (int32_t)a->m;
+    k.ep.out = a->dw;
+    k.ep.ldo = a->lddw;
+    k.ep.out_type = a->dw_type;
+    k.ep.residual = a->accumulate ? a->dw : nullptr;
+    k.ep.ldr = a->lddw;
+    k.ep.residual_type = a->dw_type;
+    hipError_t e = ptg::launch_product_simple(k, ptg::kFormTN, s);
+    if (e != hipSuccess) return hip_fail(p, e, "linear backward, dw");
+  }
+  return GEMM_OK;
+}
+
+}  // extern "C"

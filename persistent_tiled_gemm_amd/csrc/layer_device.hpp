@@ -1,0 +1,112 @@
+// Device-side pieces shared by the layer operators' kernels: 8-element loads
+// and stores of the stream types, activations and their derivatives, and the
+// shapes the host and the kernels agree on.
+#pragma once
+
+#include "ptg_device.hpp"
+#include "layer_internal.hpp"
+
+namespace ptg {
+
+typedef __attribute__((ext_vector_type(8))) float f32x8;
+
+// Eight consecutive elements as fp32. Rows are 16-byte aligned (8-byte for e4m3).
+template <typename T> __device__ __forceinline__ f32x8 load8(const T *p);
+template <> __device__ __forceinline__ f32x8 load8<float>(const float *p) {
+  const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <> __device__ __forceinline__ f32x8 load8<__bf16>(const __bf16 *p) {
+  return __builtin_convertvector(*(const bf16x8 *)p, f32x8);
+}
+// The element type named at run time (the weight's or a bias's: read once a row or column).
+__device__ __forceinline__ f32x8 load8_as(const void *p, int32_t type, int64_t i) {
+  return type == kTypeF32 ? load8((const float *)p + i) : load8((const __bf16 *)p + i);
+}
+
+// Rounded to nearest even, once, from the fp32 result.
+template <typename T> __device__ __forceinline__ void store8(T *p, const f32x8 &v);
+template <> __device__ __forceinline__ void store8<float>(float *p, const f32x8 &v) {
+  *(f32x4 *)p = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+  *(f32x4 *)(p + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+}
+template <> __device__ __forceinline__ void store8<__bf16>(__bf16 *p, const f32x8 &v) {
+  *(bf16x8 *)p = __builtin_convertvector(v, bf16x8);
+}
+static constexpr float kE4m3Max = 448.0f;  // the largest e4m3 value
+struct e4m3_t { uint8_t bits; };
+template <> __device__ __forceinline__ void store8<e4m3_t>(e4m3_t *p, const f32x8 &v) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  *(int2 *)p = make_int2(lo, hi);
+}
+
+// exp through the hardware's 2^x: relative error about 2^-22 over the range the
+// activations use it on (the argument's own rounding, |t| 2^-24, dominates).
+__device__ __forceinline__ float exp_f32(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504088896341f); }
+
+// Activations in fp32. The logistic function is 1 / (1 + e^-t): e^-t that
+// overflows to infinity gives 0, and the products with z below are then 0 z; for
+// z = -inf that is NaN where the limit is 0, so the result is selected, not
+// multiplied, there.
+__device__ __forceinline__ float logistic(float t) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-t)); }
+
+static constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
+static constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float act_f32(int32_t act, float z) {
+  switch (act) {
+    case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
+    case kActGelu: return z == -INFINITY ? 0.0f : 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case kActGeluTanh: {
+      // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+      const float p = logistic(2.0f * kGeluC * (z + kGeluA * z * z * z));
+      return p == 0.0f ? 0.0f : z * p;
+    }
+    case kActSilu: {
+      const float p = logistic(z);
+      return p == 0.0f ? 0.0f : z * p;
+    }
+    default: return z;
+  }
+}
+
+// d act / dz. The terms z f'(z) vanish faster than z grows; where the factor
+// has underflowed to 0 the term is 0 (selected, so that infinite z gives no NaN).
+__device__ __forceinline__ float act_grad_f32(int32_t act, float z) {
+  switch (act) {
+    case kActRelu: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+    case kActGelu: {
+      const float pdf = 0.39894228040143268f * exp_f32(-0.5f * z * z);
+      return 0.5f * erfcf(z * -0.70710678118654752f) + (pdf == 0.0f ? 0.0f : z * pdf);
+    }
+    case kActGeluTanh: {
+      const float p = logistic(2.0f * kGeluC * (z + kGeluA * z * z * z));
+      const float q = p * (1.0f - p);
+      return p + (q == 0.0f ? 0.0f : 2.0f * kGeluC * z * (1.0f + 3.0f * kGeluA * z * z) * q);
+    }
+    case kActSilu: {
+      const float p = logistic(z);
+      const float q = p * (1.0f - p);
+      return p + (q == 0.0f ? 0.0f : z * q);
+    }
+    default: return 1.0f;
+  }
+}
+
+// Sum (or, for bit patterns, unsigned maximum) over the 64 lanes, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+  return v;
+}
+
+}  // namespace ptg

@@ -1,0 +1,79 @@
+// Types shared by the layer operators' host code and kernels (not part of the
+// C ABI; the numbers equal the ABI's LAYER_* constants).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ptg {
+
+enum LayerType { kTypeF32 = 0, kTypeBf16 = 1, kTypeE4m3 = 2 };
+enum LayerAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+struct NormArgs {
+  const void *x, *residual, *weight;
+  void *sum_out, *out;
+  float *scale;
+  int64_t ldx, ldr, lds, ldo;
+  int32_t m, n;
+  int32_t type, weight_type, out_type;
+  float eps;
+};
+
+struct NormGradArgs {
+  const void *dy, *s, *weight, *dsum;
+  void *dx;
+  float *partial;  // [partial rows][n] sums of dweight, or NULL
+  int64_t lddy, lds, lddsum, lddx;
+  int32_t m, n;
+  int32_t type, dy_type, weight_type;
+  float eps;
+};
+
+struct ActGradArgs {
+  const void *dout, *pre;
+  void *dpre;
+  float *partial;  // [row groups][n] sums of dbias, or NULL
+  int64_t lddo, ldp, lddp;
+  int32_t m, n;
+  int32_t act;
+  int32_t rows_per_group;
+};
+
+// What a product's epilogue does with z = sum_k a b: out = act(z scales + bias) + residual.
+struct EpilogueArgs {
+  const float *row_scale, *col_scale;
+  const void *bias, *residual;
+  void *pre, *out;
+  int64_t ldr, ldp, ldo;
+  int32_t bias_type, residual_type, out_type;
+  int32_t act;
+};
+
+// The operands of a product out[m][n] = sum_k A(m, k) B(n, k), each with the
+// contracted index along its rows ("k-contiguous") or down its columns.
+struct ProductArgs {
+  const void *a, *b;
+  int64_t lda, ldb;
+  int32_t m, n, k;
+  EpilogueArgs ep;
+};
+
+// Forms of a product, by operand layout and type.
+enum ProductForm {
+  kFormNT = 0,     // A m x k, B n x k, bf16: a linear layer
+  kFormNN = 1,     // A m x k, B k x n, bf16: the gradient of x
+  kFormTN = 2,     // A k x m, B k x n, bf16: the gradient of w
+  kFormNTE4m3 = 3  // A m x k, B n x k, e4m3
+};
+
+hipError_t launch_rmsnorm(const NormArgs &a, int cu_count, hipStream_t s);
+// Rows of the partial sums that launch_rmsnorm_backward writes for m x n.
+int rmsnorm_partial_rows(int32_t m, int32_t n, int cu_count);
+hipError_t launch_rmsnorm_backward(const NormGradArgs &a, int cu_count, hipStream_t s);
+// out[j] = sum over `rows` of partial[row][j] (+ out[j] with accumulate), in row order.
+hipError_t launch_column_sum(const float *partial, int rows, int32_t n, float *out, int accumulate, hipStream_t s);
+hipError_t launch_activation_backward(const ActGradArgs &a, int row_groups, hipStream_t s);
+hipError_t launch_product_simple(const ProductArgs &a, int form, hipStream_t s);
+
+}  // namespace ptg

@@ -1,0 +1,276 @@
+"""Python binding of the layer operators' C ABI (include/ptg_layer.h): the RMS norm with the residual's
+addition, the product with bias, activation and residual in its epilogue, and their gradients.
+
+Argument marshalling only, like the GEMM's binding. The function names are the C ABI's: layer_create,
+layer_destroy, layer_sync, layer_last_hip_error, layer_rmsnorm, layer_rmsnorm_backward, layer_linear,
+layer_activation_backward, layer_linear_backward. Matrices are 2-D device tensors whose rows are dense; the row
+stride is free (a column slice of a wider buffer works). Streams are torch.cuda streams (default: the current
+stream). Outputs are given by the caller.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+from . import GEMM_OK, PtgError, _stream_ptr, load_library
+
+LAYER_F32, LAYER_BF16, LAYER_E4M3 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+# exported names, in the order of the header
+LAYER_ABI_FUNCTIONS = ("layer_create", "layer_destroy", "layer_sync", "layer_last_hip_error", "layer_rmsnorm",
+                       "layer_rmsnorm_backward", "layer_linear", "layer_activation_backward", "layer_linear_backward")
+
+
+def _struct(pointers, sizes, ints, floats=()):
+    return ([(n, ctypes.c_void_p) for n in pointers] + [(n, ctypes.c_int64) for n in sizes] +
+            [(n, ctypes.c_int32) for n in ints] + [(n, ctypes.c_float) for n in floats])
+
+
+class RmsnormArgs(ctypes.Structure):
+    _fields_ = _struct(("x", "residual", "weight", "sum_out", "out", "scale"), ("m", "n", "ldx", "ldr", "lds", "ldo"),
+                       ("type", "weight_type", "out_type"), ("eps",))
+
+
+class RmsnormGradArgs(ctypes.Structure):
+    _fields_ = _struct(("dy", "s", "weight", "dsum", "dx", "dweight"), ("m", "n", "lddy", "lds", "lddsum", "lddx"),
+                       ("type", "dy_type", "weight_type", "accumulate"), ("eps",))
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = _struct(("x", "w", "x_scale", "w_scale", "bias", "residual", "pre", "out"),
+                       ("m", "n", "k", "ldx", "ldw", "ldr", "ldp", "ldo"),
+                       ("in_type", "bias_type", "residual_type", "out_type", "activation", "pad"))
+
+
+class ActivationGradArgs(ctypes.Structure):
+    _fields_ = _struct(("dout", "pre", "dpre", "dbias"), ("m", "n", "lddo", "ldp", "lddp"), ("activation", "accumulate"))
+
+
+class LinearGradArgs(ctypes.Structure):
+    _fields_ = _struct(("dpre", "x", "w", "dx", "dw"), ("m", "n", "k", "lddp", "ldx", "ldw", "lddx", "lddw"),
+                       ("dx_type", "dw_type", "accumulate", "pad"))
+
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        vp = ctypes.c_void_p
+        lib.layer_create.argtypes = [ctypes.POINTER(vp), ctypes.c_int32]
+        lib.layer_destroy.argtypes = [vp]
+        lib.layer_sync.argtypes = [vp]
+        lib.layer_last_hip_error.argtypes = [vp]
+        lib.layer_last_hip_error.restype = ctypes.c_char_p
+        lib.layer_rmsnorm.argtypes = [ctypes.POINTER(RmsnormArgs), vp]
+        lib.layer_rmsnorm_backward.argtypes = [ctypes.POINTER(RmsnormGradArgs), vp, vp]
+        lib.layer_linear.argtypes = [ctypes.POINTER(LinearArgs), vp, vp]
+        lib.layer_activation_backward.argtypes = [ctypes.POINTER(ActivationGradArgs), vp, vp]
+        lib.layer_linear_backward.argtypes = [ctypes.POINTER(LinearGradArgs), vp, vp]
+        _lib = lib
+    return _lib
+
+
+def _check(status: int, what: str, plan=None) -> None:
+    if status != GEMM_OK:
+        lib = _library()
+        detail = (lib.layer_last_hip_error(plan.handle) or b"").decode() if plan is not None and plan.handle else ""
+        raise PtgError(status, what, detail or (lib.gemm_status_str(status) or b"").decode())
+
+
+class LayerPlan:
+    """A layer_cfg handle (owns the operators' scratch)."""
+
+    def __init__(self, device: int = 0):
+        self.handle = ctypes.c_void_p()
+        self.device = int(device)
+        _check(_library().layer_create(ctypes.byref(self.handle), self.device), "layer_create")
+
+    def destroy(self) -> None:
+        if self.handle:
+            _library().layer_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.destroy()
+
+
+def layer_create(device: int = 0) -> LayerPlan:
+    """layer_create: a plan on `device` (the current device)."""
+    return LayerPlan(device)
+
+
+def layer_destroy(plan: LayerPlan) -> None:
+    plan.destroy()
+
+
+def layer_sync(plan: LayerPlan, strict: bool = True) -> int:
+    """layer_sync: wait for the plan's last stream and return (strict=False) or raise on (strict=True) the
+    device status of its products."""
+    st = int(_library().layer_sync(plan.handle))
+    if strict:
+        _check(st, "layer_sync", plan)
+    return st
+
+
+def layer_last_hip_error(plan: LayerPlan) -> str:
+    return (_library().layer_last_hip_error(plan.handle) or b"").decode()
+
+
+def _types():
+    import torch
+    return {torch.float32: LAYER_F32, torch.bfloat16: LAYER_BF16, torch.float8_e4m3fn: LAYER_E4M3}
+
+
+def _type(name, t, allowed):
+    code = _types().get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    return code
+
+
+def _place(name, t, like):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _matrix(name, t, rows, cols, like, allowed):
+    """(pointer, row stride, type code) of an optional rows x cols matrix with dense rows."""
+    if t is None:
+        return None, 0, LAYER_F32
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    _place(name, t, like)
+    code = _type(name, t, allowed)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows (stride 1 along its columns)")
+    return t.data_ptr(), int(t.stride(0)) if rows > 1 else int(cols), code
+
+
+def _vector(name, t, n, like, allowed):
+    """(pointer, type code) of an optional dense vector of n elements."""
+    if t is None:
+        return None, LAYER_F32
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
+    _place(name, t, like)
+    code = _type(name, t, allowed)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), code
+
+
+def _two_d(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+_STREAM = (LAYER_F32, LAYER_BF16)
+
+
+def layer_rmsnorm(x, weight, out, *, residual=None, sum_out=None, scale=None, eps: float = 1e-6, stream=None) -> None:
+    """layer_rmsnorm: out = s / sqrt(mean(s^2) + eps) * weight per row, s = x + residual (kept in sum_out, which
+    may be x or residual). x, residual, sum_out: one dtype, bf16 or fp32. weight: bf16 or fp32, or None. out: fp32,
+    bf16, or float8_e4m3fn with `scale` (fp32, one value a row): s's norm is then about out * scale[:, None]."""
+    m, n = _two_d("x", x)
+    a = RmsnormArgs(m=m, n=n, eps=eps)
+    _place("x", x, x)
+    a.x, a.ldx, a.type = _matrix("x", x, m, n, x, _STREAM)
+    a.residual, a.ldr, _ = _matrix("residual", residual, m, n, x, (a.type,))
+    a.sum_out, a.lds, _ = _matrix("sum_out", sum_out, m, n, x, (a.type,))
+    a.weight, a.weight_type = _vector("weight", weight, n, x, _STREAM)
+    a.out, a.ldo, a.out_type = _matrix("out", out, m, n, x, (LAYER_F32, LAYER_BF16, LAYER_E4M3))
+    a.scale, _ = _vector("scale", scale, m, x, (LAYER_F32,))
+    _check(_library().layer_rmsnorm(ctypes.byref(a), ctypes.c_void_p(_stream_ptr(stream))), "layer_rmsnorm")
+
+
+def layer_rmsnorm_backward(dy, s, weight, dx, dweight, plan: LayerPlan, *, dsum=None, accumulate: bool = False,
+                           eps: float = 1e-6, stream=None) -> None:
+    """layer_rmsnorm_backward: dx (of the sum s, so of x and of the residual) and dweight (fp32) from dy, at s.
+    dsum: the gradient that reaches s from elsewhere, added to dx (dx may be dsum). dx or dweight may be None."""
+    m, n = _two_d("s", s)
+    a = RmsnormGradArgs(m=m, n=n, eps=eps, accumulate=int(bool(accumulate)))
+    a.s, a.lds, a.type = _matrix("s", s, m, n, s, _STREAM)
+    a.dy, a.lddy, a.dy_type = _matrix("dy", dy, m, n, s, _STREAM)
+    a.weight, a.weight_type = _vector("weight", weight, n, s, _STREAM)
+    a.dsum, a.lddsum, _ = _matrix("dsum", dsum, m, n, s, (a.type,))
+    a.dx, a.lddx, _ = _matrix("dx", dx, m, n, s, (a.type,))
+    a.dweight, _ = _vector("dweight", dweight, n, s, (LAYER_F32,))
+    _check(_library().layer_rmsnorm_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
+           "layer_rmsnorm_backward", plan)
+
+
+def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "none", residual=None, pre=None, x_scale=None,
+                 w_scale=None, stream=None) -> None:
+    """layer_linear: out = act(x . w^T + bias) + residual, x: m x k, w: n x k, both bf16 or both float8_e4m3fn (then
+    with row scales x_scale and w_scale, fp32). out and residual: bf16 or fp32; residual may be out. pre (bf16)
+    keeps the activation's argument for layer_activation_backward."""
+    m, k = _two_d("x", x)
+    n, k2 = _two_d("w", w)
+    if k2 != k:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    a = LinearArgs(m=m, n=n, k=k, activation=_activation(activation))
+    a.x, a.ldx, a.in_type = _matrix("x", x, m, k, x, (LAYER_BF16, LAYER_E4M3))
+    a.w, a.ldw, _ = _matrix("w", w, n, k, x, (a.in_type,))
+    a.x_scale, _ = _vector("x_scale", x_scale, m, x, (LAYER_F32,))
+    a.w_scale, _ = _vector("w_scale", w_scale, n, x, (LAYER_F32,))
+    a.bias, a.bias_type = _vector("bias", bias, n, x, _STREAM)
+    a.residual, a.ldr, a.residual_type = _matrix("residual", residual, m, n, x, _STREAM)
+    a.pre, a.ldp, _ = _matrix("pre", pre, m, n, x, (LAYER_BF16,))
+    a.out, a.ldo, a.out_type = _matrix("out", out, m, n, x, _STREAM)
+    _check(_library().layer_linear(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))), "layer_linear", plan)
+
+
+def layer_activation_backward(dout, pre, dpre, plan: LayerPlan, *, activation: str = "none", dbias=None,
+                              accumulate: bool = False, stream=None) -> None:
+    """layer_activation_backward: dpre = dout * act'(pre) (bf16; dpre may be dout or pre, or None) and dbias = its
+    column sums before rounding (fp32, or None). pre may be None with activation "none"."""
+    m, n = _two_d("dout", dout)
+    a = ActivationGradArgs(m=m, n=n, activation=_activation(activation), accumulate=int(bool(accumulate)))
+    a.dout, a.lddo, _ = _matrix("dout", dout, m, n, dout, (LAYER_BF16,))
+    a.pre, a.ldp, _ = _matrix("pre", pre, m, n, dout, (LAYER_BF16,))
+    a.dpre, a.lddp, _ = _matrix("dpre", dpre, m, n, dout, (LAYER_BF16,))
+    a.dbias, _ = _vector("dbias", dbias, n, dout, (LAYER_F32,))
+    _check(_library().layer_activation_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
+           "layer_activation_backward", plan)
+
+
+def layer_linear_backward(dpre, x, w, plan: LayerPlan, *, dx=None, dw=None, accumulate: bool = False, stream=None) -> None:
+    """layer_linear_backward: dx = dpre . w (m x k) and dw = dpre^T . x (n x k; added to dw with accumulate), each
+    bf16 or fp32 and optional. dpre, x, w: bf16; x may be None without dw, w may be None without dx."""
+    m, n = _two_d("dpre", dpre)
+    given = w if w is not None else x if x is not None else dx if dx is not None else dw
+    if given is None:
+        raise ValueError("layer_linear_backward needs x for dw and w for dx")
+    k = _two_d("x or w", given)[1]
+    if (dx is not None and w is None) or (dw is not None and x is None):
+        raise ValueError("layer_linear_backward needs x for dw and w for dx")
+    a = LinearGradArgs(m=m, n=n, k=k, accumulate=int(bool(accumulate)))
+    a.dpre, a.lddp, _ = _matrix("dpre", dpre, m, n, dpre, (LAYER_BF16,))
+    a.x, a.ldx, _ = _matrix("x", x, m, k, dpre, (LAYER_BF16,))
+    a.w, a.ldw, _ = _matrix("w", w, n, k, dpre, (LAYER_BF16,))
+    a.dx, a.lddx, a.dx_type = _matrix("dx", dx, m, k, dpre, _STREAM)
+    a.dw, a.lddw, a.dw_type = _matrix("dw", dw, n, k, dpre, _STREAM)
+    _check(_library().layer_linear_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
+           "layer_linear_backward", plan)
