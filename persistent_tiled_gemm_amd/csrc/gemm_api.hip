@@ -15,6 +15,7 @@
 #include <thread>
 #include <vector>
 
+#include "layer_internal.hpp"
 #include "ptg_gemm.h"
 #include "ptg_internal.hpp"
 
@@ -248,8 +249,9 @@ void plan_units(const gemm_plan *p, bool grouped, int32_t mode, int64_t tiles, i
   *items = tiles - r + r * S;
 }
 
+// product, form: a layer operator's product instead of the plain GEMM (dynamic mode, one problem).
 gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, int64_t tiles, int64_t K,
-                   hipStream_t s) {
+                   hipStream_t s, const ptg::ProductOpArgs *product = nullptr, int form = 0) {
   if (mode < GEMM_SCHED_NONPERSISTENT || mode > GEMM_SCHED_DYNAMIC) return GEMM_E_INVALID_ARG;
   int64_t items = tiles, split_base = tiles;
   int32_t chunks = 1, group = 1;
@@ -315,7 +317,8 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
     args.self_clean = 0;
   }
   args.log = p->d_log;
-  e = ptg::launch_gemm(p->desc.bm, mode, grouped, p->desc.b_layout == 1, args, (int)grid, p->dyn_lds, s);
+  e = product ? ptg::launch_product(p->desc.bm, form, args, *product, (int)grid, s)
+              : ptg::launch_gemm(p->desc.bm, mode, grouped, p->desc.b_layout == 1, args, (int)grid, p->dyn_lds, s);
   if (e != hipSuccess) return hip_fail(p, e, "kernel launch");
   if (!captured) ++p->runs;
   p->last_set = cur;
@@ -390,6 +393,35 @@ gemm_status noalloc_setup(int dev, hipStream_t s, NoallocDevice **out) {
 }
 
 }  // namespace
+
+namespace ptg {
+
+gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, hipStream_t s) {
+  const int64_t units = form == kFormNTE4m3 ? 2 : 1;  // values per 16-bit unit along k
+  const int64_t K = a.k / units;
+  const int64_t tm = ceil_div(a.m, p->desc.bm), tn = ceil_div(a.n, p->desc.bn);
+  if (tm * tn > GEMM_MAX_TILES) return GEMM_E_SHAPE;
+  KernelArgs args;
+  std::memset(&args, 0, sizeof(args));
+  args.single.A = static_cast<const uint16_t *>(a.a);
+  args.single.B = static_cast<const uint16_t *>(a.b);
+  args.single.M = a.m;
+  args.single.N = a.n;
+  args.single.K = (int32_t)K;
+  args.single.tiles_m = (int32_t)tm;
+  args.single.tiles_n = (int32_t)tn;
+  args.G = 1;
+  ProductOpArgs op;
+  op.ep = a.ep;
+  op.lda = (int32_t)(a.lda / units);
+  op.ldb = (int32_t)(a.ldb / units);
+  p->last_tile_start.assign(1, 0);
+  p->last_k.assign(1, (int32_t)K);
+  p->last_unit_map.clear();
+  return launch(p, GEMM_SCHED_DYNAMIC, false, args, tm * tn, K, s, &op, form);
+}
+
+}  // namespace ptg
 
 extern "C" {
 

@@ -17,6 +17,7 @@ static_assert(LAYER_ACT_NONE == ptg::kActNone && LAYER_ACT_RELU == ptg::kActRelu
 struct layer_plan {
   int device = 0;
   int cu_count = 0;
+  gemm_tile_cfg tiles256 = nullptr, tiles128 = nullptr;  // the tiled products' plans
   float *d_ws = nullptr;  // partial sums
   hipEvent_t stream_switch = nullptr;
   hipStream_t last_stream = nullptr;
@@ -88,6 +89,25 @@ bool bad_stride(int64_t ld, int64_t m, int64_t n, int64_t step) {
   return m > 1 && n > 0 && (ld < n || ld > LAYER_MAX_COLS || ld % step != 0);
 }
 
+// The GEMM plan of a layer plan: the library's defaults with a split tail.
+gemm_status make_tiles(gemm_tile_cfg *out, int32_t edge, int32_t device) {
+  gemm_tile_desc d;
+  gemm_status st = gemm_default_desc(&d, edge, device);
+  if (st != GEMM_OK) return st;
+  d.tail_split = GEMM_TAIL_SPLIT_AUTO;
+  d.max_groups = 1;
+  return gemm_create(out, &d);
+}
+
+// Tiles of 256 x 256 where they fill the machine, of 128 x 128 below that.
+gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStream_t s) {
+  const int64_t tiles = ceil_div(a.m, 256) * ceil_div(a.n, 256);
+  gemm_tile_cfg t = tiles >= p->cu_count ? p->tiles256 : p->tiles128;
+  gemm_status st = ptg::plan_run_product(t, a, form, s);
+  if (st == GEMM_E_HIP) p->last_error = gemm_last_hip_error(t);
+  return st;
+}
+
 // Partial sums of n columns over at most `wanted` rows: as many rows as the workspace holds.
 int64_t partial_rows(int64_t wanted, int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(wanted, kWsFloats / std::max<int64_t>(n, 1))); }
 
@@ -120,6 +140,10 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
     layer_destroy(p);
     return GEMM_E_HIP;
   }
+  if ((st = make_tiles(&p->tiles256, 256, device)) != GEMM_OK || (st = make_tiles(&p->tiles128, 128, device)) != GEMM_OK) {
+    layer_destroy(p);
+    return st;
+  }
   *out = p;
   return GEMM_OK;
 }
@@ -127,6 +151,8 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
 gemm_status layer_destroy(layer_cfg p) {
   if (!p) return GEMM_OK;
   if (p->has_run) (void)hipStreamSynchronize(p->last_stream);
+  (void)gemm_destroy(p->tiles256);
+  (void)gemm_destroy(p->tiles128);
   if (p->stream_switch) (void)hipEventDestroy(p->stream_switch);
   if (p->d_ws) (void)hipFree(p->d_ws);
   delete p;
@@ -137,7 +163,15 @@ gemm_status layer_sync(layer_cfg p) {
   if (!p) return GEMM_E_INVALID_ARG;
   if (!p->has_run) return GEMM_OK;
   hipError_t e = hipStreamSynchronize(p->last_stream);
-  return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "hipStreamSynchronize");
+  if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
+  gemm_status st = GEMM_OK;
+  for (gemm_tile_cfg t : {p->tiles256, p->tiles128}) {
+    const gemm_status one = gemm_sync(t);
+    if (one == GEMM_OK) continue;
+    p->last_error = gemm_last_hip_error(t);
+    st = one;
+  }
+  return st;
 }
 
 const char *layer_last_hip_error(layer_cfg p) { return p ? p->last_error.c_str() : ""; }
@@ -277,8 +311,7 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
-  hipError_t e = ptg::launch_product_simple(k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
-  return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
+  return run_tiles(p, k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
 }
 
 gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer_cfg p, void *stream) {
@@ -359,8 +392,8 @@ gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, 
     k.ep.out = a->dx;
     k.ep.ldo = a->lddx;
     k.ep.out_type = a->dx_type;
-    hipError_t e = ptg::launch_product_simple(k, ptg::kFormNN, s);
-    if (e != hipSuccess) return hip_fail(p, e, "linear backward, dx");
+    st = run_tiles(p, k, ptg::kFormNN, s);
+    if (st != GEMM_OK) return st;
   }
   if (any_dw) {
     std::memset(&k, 0, sizeof(k));
@@ -377,8 +410,8 @@ gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, 
     k.ep.residual = a->accumulate ? a->dw : nullptr;
     k.ep.ldr = a->lddw;
     k.ep.residual_type = a->dw_type;
-    hipError_t e = ptg::launch_product_simple(k, ptg::kFormTN, s);
-    if (e != hipSuccess) return hip_fail(p, e, "linear backward, dw");
+    st = run_tiles(p, k, ptg::kFormTN, s);
+    if (st != GEMM_OK) return st;
   }
   return GEMM_OK;
 }

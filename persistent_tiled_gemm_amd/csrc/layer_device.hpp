@@ -48,11 +48,33 @@ template <> __device__ __forceinline__ void store8<e4m3_t>(e4m3_t *p, const f32x
 // activations use it on (the argument's own rounding, |t| 2^-24, dominates).
 __device__ __forceinline__ float exp_f32(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504088896341f); }
 
+// The same past the caches: written once, not read by the kernel that writes it.
+template <typename T> __device__ __forceinline__ void store8_nt(T *p, const f32x8 &v);
+template <> __device__ __forceinline__ void store8_nt<float>(float *p, const f32x8 &v) {
+  __builtin_nontemporal_store(__builtin_shufflevector(v, v, 0, 1, 2, 3), (f32x4 *)p);
+  __builtin_nontemporal_store(__builtin_shufflevector(v, v, 4, 5, 6, 7), (f32x4 *)(p + 4));
+}
+template <> __device__ __forceinline__ void store8_nt<__bf16>(__bf16 *p, const f32x8 &v) {
+  __builtin_nontemporal_store(__builtin_convertvector(v, bf16x8), (bf16x8 *)p);
+}
+
 // Activations in fp32. The logistic function is 1 / (1 + e^-t): e^-t that
 // overflows to infinity gives 0, and the products with z below are then 0 z; for
 // z = -inf that is NaN where the limit is 0, so the result is selected, not
 // multiplied, there.
 __device__ __forceinline__ float logistic(float t) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-t)); }
+
+// Phi(z), the normal distribution function: erfc by Abramowitz and Stegun's
+// formula 7.1.26 (a polynomial in 1 / (1 + p x) times e^-x^2, absolute error of
+// erf below 1.5e-7), x = |z| / sqrt 2. Written with erfc, so that the left tail
+// keeps its size instead of cancelling against 1.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+  const float poly = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  const float half = 0.5f * poly * exp_f32(-x * x);
+  return z < 0.0f ? half : 1.0f - half;
+}
 
 static constexpr float kGeluC = 0.79788456080286536f;  // sqrt(2 / pi)
 static constexpr float kGeluA = 0.044715f;
@@ -60,7 +82,10 @@ static constexpr float kGeluA = 0.044715f;
 __device__ __forceinline__ float act_f32(int32_t act, float z) {
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
-    case kActGelu: return z == -INFINITY ? 0.0f : 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case kActGelu: {
+      const float p = normal_cdf(z);
+      return p == 0.0f ? 0.0f : z * p;
+    }
     case kActGeluTanh: {
       // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
       const float p = logistic(2.0f * kGeluC * (z + kGeluA * z * z * z));
@@ -74,6 +99,29 @@ __device__ __forceinline__ float act_f32(int32_t act, float z) {
   }
 }
 
+// act_f32 of eight values, the activation decided once.
+__device__ __forceinline__ void act8(int32_t act, f32x8 &v) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActRelu, v[e]);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActGelu, v[e]);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActGeluTanh, v[e]);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActSilu, v[e]);
+      break;
+    default: break;
+  }
+}
+
 // d act / dz. The terms z f'(z) vanish faster than z grows; where the factor
 // has underflowed to 0 the term is 0 (selected, so that infinite z gives no NaN).
 __device__ __forceinline__ float act_grad_f32(int32_t act, float z) {
@@ -81,7 +129,7 @@ __device__ __forceinline__ float act_grad_f32(int32_t act, float z) {
     case kActRelu: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
     case kActGelu: {
       const float pdf = 0.39894228040143268f * exp_f32(-0.5f * z * z);
-      return 0.5f * erfcf(z * -0.70710678118654752f) + (pdf == 0.0f ? 0.0f : z * pdf);
+      return normal_cdf(z) + (pdf == 0.0f ? 0.0f : z * pdf);
     }
     case kActGeluTanh: {
       const float p = logistic(2.0f * kGeluC * (z + kGeluA * z * z * z));

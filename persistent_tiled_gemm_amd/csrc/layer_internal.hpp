@@ -5,6 +5,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ptg_gemm.h"
+#include "ptg_internal.hpp"
+
 namespace ptg {
 
 enum LayerType { kTypeF32 = 0, kTypeBf16 = 1, kTypeE4m3 = 2 };
@@ -74,6 +77,16 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs &a, int cu_count, hipStrea
 // out[j] = sum over `rows` of partial[row][j] (+ out[j] with accumulate), in row order.
 hipError_t launch_column_sum(const float *partial, int rows, int32_t n, float *out, int accumulate, hipStream_t s);
 hipError_t launch_activation_backward(const ActGradArgs &a, int row_groups, hipStream_t s);
-hipError_t launch_product_simple(const ProductArgs &a, int form, hipStream_t s);
+
+// What a tiled product takes beside the GEMM's own arguments. Row strides in
+// 16-bit units (two e4m3 values), as the GEMM's body counts them.
+struct ProductOpArgs {
+  EpilogueArgs ep;
+  int32_t lda, ldb;
+};
+hipError_t launch_product(int tile_edge, int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+// The product as a run of a GEMM plan: its tiles, dynamic scheduler and split
+// tail. The caller orders runs on different streams.
+gemm_status plan_run_product(gemm_tile_cfg plan, const ProductArgs &a, int form, hipStream_t s);
 
 }  // namespace ptg
