@@ -20,7 +20,7 @@ LIB_NAME = "libptg_gemm.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["gemm_kernel.hip", "spoiler.hip", "mfma_probe.hip", "hbm_probe.hip", "gemm_api.hip",
-           "layer_api.hip", "norm_kernel.hip", "act_kernel.hip", "product_kernel.hip"]
+           "layer_api.hip", "norm_kernel.hip", "act_kernel.hip", "product_kernel.hip", "rows_kernel.hip"]
 
 # gfx950 only. Packed-fp32 VALU forms are disabled (hipcc makes them from plain
 # float code; some of their forms have produced wrong results on this part).

@@ -19,6 +19,7 @@ struct layer_plan {
   int cu_count = 0;
   gemm_tile_cfg tiles256 = nullptr, tiles128 = nullptr;  // the tiled products' plans
   float *d_ws = nullptr;  // partial sums
+  uint32_t *d_arrivals = nullptr;  // arrival counts of the few-row product's shared tiles, zero between calls
   hipEvent_t stream_switch = nullptr;
   hipStream_t last_stream = nullptr;
   bool has_run = false;
@@ -28,6 +29,7 @@ struct layer_plan {
 namespace {
 
 constexpr int64_t kWsFloats = 16 << 20;  // 64 MiB: 16 partial rows of the widest column sum
+constexpr int64_t kArrivals = 4096;      // a tile whose k is shared is one of fewer than 16 waves x CUs / 4
 
 gemm_status hip_fail(layer_plan *p, hipError_t e, const char *what) {
   if (p) p->last_error = std::string(what) + ": " + hipGetErrorString(e);
@@ -135,6 +137,15 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
     layer_destroy(p);
     return GEMM_E_NOMEM;
   }
+  if (hipMalloc(&p->d_arrivals, sizeof(uint32_t) * (size_t)kArrivals) != hipSuccess) {
+    p->d_arrivals = nullptr;
+    layer_destroy(p);
+    return GEMM_E_NOMEM;
+  }
+  if (hipMemset(p->d_arrivals, 0, sizeof(uint32_t) * (size_t)kArrivals) != hipSuccess) {
+    layer_destroy(p);
+    return GEMM_E_HIP;
+  }
   if (hipEventCreateWithFlags(&p->stream_switch, hipEventDisableTiming) != hipSuccess) {
     p->stream_switch = nullptr;
     layer_destroy(p);
@@ -155,6 +166,7 @@ gemm_status layer_destroy(layer_cfg p) {
   (void)gemm_destroy(p->tiles128);
   if (p->stream_switch) (void)hipEventDestroy(p->stream_switch);
   if (p->d_ws) (void)hipFree(p->d_ws);
+  if (p->d_arrivals) (void)hipFree(p->d_arrivals);
   delete p;
   return GEMM_OK;
 }
@@ -311,6 +323,12 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
+  if (a->m <= ptg::kRowsMost) {
+    int64_t tiles = 0;
+    if (ptg::rows_partial_floats(k, e8, p->cu_count, &tiles) > kWsFloats || tiles > kArrivals) return GEMM_E_SHAPE;
+    hipError_t e = ptg::launch_rows(k, e8, p->d_ws, p->d_arrivals, p->cu_count, s);
+    return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
+  }
   return run_tiles(p, k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
 }
 

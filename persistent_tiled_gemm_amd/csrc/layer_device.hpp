@@ -34,6 +34,12 @@ template <> __device__ __forceinline__ void store8<__bf16>(__bf16 *p, const f32x
   *(bf16x8 *)p = __builtin_convertvector(v, bf16x8);
 }
 static constexpr float kE4m3Max = 448.0f;  // the largest e4m3 value
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+// Four at a time (rows are 8-byte aligned there).
+__device__ __forceinline__ f32x4 load4_as(const void *p, int32_t type, int64_t i) {
+  return type == kTypeF32 ? *(const f32x4 *)((const float *)p + i) : __builtin_convertvector(*(const bf16x4 *)((const __bf16 *)p + i), f32x4);
+}
+__device__ __forceinline__ void store4(__bf16 *p, const f32x4 &v) { *(bf16x4 *)p = __builtin_convertvector(v, bf16x4); }
 struct e4m3_t { uint8_t bits; };
 template <> __device__ __forceinline__ void store8<e4m3_t>(e4m3_t *p, const f32x8 &v) {
   int lo = 0, hi = 0;
