@@ -251,11 +251,17 @@ void plan_units(const gemm_plan *p, bool grouped, int32_t mode, int64_t tiles, i
 
 // product, form: a layer operator's product instead of the plain GEMM (dynamic mode, one problem).
 gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, int64_t tiles, int64_t K,
-                   hipStream_t s, const ptg::ProductOpArgs *product = nullptr, int form = 0) {
+                   hipStream_t s, const ptg::ProductOpArgs *product = nullptr, int form = 0, int32_t split = 1, int64_t split_base_ = 0) {
   if (mode < GEMM_SCHED_NONPERSISTENT || mode > GEMM_SCHED_DYNAMIC) return GEMM_E_INVALID_ARG;
   int64_t items = tiles, split_base = tiles;
   int32_t chunks = 1, group = 1;
-  plan_units(p, grouped, mode, tiles, K, &items, &split_base, &chunks, &group);
+  if (!product) {
+    plan_units(p, grouped, mode, tiles, K, &items, &split_base, &chunks, &group);
+  } else if (split > 1) {
+    split_base = split_base_;
+    chunks = split;
+    items = split_base + (tiles - split_base) * split;
+  }
   if (items > GEMM_MAX_TILES) return GEMM_E_SHAPE;
   const int64_t units = ceil_div(items, group);
   // Non-persistent: one workgroup per unit. Static: P workers. Dynamic: one
@@ -396,7 +402,7 @@ gemm_status noalloc_setup(int dev, hipStream_t s, NoallocDevice **out) {
 
 namespace ptg {
 
-gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, hipStream_t s) {
+gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s) {
   const int64_t units = form == kFormNTE4m3 ? 2 : 1;  // values per 16-bit unit along k
   const int64_t K = a.k / units;
   const int64_t tm = ceil_div(a.m, p->desc.bm), tn = ceil_div(a.n, p->desc.bn);
@@ -418,7 +424,12 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, hi
   p->last_tile_start.assign(1, 0);
   p->last_k.assign(1, (int32_t)K);
   p->last_unit_map.clear();
-  return launch(p, GEMM_SCHED_DYNAMIC, false, args, tm * tn, K, s, &op, form);
+  if (split > 1 && (tm * tn - split_base) * split > p->ws_tiles) return GEMM_E_SHAPE;
+  const gemm_status st = launch(p, GEMM_SCHED_DYNAMIC, false, args, tm * tn, K, s, &op, form, split, split_base);
+  if (st != GEMM_OK || split <= 1) return st;
+  const hipError_t e = launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, (int32_t)split_base, (int32_t)(tm * tn - split_base),
+                                             split, s);
+  return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "split product");
 }
 
 }  // namespace ptg

@@ -65,12 +65,12 @@ namespace ptg {
 // wave64s; each wave owns a (BM/WAVES_M) x (BN/WAVES_N) block of the output
 // tile, made of MB x MB MFMA blocks: MB = 32 uses v_mfma_f32_32x32x16_bf16 (two
 // MFMAs per 32-deep stage), MB = 16 uses v_mfma_f32_16x16x32_bf16 (one).
-template <int BM, int BN, int WAVES_M, int WAVES_N, int MB_>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int MB_, int STAGES = 4>
 struct Cfg {
   static constexpr int BM_ = BM, BN_ = BN, WAVES_N_ = WAVES_N;
   static constexpr int NW = WAVES_M * WAVES_N;
   static constexpr int THREADS = 64 * NW;
-  static constexpr int BK = 32, NSTAGE = 4;          // k per stage, LDS stages
+  static constexpr int BK = 32, NSTAGE = STAGES;     // k per stage, LDS stages
   static constexpr int MB = MB_, KS = 512 / MB_;     // MFMA block edge, k per MFMA
   static constexpr int ACC_N = MB * MB / 64;         // accumulator floats per lane per block
   static constexpr int QUADS = ACC_N / 4;            // 16-byte groups of them
@@ -766,19 +766,19 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
 
     constexpr int kLoads = CF::A_LOADS + CF::B_LOADS;
     constexpr int kMfma = CF::MI * CF::NI;
-    static_assert(CF::NSTAGE == 4, "stage ring");
+    constexpr int NST = CF::NSTAGE, kMask = NST - 1;
+    static_assert((NST & kMask) == 0 && NST >= 4, "stage ring");
     if constexpr (CF::MB == 32) {
       if (ke > kb) {
-        // four 32-deep stages: the loads of k-step kt+3 go out during k-step kt
-        // into the stage k-step kt-1 just left, so a load has two and a half to
-        // three k-steps to land;
+        // four 32-deep stages (or eight): the loads of k-step kt+3 (kt+7) go out
+        // during k-step kt into the stage k-step kt-1 just left, so a load has two
+        // and a half to three (six and a half to seven) k-steps to land;
         // each k-step is two 16-deep MFMA slices, and the fragments of one slice
         // are read while the other's MFMAs run
         static_assert(kLoads == 4, "stage ring");
-        issue_all(0, kb);
-        issue_all(1, kb + 1);
-        issue_all(2, kb + 2);
-        asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+#pragma unroll
+        for (int q = 0; q < NST - 1; ++q) issue_all(q, kb + q);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
         wg_barrier();
         frag a0[CF::MI], b0[CF::NI], a1[CF::MI], b1[CF::NI];
         read_frags(0, 0, a0, b0, 0, 0, 0);
@@ -788,21 +788,21 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         uint32_t voff_fast[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) voff_fast[j] = load_voff_edge(j);
-        const int32_t slow_from = (K % CF::BK != 0 && full < ke) ? max(kb, full - 3) : ke;
+        const int32_t slow_from = (K % CF::BK != 0 && full < ke) ? max(kb, full - (NST - 1)) : ke;
         auto step = [&](int32_t kt, bool fast) {
-          const int st = (kt - kb) & 3;
+          const int st = (kt - kb) & kMask;
           // two of the four loads of k-step kt+3 go out with each slice's reads
           // (spread over the step: 4096^3 dynamic 175 -> 152 us against all four
           // with the first slice)
-          read_frags(st, 1, a1, b1, (st + 3) & 3, kt + 3, kLoads / 2, fast ? voff_fast : nullptr);
+          read_frags(st, 1, a1, b1, (st + NST - 1) & kMask, kt + NST - 1, kLoads / 2, fast ? voff_fast : nullptr);
           mma(a0, b0);
           interleave<kReads, kMfma>();
           // stage st fully read and stage st+1 landed (its loads went out during
-          // step kt-2; the six loads issued since may still be in flight)
+          // step kt-2, or kt-6; the loads issued since, six or 22, may still be in flight)
           wait_lds_all();
-          asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 3) * kLoads + kLoads / 2) : "memory");
           wg_barrier();
-          read_frags((st + 1) & 3, 0, a0, b0, (st + 3) & 3, kt + 3, kLoads / 2, fast ? voff_fast : nullptr, kLoads / 2);
+          read_frags((st + 1) & kMask, 0, a0, b0, (st + NST - 1) & kMask, kt + NST - 1, kLoads / 2, fast ? voff_fast : nullptr, kLoads / 2);
           mma(a1, b1);
           interleave<kReads, kMfma>();
         };
@@ -827,12 +827,9 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // wave finished reading it before the barrier that ended step kt-1), and
         // must have landed by the barrier that ends step kt+2: between two and
         // three k-steps in flight.
-        static_assert(kLoads == 8 || E8, "stage ring");
-        issue_all(0, kb);
-        issue_all(1, kb + 1);
-        issue_all(2, kb + 2);
-        issue_all(3, kb + 3);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");  // stages 0 and 1 landed
+#pragma unroll
+        for (int q = 0; q < NST; ++q) issue_all(q, kb + q);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");  // stages 0 and 1 landed
         wg_barrier();
         frag a0[CF::MI], b0[CF::NI], a1[CF::MI], b1[CF::NI];
         // e4m3: the k-step's fragments as they lie in LDS, 16 values a lane: lane
@@ -896,10 +893,10 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // per-lane base plus an immediate offset
         auto step = [&](auto fast, int32_t kt, int st, const frag(&ac)[CF::MI], const frag(&bc)[CF::NI],
                         frag(&an)[CF::MI], frag(&bn)[CF::NI]) {
-          const int rst = (st + 1) & 3;
+          const int rst = (st + 1) & kMask;
           const unsigned char *sa = smem + CF::a_off(rst);
           const unsigned char *sb = smem + CF::b_off(rst);
-          const int32_t kt_load = kt + 4;
+          const int32_t kt_load = kt + NST;
           const i32x4 ra = make_rsrc_words(a_kstep(phys(kt_load)), kt_load < ke);
           const i32x4 rb = make_rsrc_words(b_kstep(phys(kt_load)), kt_load < ke);
           const uint32_t lbase = lds_addr(smem);
@@ -930,19 +927,21 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
           };
           // (a spacing of eight, which lines the loads up with the rows of the
           // accumulator grid, made the compiler give up unrolling the step)
-          static_assert(E8 || 3 + 7 * (kLoads - 1) < kMfma, "load placement");
+          constexpr int kLoadFirst = kMfma >= 64 ? 3 : 1, kLoadEvery = kMfma >= 64 ? 7 : kMfma / kLoads;
+          static_assert(kLoadFirst + kLoadEvery * (kLoads - 1) < kMfma && (kReads <= kMfma), "load placement");
 #pragma unroll
           for (int i = 0; i < kMfma; ++i) {
             mfma16(i / CF::NI, i % CF::NI, ac[i / CF::NI], bc[i % CF::NI]);
             if (i < kReads) read(i);
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-              if (3 + 7 * j == i)
+              if (kLoadFirst + kLoadEvery * j == i)
                 load16_to_lds(j < CF::A_LOADS ? ra : rb, lbase + load_dst(j, st),
                               decltype(fast)::value ? voff_fast[j] : load_voff(j, kt_load));
           }
-          wait_lds_all();
-          asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+          if constexpr (OP::kPlain) wait_lds_all();
+          else __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), known to the compiler: no waits for these reads in the next step
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
           wg_barrier();
         };
         // The e4m3 k-step: the first half's MFMAs with the second half's widening
@@ -951,8 +950,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // tile: they issue in the MFMAs' shadow). The conversions are pinned where
         // they stand; left free, they gather at the ends of the halves.
         auto step8 = [&](auto fast, int32_t kt, int st) {
-          const int rst = (st + 1) & 3;
-          const int32_t kt_load = kt + 4;
+          const int rst = (st + 1) & kMask;
+          const int32_t kt_load = kt + NST;
           const i32x4 ra = make_rsrc_words(a_kstep(phys(kt_load)), kt_load < ke);
           const i32x4 rb = make_rsrc_words(b_kstep(phys(kt_load)), kt_load < ke);
           const uint32_t lbase = lds_addr(smem);
@@ -992,8 +991,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
               __builtin_amdgcn_sched_barrier(0);
             }
           }
-          wait_lds_all();
-          asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // as in step
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
           wg_barrier();
         };
         // the zeroed accumulators in their registers, then 16 wait states, before
@@ -1013,7 +1012,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // t (t - kb even) with t + 5 >= full on; the trips before it use the fast
         // offsets.
         const int32_t slow_from =
-            (K % CF::BK != 0 && full < ke) ? kb + ((max(full - 5 - kb, 0) + 1) / 2) * 2 : ke + 2;
+            (K % CF::BK != 0 && full < ke) ? kb + ((max(full - (NST + 1) - kb, 0) + 1) / 2) * 2 : ke + 2;
         // Fast trips of four steps while whole ones fit (constant stages), then
         // two-step trips with the stage computed at run time. A run starts with
         // kt - kb a multiple of 4.
@@ -1021,29 +1020,31 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
           const int32_t fast_end = min(end, slow_from);
           if constexpr (E8) {
             for (; kt + 4 <= fast_end; kt += 4) {
-              step8(std::true_type{}, kt, 0);
-              step8(std::true_type{}, kt + 1, 1);
-              step8(std::true_type{}, kt + 2, 2);
-              step8(std::true_type{}, kt + 3, 3);
+              const int st = NST == 4 ? 0 : (kt - kb) & kMask;
+              step8(std::true_type{}, kt, st);
+              step8(std::true_type{}, kt + 1, st + 1);
+              step8(std::true_type{}, kt + 2, st + 2);
+              step8(std::true_type{}, kt + 3, st + 3);
             }
-            for (; kt < end; ++kt) step8(std::false_type{}, kt, (kt - kb) & 3);
+            for (; kt < end; ++kt) step8(std::false_type{}, kt, (kt - kb) & kMask);
             return;
           }
           for (; kt + 4 <= fast_end; kt += 4) {
-            step(std::true_type{}, kt, 0, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 1, 1, a1, b1, a0, b0);
-            step(std::true_type{}, kt + 2, 2, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 3, 3, a1, b1, a0, b0);
+            const int st = NST == 4 ? 0 : (kt - kb) & kMask;
+            step(std::true_type{}, kt, st, a0, b0, a1, b1);
+            step(std::true_type{}, kt + 1, st + 1, a1, b1, a0, b0);
+            step(std::true_type{}, kt + 2, st + 2, a0, b0, a1, b1);
+            step(std::true_type{}, kt + 3, st + 3, a1, b1, a0, b0);
           }
           for (; kt < fast_end; kt += 2) {
-            const int st = (kt - kb) & 3;
+            const int st = (kt - kb) & kMask;
             step(std::true_type{}, kt, st, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 1, (st + 1) & 3, a1, b1, a0, b0);
+            step(std::true_type{}, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
           }
           for (; kt < end; kt += 2) {
-            const int st = (kt - kb) & 3;
+            const int st = (kt - kb) & kMask;
             step(std::false_type{}, kt, st, a0, b0, a1, b1);
-            step(std::false_type{}, kt + 1, (st + 1) & 3, a1, b1, a0, b0);
+            step(std::false_type{}, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
           }
         };
         int32_t kt = kb;
@@ -1155,7 +1156,12 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
           if (interior || (m < M && n < N)) __builtin_nontemporal_store(v, (f32x4 *)(pb.C + (size_t)m * (size_t)N + n));
         }
       } else {
-        OP::template flush<RP, ROW_B>(op, wl, lane, m0 + (int32_t)(wm * CF::WM) + p * RP, n0 + (int32_t)(wn * CF::WN), M, N);
+        // a K-chunk's rows go to its slot of the workspace as they are: a second
+        // kernel adds the chunks and finishes the tile
+        float *slot = split ? args.ws + (size_t)(item - (uint32_t)args.split_base) * (BM * BN) +
+                                  (size_t)(wm * CF::WM + p * RP) * BN + wn * CF::WN
+                            : nullptr;
+        OP::template flush<RP, ROW_B, BN>(op, wl, lane, m0 + (int32_t)(wm * CF::WM) + p * RP, n0 + (int32_t)(wn * CF::WN), M, N, slot);
       }
       // the reads are done before the next pass (or the next unit's loads) writes the region
       wait_lds_all();
@@ -1163,7 +1169,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     };
     auto epi_end = [&]() { wg_barrier(); };
 
-    if (!split) {
+    if (!OP::kPlain || !split) {
       epi_begin();
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
@@ -1178,7 +1184,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         flush(p);
       }
       epi_end();
-    } else {
+    } else if constexpr (OP::kPlain) {
       // K-chunk of a split tile: publish the partial sum; the workgroup that
       // completes the tile's last chunk adds all partials in chunk order and
       // writes C. The order is fixed, so the result does not depend on who

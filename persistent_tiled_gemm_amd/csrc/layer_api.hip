@@ -101,11 +101,56 @@ gemm_status make_tiles(gemm_tile_cfg *out, int32_t edge, int32_t device) {
   return gemm_create(out, &d);
 }
 
-// Tiles of 256 x 256 where they fill the machine, of 128 x 128 below that.
+// How a product of T output tiles and nk k-steps (32 deep) runs: tile edge, and
+// the K-chunks S that the tiles from `base` on are split into.
+struct TileChoice { int edge; int32_t split; int64_t base; double us; };
+
+// The choice is the least of the times that two fits give, in microseconds (256
+// CUs; measured over m = 100 .. 4096, n = 1024 .. 16384, k = 776 .. 8192 in the
+// linear layer's and the weight gradient's layouts; within about 15% of them):
+//   128 x 128 tiles   a k-step takes 0.24 while a CU has one tile and 0.29 a tile
+//                     when it has more; 8 to fill and drain;
+//   256 x 256 tiles   a k-step takes 0.45 with few CUs at work and 0.7 with all of
+//                     them (power and memory shared), 22 to fill and drain;
+//   splitting         4 for the second launch, and each chunk's sums written and
+//                     read: 0.02 a chunk of 128 x 128, 0.06 of 256 x 256.
+// Both sides where it matters: 512 x 8192 x 8192, 256 tiles of 128: 72 us, 64 tiles
+// of 256 in 3 chunks: 86; 1024 x 8192 x 8192, 512 tiles of 128: 154, 128 tiles of
+// 256 in 2 chunks: 132; 256 x 4096 x 4096, 64 tiles of 128: 38, in 4 chunks: 26;
+// 100 x 1024 x 8192, 8 tiles of 128: 46, in 8 chunks: 21.
+TileChoice choose_tiles(int64_t m, int64_t n, int64_t nk, int64_t cus) {
+  TileChoice best = {256, 1, 0, 1e300};
+  for (const int edge : {128, 256}) {
+    const int64_t T = ceil_div(m, edge) * ceil_div(n, edge);
+    const int64_t slots = edge == 256 ? cus : 2 * cus;  // chunks the workspace holds
+    // the time of `units` tiles or chunks of `steps` k-steps
+    auto run = [&](int64_t units, double steps) {
+      const double load = (double)units / (double)cus;
+      if (edge == 128) return steps * (load <= 1.0 ? 0.24 : std::max(0.58, 0.29 * load));
+      return steps * (load <= 1.0 ? 0.45 + 0.25 * load * load : 0.7 * (double)ceil_div(units, cus));
+    };
+    const double fixed = edge == 256 ? 22.0 : 8.0, join = edge == 256 ? 0.06 : 0.02;
+    const double whole = fixed + run(T, (double)nk);
+    if (whole < best.us) best = {edge, 1, 0, whole};
+    // all tiles, or those of the partial last wave
+    const int64_t waves = T / cus * cus;
+    for (const int64_t base : {(int64_t)0, waves}) {
+      const int64_t r = T - base;
+      if (r == 0 || (base != 0 && edge == 128)) continue;  // (small tiles' last wave shares the CUs of the wave before)
+      for (int32_t S = 2; S <= 32 && r * S <= slots && nk / S >= 4; ++S) {
+        const double us = fixed + (base ? run(base, (double)nk) : 0.0) + run(r * S, (double)ceil_div(nk, S)) + 4.0 + join * (double)(r * S);
+        if (us < best.us) best = {edge, S, base, us};
+      }
+    }
+  }
+  return best;
+}
+
 gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStream_t s) {
-  const int64_t tiles = ceil_div(a.m, 256) * ceil_div(a.n, 256);
-  gemm_tile_cfg t = tiles >= p->cu_count ? p->tiles256 : p->tiles128;
-  gemm_status st = ptg::plan_run_product(t, a, form, s);
+  const int64_t nk = ceil_div(form == ptg::kFormNTE4m3 ? a.k / 2 : a.k, 32);
+  const TileChoice c = choose_tiles(a.m, a.n, nk, p->cu_count);
+  gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
+  gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
   if (st == GEMM_E_HIP) p->last_error = gemm_last_hip_error(t);
   return st;
 }

@@ -98,8 +98,12 @@ struct ProductOpArgs {
   int32_t lda, ldb;
 };
 hipError_t launch_product(int tile_edge, int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
-// The product as a run of a GEMM plan: its tiles, dynamic scheduler and split
-// tail. The caller orders runs on different streams.
-gemm_status plan_run_product(gemm_tile_cfg plan, const ProductArgs &a, int form, hipStream_t s);
+// Adds the chunks of the tiles [first, first + tiles) and finishes them.
+hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
+                                 int32_t tiles, int32_t chunks, hipStream_t s);
+// The product as a run of a GEMM plan: its tiles and dynamic scheduler; the tiles
+// from split_base on are split into `split` K-chunks each (1: none), which a
+// second kernel joins. The caller orders runs on different streams.
+gemm_status plan_run_product(gemm_tile_cfg plan, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s);
 
 }  // namespace ptg

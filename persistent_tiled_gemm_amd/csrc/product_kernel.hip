@@ -30,12 +30,59 @@ __device__ __forceinline__ EpilogueArgs epilogue_args() {
   return e;
 }
 
+// What the epilogue needs of one row's eight columns, as loaded: the residual's 16
+// or 32 bytes and the row's scale.
+struct RowTerms { i32x4 lo, hi; float scale; };
+template <bool E8>
+__device__ __forceinline__ RowTerms row_terms(const EpilogueArgs &e, int64_t m, int32_t n) {
+  RowTerms t = {{0, 0, 0, 0}, {0, 0, 0, 0}, 1.0f};
+  if (e.residual) {
+    const int64_t at = m * e.ldr + n;
+    if (e.residual_type == kTypeF32) {
+      t.lo = *(const i32x4 *)((const float *)e.residual + at);
+      t.hi = *(const i32x4 *)((const float *)e.residual + at + 4);
+    } else {
+      t.lo = *(const i32x4 *)((const __bf16 *)e.residual + at);
+    }
+  }
+  if (E8 && e.row_scale) t.scale = e.row_scale[m];
+  return t;
+}
+
+// Of eight columns, the same for every row.
+struct ColumnTerms { f32x8 bias, scale; };
+template <bool E8>
+__device__ __forceinline__ ColumnTerms column_terms(const EpilogueArgs &e, int32_t n) {
+  ColumnTerms t = {{}, {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}};
+  if (e.bias) t.bias = load8_as(e.bias, e.bias_type, n);
+  if (E8 && e.col_scale) t.scale = load8(e.col_scale + n);
+  return t;
+}
+
+// z of row m, columns n .. n + 7, to out (and pre).
+template <bool E8>
+__device__ __forceinline__ void finish8(const EpilogueArgs &e, int64_t m, int32_t n, f32x8 z, const ColumnTerms &col, const RowTerms &row) {
+  if constexpr (E8) z = z * row.scale * col.scale;
+  z += col.bias;
+  if (e.pre) store8_nt((__bf16 *)e.pre + m * e.ldp + n, z);
+  act8(e.act, z);
+  if (e.residual) {
+    if (e.residual_type == kTypeF32)
+      z += __builtin_shufflevector(__builtin_bit_cast(f32x4, row.lo), __builtin_bit_cast(f32x4, row.hi), 0, 1, 2, 3, 4, 5, 6, 7);
+    else
+      z += __builtin_convertvector(__builtin_bit_cast(bf16x8, row.lo), f32x8);
+  }
+  if (e.out_type == kTypeF32) store8_nt((float *)e.out + m * e.ldo + n, z);
+  else store8_nt((__bf16 *)e.out + m * e.ldo + n, z);
+}
+
 template <int FORM>
 struct ProductOp {
   using Args = ProductOpArgs;
   static constexpr bool AT = FORM == kFormTN, E8 = FORM == kFormNTE4m3, BT = FORM == kFormNT || E8, kPlain = false;
-  // e4m3: 16 x 16 blocks for both tile edges
-  template <int EDGE> using Tile = typename std::conditional<E8, Cfg<EDGE, EDGE, 2, 2, 16>, typename TileCfg<EDGE>::type>::type;
+  // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step ahead of their MFMAs (the 128 x 128
+  // tile's other form, 32 x 32 blocks read half a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192)
+  template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
 
@@ -47,9 +94,10 @@ struct ProductOp {
   // the code (five activations of eight values: unrolled over the rows they
   // outgrow the instruction cache and the registers), with the residuals and row
   // scales of the next kAhead rows under way.
-  template <int RP, int ROW_B>
+  // slot: a K-chunk's sums go there unfinished, rows STRIDE floats apart.
+  template <int RP, int ROW_B, int STRIDE>
   static __device__ __forceinline__ void flush(const Args &, const unsigned char *wl, uint32_t lane, int32_t m_base, int32_t n_base,
-                                               int32_t M, int32_t N) {
+                                               int32_t M, int32_t N, float *slot) {
     constexpr int LPR = ROW_B / 32, RPI = 64 / LPR, kRows = RP / RPI, kAhead = 4;
     static_assert(kRows >= kAhead && (LPR == 16 || LPR == 8), "epilogue");
     const EpilogueArgs e = epilogue_args();
@@ -58,28 +106,13 @@ struct ProductOp {
     const uint32_t q = lane % LPR, r0 = lane / LPR;
     const int32_t n = n_base + (int32_t)(8u * q);
     if (n >= N) return;
-    f32x8 bias = {}, cs = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-    if (e.bias) bias = load8_as(e.bias, e.bias_type, n);
-    if (E8 && e.col_scale) cs = load8(e.col_scale + n);
-    struct Ahead { i32x4 lo, hi; float rs; };  // a row's residual as loaded, and its scale
-    auto ask = [&](int i) -> Ahead {
-      Ahead a = {{0, 0, 0, 0}, {0, 0, 0, 0}, 1.0f};
+    const ColumnTerms col = column_terms<E8>(e, n);
+    auto ask = [&](int i) -> RowTerms {
       const int64_t m = (int64_t)m_base + (uint32_t)(i * RPI) + r0;
-      if (i < kRows && m < M) {
-        if (e.residual) {
-          const int64_t at = m * e.ldr + n;
-          if (e.residual_type == kTypeF32) {
-            a.lo = *(const i32x4 *)((const float *)e.residual + at);
-            a.hi = *(const i32x4 *)((const float *)e.residual + at + 4);
-          } else {
-            a.lo = *(const i32x4 *)((const __bf16 *)e.residual + at);
-          }
-        }
-        if (E8 && e.row_scale) a.rs = e.row_scale[m];
-      }
-      return a;
+      if (slot == nullptr && i < kRows && m < M) return row_terms<E8>(e, m, n);
+      return RowTerms{{0, 0, 0, 0}, {0, 0, 0, 0}, 1.0f};
     };
-    Ahead ahead[kAhead];
+    RowTerms ahead[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) ahead[u] = ask(u);
     // 16 lanes a row (32 chunks): lanes 8..15 read their odd chunk first, which
@@ -92,24 +125,14 @@ struct ProductOp {
       const f32x4 v0 = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + odd) ^ (row & 15u)) << 4));
       const f32x4 v1 = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + 1u - odd) ^ (row & 15u)) << 4));
       const f32x4 lo = odd ? v1 : v0, hi = odd ? v0 : v1;
-      f32x8 z = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      const Ahead now = ahead[0];
+      const f32x8 z = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const RowTerms now = ahead[0];
 #pragma unroll
       for (int u = 0; u + 1 < kAhead; ++u) ahead[u] = ahead[u + 1];
       ahead[kAhead - 1] = ask(i + kAhead);
       if (m >= M) continue;
-      if constexpr (E8) z = z * now.rs * cs;
-      z += bias;
-      if (e.pre) store8_nt((__bf16 *)e.pre + m * e.ldp + n, z);
-      act8(e.act, z);
-      if (e.residual) {
-        if (e.residual_type == kTypeF32)
-          z += __builtin_shufflevector(__builtin_bit_cast(f32x4, now.lo), __builtin_bit_cast(f32x4, now.hi), 0, 1, 2, 3, 4, 5, 6, 7);
-        else
-          z += __builtin_convertvector(__builtin_bit_cast(bf16x8, now.lo), f32x8);
-      }
-      if (e.out_type == kTypeF32) store8_nt((float *)e.out + m * e.ldo + n, z);
-      else store8_nt((__bf16 *)e.out + m * e.ldo + n, z);
+      if (slot) store8(slot + row * STRIDE + 8u * q, z);
+      else finish8<E8>(e, m, n, z, col, now);
     }
   }
 };
@@ -117,6 +140,45 @@ struct ProductOp {
 template <int EDGE, int FORM>
 __global__ __launch_bounds__(256, EDGE == 128 ? 2 : 1) void ptg_product_kernel(const ProductKernelArgs a) {
   gemm_body<EDGE, EDGE, kDynamic, false, ProductOp<FORM>>(a.gemm, a.op);
+}
+
+// The tiles that were split along k: their chunks' sums, added in chunk order,
+// through the epilogue. A second launch, so that the whole machine reads the
+// sums: the workgroup that completes a tile, left to finish it alone (as the
+// plain GEMM's split tail is), reads its S x 64 or 256 KiB at the 55 GB/s or so
+// that one CU gets past its L2 (100 x 1024 x 8192, 8 tiles in 8 chunks: 24.8 us).
+struct ReduceArgs {
+  EpilogueArgs ep;
+  const float *ws;
+  int32_t m, n, tiles_n, first, chunks;  // first: the first split tile
+};
+template <int EDGE, bool E8>
+__global__ __launch_bounds__(256) void ptg_product_reduce_kernel(const ReduceArgs a) {
+  constexpr int LPR = EDGE / 8, kRows = 256 / LPR, kParts = EDGE / kRows;  // a workgroup: kRows rows of a tile
+  const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
+  const int32_t t = a.first + (int32_t)tile;
+  const int32_t m = t / a.tiles_n * EDGE + (int32_t)r, n = t % a.tiles_n * EDGE + (int32_t)(8u * q);
+  if (m >= a.m || n >= a.n) return;
+  const RowTerms row = row_terms<E8>(a.ep, m, n);
+  const ColumnTerms col = column_terms<E8>(a.ep, n);
+  const float *p = a.ws + (size_t)tile * a.chunks * (EDGE * EDGE) + r * EDGE + 8u * q;
+  f32x8 z = load8(p);
+  for (int32_t c = 1; c < a.chunks; ++c) z += load8(p + (size_t)c * (EDGE * EDGE));
+  finish8<E8>(a.ep, m, n, z, col, row);
+}
+
+template <int EDGE>
+static hipError_t launch_reduce_edge(const ReduceArgs &a, int tiles, bool e8, hipStream_t s) {
+  const dim3 grid((uint32_t)tiles * (EDGE / (256 / (EDGE / 8))));
+  if (e8) hipLaunchKernelGGL((ptg_product_reduce_kernel<EDGE, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((ptg_product_reduce_kernel<EDGE, false>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
+                                 int32_t tiles, int32_t chunks, hipStream_t s) {
+  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks};
+  return tile_edge == 256 ? launch_reduce_edge<256>(a, tiles, form == kFormNTE4m3, s) : launch_reduce_edge<128>(a, tiles, form == kFormNTE4m3, s);
 }
 
 template <int EDGE>

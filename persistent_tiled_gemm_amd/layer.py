@@ -11,6 +11,7 @@ stream). Outputs are given by the caller.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import GEMM_OK, PtgError, _stream_ptr, load_library
 
@@ -52,6 +53,18 @@ class LinearGradArgs(ctypes.Structure):
                        ("dx_type", "dw_type", "accumulate", "pad"))
 
 
+def _packer(cls):
+    """The structure's values as bytes in one call (setting ctypes fields one by one costs microseconds a call, which is
+    what a decode step's small operators take on the device)."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    p = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")  # native sizes and alignment, padded to 8
+    assert p.size == ctypes.sizeof(cls)
+    return p.pack
+
+
+_RMSNORM, _RMSNORM_GRAD, _LINEAR, _ACTIVATION_GRAD, _LINEAR_GRAD = (
+    _packer(c) for c in (RmsnormArgs, RmsnormGradArgs, LinearArgs, ActivationGradArgs, LinearGradArgs))
+
 _lib = None
 
 
@@ -65,11 +78,11 @@ def _library():
         lib.layer_sync.argtypes = [vp]
         lib.layer_last_hip_error.argtypes = [vp]
         lib.layer_last_hip_error.restype = ctypes.c_char_p
-        lib.layer_rmsnorm.argtypes = [ctypes.POINTER(RmsnormArgs), vp]
-        lib.layer_rmsnorm_backward.argtypes = [ctypes.POINTER(RmsnormGradArgs), vp, vp]
-        lib.layer_linear.argtypes = [ctypes.POINTER(LinearArgs), vp, vp]
-        lib.layer_activation_backward.argtypes = [ctypes.POINTER(ActivationGradArgs), vp, vp]
-        lib.layer_linear_backward.argtypes = [ctypes.POINTER(LinearGradArgs), vp, vp]
+        lib.layer_rmsnorm.argtypes = [vp, vp]
+        lib.layer_rmsnorm_backward.argtypes = [vp, vp, vp]
+        lib.layer_linear.argtypes = [vp, vp, vp]
+        lib.layer_activation_backward.argtypes = [vp, vp, vp]
+        lib.layer_linear_backward.argtypes = [vp, vp, vp]
         _lib = lib
     return _lib
 
@@ -129,55 +142,67 @@ def layer_last_hip_error(plan: LayerPlan) -> str:
     return (_library().layer_last_hip_error(plan.handle) or b"").decode()
 
 
-def _types():
+_codes = {}      # torch dtype -> type code
+_raw_stream = None  # device index -> the current stream's handle
+_current_device = None
+
+
+def _prepare():
+    global _raw_stream, _current_device
     import torch
-    return {torch.float32: LAYER_F32, torch.bfloat16: LAYER_BF16, torch.float8_e4m3fn: LAYER_E4M3}
+    _codes.update({torch.float32: LAYER_F32, torch.bfloat16: LAYER_BF16, torch.float8_e4m3fn: LAYER_E4M3})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _type(name, t, allowed):
-    code = _types().get(t.dtype)
-    if code not in allowed:
-        raise ValueError(f"{name} has dtype {t.dtype}")
-    return code
+def _stream_of(stream, like):
+    return _raw_stream(like.get_device()) if stream is None else _stream_ptr(stream)
 
 
-def _place(name, t, like):
+def _first(name, t, device=None):
+    """Rows and columns of the operand that the others are measured by; it is on `device` (a plan's) or the current one."""
+    if not _codes:
+        _prepare()
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.get_device() != (_current_device() if device is None else device):
+        raise ValueError(f"{name} is on {t.device}, the call's device is another one")
+    return t.shape
 
 
 def _matrix(name, t, rows, cols, like, allowed):
     """(pointer, row stride, type code) of an optional rows x cols matrix with dense rows."""
     if t is None:
-        return None, 0, LAYER_F32
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        return 0, 0, LAYER_F32
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    _place(name, t, like)
-    code = _type(name, t, allowed)
-    if cols > 1 and t.stride(1) != 1:
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    code = _codes.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError(f"{name} must have dense rows (stride 1 along its columns)")
-    return t.data_ptr(), int(t.stride(0)) if rows > 1 else int(cols), code
+    return t.data_ptr(), row if rows > 1 else cols, code
 
 
 def _vector(name, t, n, like, allowed):
     """(pointer, type code) of an optional dense vector of n elements."""
     if t is None:
-        return None, LAYER_F32
-    if t.dim() != 1 or t.shape[0] != n:
+        return 0, LAYER_F32
+    if t.shape != (n,):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
-    _place(name, t, like)
-    code = _type(name, t, allowed)
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    code = _codes.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} has dtype {t.dtype}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr(), code
-
-
-def _two_d(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return int(t.shape[0]), int(t.shape[1])
 
 
 def _activation(name) -> int:
@@ -193,32 +218,34 @@ def layer_rmsnorm(x, weight, out, *, residual=None, sum_out=None, scale=None, ep
     """layer_rmsnorm: out = s / sqrt(mean(s^2) + eps) * weight per row, s = x + residual (kept in sum_out, which
     may be x or residual). x, residual, sum_out: one dtype, bf16 or fp32. weight: bf16 or fp32, or None. out: fp32,
     bf16, or float8_e4m3fn with `scale` (fp32, one value a row): s's norm is then about out * scale[:, None]."""
-    m, n = _two_d("x", x)
-    a = RmsnormArgs(m=m, n=n, eps=eps)
-    _place("x", x, x)
-    a.x, a.ldx, a.type = _matrix("x", x, m, n, x, _STREAM)
-    a.residual, a.ldr, _ = _matrix("residual", residual, m, n, x, (a.type,))
-    a.sum_out, a.lds, _ = _matrix("sum_out", sum_out, m, n, x, (a.type,))
-    a.weight, a.weight_type = _vector("weight", weight, n, x, _STREAM)
-    a.out, a.ldo, a.out_type = _matrix("out", out, m, n, x, (LAYER_F32, LAYER_BF16, LAYER_E4M3))
-    a.scale, _ = _vector("scale", scale, m, x, (LAYER_F32,))
-    _check(_library().layer_rmsnorm(ctypes.byref(a), ctypes.c_void_p(_stream_ptr(stream))), "layer_rmsnorm")
+    m, n = _first("x", x)
+    px, ldx, ty = _matrix("x", x, m, n, x, _STREAM)
+    pr, ldr, _ = _matrix("residual", residual, m, n, x, (ty,))
+    ps, lds, _ = _matrix("sum_out", sum_out, m, n, x, (ty,))
+    pw, wt = _vector("weight", weight, n, x, _STREAM)
+    po, ldo, ot = _matrix("out", out, m, n, x, (LAYER_F32, LAYER_BF16, LAYER_E4M3))
+    pc, _ = _vector("scale", scale, m, x, (LAYER_F32,))
+    a = _RMSNORM(px, pr, pw, ps, po, pc, m, n, ldx, ldr, lds, ldo, ty, wt, ot, eps)
+    st = _library().layer_rmsnorm(a, _stream_of(stream, x))
+    if st:
+        _check(st, "layer_rmsnorm")
 
 
 def layer_rmsnorm_backward(dy, s, weight, dx, dweight, plan: LayerPlan, *, dsum=None, accumulate: bool = False,
                            eps: float = 1e-6, stream=None) -> None:
     """layer_rmsnorm_backward: dx (of the sum s, so of x and of the residual) and dweight (fp32) from dy, at s.
     dsum: the gradient that reaches s from elsewhere, added to dx (dx may be dsum). dx or dweight may be None."""
-    m, n = _two_d("s", s)
-    a = RmsnormGradArgs(m=m, n=n, eps=eps, accumulate=int(bool(accumulate)))
-    a.s, a.lds, a.type = _matrix("s", s, m, n, s, _STREAM)
-    a.dy, a.lddy, a.dy_type = _matrix("dy", dy, m, n, s, _STREAM)
-    a.weight, a.weight_type = _vector("weight", weight, n, s, _STREAM)
-    a.dsum, a.lddsum, _ = _matrix("dsum", dsum, m, n, s, (a.type,))
-    a.dx, a.lddx, _ = _matrix("dx", dx, m, n, s, (a.type,))
-    a.dweight, _ = _vector("dweight", dweight, n, s, (LAYER_F32,))
-    _check(_library().layer_rmsnorm_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
-           "layer_rmsnorm_backward", plan)
+    m, n = _first("s", s, plan.device)
+    ps, lds, ty = _matrix("s", s, m, n, s, _STREAM)
+    pd, lddy, dt = _matrix("dy", dy, m, n, s, _STREAM)
+    pw, wt = _vector("weight", weight, n, s, _STREAM)
+    pu, lddsum, _ = _matrix("dsum", dsum, m, n, s, (ty,))
+    px, lddx, _ = _matrix("dx", dx, m, n, s, (ty,))
+    pg, _ = _vector("dweight", dweight, n, s, (LAYER_F32,))
+    a = _RMSNORM_GRAD(pd, ps, pw, pu, px, pg, m, n, lddy, lds, lddsum, lddx, ty, dt, wt, 1 if accumulate else 0, eps)
+    st = _library().layer_rmsnorm_backward(a, plan.handle, _stream_of(stream, s))
+    if st:
+        _check(st, "layer_rmsnorm_backward", plan)
 
 
 def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "none", residual=None, pre=None, x_scale=None,
@@ -226,51 +253,54 @@ def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "no
     """layer_linear: out = act(x . w^T + bias) + residual, x: m x k, w: n x k, both bf16 or both float8_e4m3fn (then
     with row scales x_scale and w_scale, fp32). out and residual: bf16 or fp32; residual may be out. pre (bf16)
     keeps the activation's argument for layer_activation_backward."""
-    m, k = _two_d("x", x)
-    n, k2 = _two_d("w", w)
+    act = _activation(activation)
+    m, k = _first("x", x, plan.device)
+    n, k2 = _first("w", w, plan.device)
     if k2 != k:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    a = LinearArgs(m=m, n=n, k=k, activation=_activation(activation))
-    a.x, a.ldx, a.in_type = _matrix("x", x, m, k, x, (LAYER_BF16, LAYER_E4M3))
-    a.w, a.ldw, _ = _matrix("w", w, n, k, x, (a.in_type,))
-    a.x_scale, _ = _vector("x_scale", x_scale, m, x, (LAYER_F32,))
-    a.w_scale, _ = _vector("w_scale", w_scale, n, x, (LAYER_F32,))
-    a.bias, a.bias_type = _vector("bias", bias, n, x, _STREAM)
-    a.residual, a.ldr, a.residual_type = _matrix("residual", residual, m, n, x, _STREAM)
-    a.pre, a.ldp, _ = _matrix("pre", pre, m, n, x, (LAYER_BF16,))
-    a.out, a.ldo, a.out_type = _matrix("out", out, m, n, x, _STREAM)
-    _check(_library().layer_linear(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))), "layer_linear", plan)
+    px, ldx, ty = _matrix("x", x, m, k, x, (LAYER_BF16, LAYER_E4M3))
+    pw, ldw, _ = _matrix("w", w, n, k, x, (ty,))
+    pxs, _ = _vector("x_scale", x_scale, m, x, (LAYER_F32,))
+    pws, _ = _vector("w_scale", w_scale, n, x, (LAYER_F32,))
+    pb, bt = _vector("bias", bias, n, x, _STREAM)
+    pr, ldr, rt = _matrix("residual", residual, m, n, x, _STREAM)
+    pz, ldp, _ = _matrix("pre", pre, m, n, x, (LAYER_BF16,))
+    po, ldo, ot = _matrix("out", out, m, n, x, _STREAM)
+    a = _LINEAR(px, pw, pxs, pws, pb, pr, pz, po, m, n, k, ldx, ldw, ldr, ldp, ldo, ty, bt, rt, ot, act, 0)
+    st = _library().layer_linear(a, plan.handle, _stream_of(stream, x))
+    if st:
+        _check(st, "layer_linear", plan)
 
 
 def layer_activation_backward(dout, pre, dpre, plan: LayerPlan, *, activation: str = "none", dbias=None,
                               accumulate: bool = False, stream=None) -> None:
     """layer_activation_backward: dpre = dout * act'(pre) (bf16; dpre may be dout or pre, or None) and dbias = its
     column sums before rounding (fp32, or None). pre may be None with activation "none"."""
-    m, n = _two_d("dout", dout)
-    a = ActivationGradArgs(m=m, n=n, activation=_activation(activation), accumulate=int(bool(accumulate)))
-    a.dout, a.lddo, _ = _matrix("dout", dout, m, n, dout, (LAYER_BF16,))
-    a.pre, a.ldp, _ = _matrix("pre", pre, m, n, dout, (LAYER_BF16,))
-    a.dpre, a.lddp, _ = _matrix("dpre", dpre, m, n, dout, (LAYER_BF16,))
-    a.dbias, _ = _vector("dbias", dbias, n, dout, (LAYER_F32,))
-    _check(_library().layer_activation_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
-           "layer_activation_backward", plan)
+    act = _activation(activation)
+    m, n = _first("dout", dout, plan.device)
+    pd, lddo, _ = _matrix("dout", dout, m, n, dout, (LAYER_BF16,))
+    pz, ldp, _ = _matrix("pre", pre, m, n, dout, (LAYER_BF16,))
+    pg, lddp, _ = _matrix("dpre", dpre, m, n, dout, (LAYER_BF16,))
+    pb, _ = _vector("dbias", dbias, n, dout, (LAYER_F32,))
+    a = _ACTIVATION_GRAD(pd, pz, pg, pb, m, n, lddo, ldp, lddp, act, 1 if accumulate else 0)
+    st = _library().layer_activation_backward(a, plan.handle, _stream_of(stream, dout))
+    if st:
+        _check(st, "layer_activation_backward", plan)
 
 
 def layer_linear_backward(dpre, x, w, plan: LayerPlan, *, dx=None, dw=None, accumulate: bool = False, stream=None) -> None:
     """layer_linear_backward: dx = dpre . w (m x k) and dw = dpre^T . x (n x k; added to dw with accumulate), each
     bf16 or fp32 and optional. dpre, x, w: bf16; x may be None without dw, w may be None without dx."""
-    m, n = _two_d("dpre", dpre)
-    given = w if w is not None else x if x is not None else dx if dx is not None else dw
-    if given is None:
-        raise ValueError("layer_linear_backward needs x for dw and w for dx")
-    k = _two_d("x or w", given)[1]
-    if (dx is not None and w is None) or (dw is not None and x is None):
-        raise ValueError("layer_linear_backward needs x for dw and w for dx")
-    a = LinearGradArgs(m=m, n=n, k=k, accumulate=int(bool(accumulate)))
-    a.dpre, a.lddp, _ = _matrix("dpre", dpre, m, n, dpre, (LAYER_BF16,))
-    a.x, a.ldx, _ = _matrix("x", x, m, k, dpre, (LAYER_BF16,))
-    a.w, a.ldw, _ = _matrix("w", w, n, k, dpre, (LAYER_BF16,))
-    a.dx, a.lddx, a.dx_type = _matrix("dx", dx, m, k, dpre, _STREAM)
-    a.dw, a.lddw, a.dw_type = _matrix("dw", dw, n, k, dpre, _STREAM)
-    _check(_library().layer_linear_backward(ctypes.byref(a), plan.handle, ctypes.c_void_p(_stream_ptr(stream))),
-           "layer_linear_backward", plan)
+    if (dx is None and dw is None) or (dx is not None and w is None) or (dw is not None and x is None):
+        raise ValueError("layer_linear_backward needs dx or dw, w for dx and x for dw")
+    m, n = _first("dpre", dpre, plan.device)
+    k = _first("w", w, plan.device)[1] if w is not None else _first("x", x, plan.device)[1]
+    pd, lddp, _ = _matrix("dpre", dpre, m, n, dpre, (LAYER_BF16,))
+    px, ldx, _ = _matrix("x", x, m, k, dpre, (LAYER_BF16,))
+    pw, ldw, _ = _matrix("w", w, n, k, dpre, (LAYER_BF16,))
+    pdx, lddx, xt = _matrix("dx", dx, m, k, dpre, _STREAM)
+    pdw, lddw, wt = _matrix("dw", dw, n, k, dpre, _STREAM)
+    a = _LINEAR_GRAD(pd, px, pw, pdx, pdw, m, n, k, lddp, ldx, ldw, lddx, lddw, xt, wt, 1 if accumulate else 0, 0)
+    st = _library().layer_linear_backward(a, plan.handle, _stream_of(stream, dpre))
+    if st:
+        _check(st, "layer_linear_backward", plan)

@@ -137,7 +137,7 @@ def test_binding_refuses_host_tensors_and_bad_names():
         ptg.layer_rmsnorm(x[0], None, x)
 
     class Plan:
-        handle = None
+        handle, device = None, 0
     with pytest.raises(ValueError):
         ptg.layer_linear(x, x, x, Plan(), activation="tanh")
     with pytest.raises(ValueError):
