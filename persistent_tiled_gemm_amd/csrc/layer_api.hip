@@ -310,7 +310,7 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p
     k.dy_type = a->dy_type;
     k.weight_type = a->weight_type;
     k.eps = a->eps;
-    // at most 8 x CUs groups of rows of at most 2048, or 2 x CUs of 8192, or CUs
+    // at most 8 x CUs groups of rows of at most 1024, or 2 x CUs of 4096, or CUs
     // of 32768 elements: within the workspace
     rows = ptg::rmsnorm_partial_rows(k.m, k.n, p->cu_count);
     if ((int64_t)rows * a->n > kWsFloats) return GEMM_E_SHAPE;

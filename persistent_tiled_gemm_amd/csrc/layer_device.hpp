@@ -19,6 +19,13 @@ template <> __device__ __forceinline__ f32x8 load8<float>(const float *p) {
 template <> __device__ __forceinline__ f32x8 load8<__bf16>(const __bf16 *p) {
   return __builtin_convertvector(*(const bf16x8 *)p, f32x8);
 }
+// The same eight elements as they lie in memory, and widened.
+template <typename T> struct Raw8;
+typedef f32x8 f32x8_a16 __attribute__((aligned(16)));  // rows of fp32 are 16-byte aligned
+template <> struct Raw8<float> { typedef f32x8_a16 type; };
+template <> struct Raw8<__bf16> { typedef bf16x8 type; };
+__device__ __forceinline__ f32x8 widen(const f32x8_a16 &v) { return v; }
+__device__ __forceinline__ f32x8 widen(const bf16x8 &v) { return __builtin_convertvector(v, f32x8); }
 // The element type named at run time (the weight's or a bias's: read once a row or column).
 __device__ __forceinline__ f32x8 load8_as(const void *p, int32_t type, int64_t i) {
   return type == kTypeF32 ? load8((const float *)p + i) : load8((const __bf16 *)p + i);
@@ -69,6 +76,13 @@ template <> __device__ __forceinline__ void store8_nt<__bf16>(__bf16 *p, const f
 // z = -inf that is NaN where the limit is 0, so the result is selected, not
 // multiplied, there.
 __device__ __forceinline__ float logistic(float t) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-t)); }
+
+template <> __device__ __forceinline__ void store8_nt<e4m3_t>(e4m3_t *p, const f32x8 &v) {
+  typedef __attribute__((ext_vector_type(2))) int i32x2;
+  i32x2 w;
+  store8((e4m3_t *)&w, v);
+  __builtin_nontemporal_store(w, (i32x2 *)p);
+}
 
 // Phi(z), the normal distribution function: erfc by Abramowitz and Stegun's
 // formula 7.1.26 (a polynomial in 1 / (1 + p x) times e^-x^2, absolute error of
