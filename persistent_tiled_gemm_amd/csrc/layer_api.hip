@@ -368,7 +368,7 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
-  if (a->m <= ptg::kRowsMost) {
+  if (ptg::rows_preferred(k, e8)) {
     int64_t tiles = 0;
     if (ptg::rows_partial_floats(k, e8, p->cu_count, &tiles) > kWsFloats || tiles > kArrivals) return GEMM_E_SHAPE;
     hipError_t e = ptg::launch_rows(k, e8, p->d_ws, p->d_arrivals, p->cu_count, s);

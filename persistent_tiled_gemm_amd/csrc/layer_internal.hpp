@@ -78,7 +78,7 @@ hipError_t launch_rmsnorm_backward(const NormGradArgs &a, int cu_count, hipStrea
 hipError_t launch_column_sum(const float *partial, int rows, int32_t n, float *out, int accumulate, hipStream_t s);
 hipError_t launch_activation_backward(const ActGradArgs &a, int row_groups, hipStream_t s);
 
-// The product for few rows (m <= kRowsMost, k-contiguous operands).
+// The product for few rows (m <= kRowsMost, the most that the kernel takes).
 constexpr int32_t kRowsMost = 64;
 struct RowsArgs {
   const void *x, *w;
@@ -87,6 +87,8 @@ struct RowsArgs {
   EpilogueArgs ep;
   int32_t ldx, ldw, m, n, k;
 };
+// Whether a product (k-contiguous operands) runs there rather than as tiles.
+bool rows_preferred(const ProductArgs &p, bool e8);
 // Workspace of a call, floats; *tiles: the arrival counts it uses.
 int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t *tiles);
 hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);

@@ -48,6 +48,13 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
   const uint32_t steps = ((uint32_t)a.k + kStep - 1) / kStep;
   const int32_t s0 = (int32_t)((uint64_t)steps * mine / parts), s1 = (int32_t)((uint64_t)steps * (mine + 1) / parts);
 
+  // Each wave starts part-way into its range and wraps around (a phase from its
+  // place in the grid; the order of a sum depends on that alone). Started at
+  // their first steps, waves whose ranges lie a multiple of 4 KiB apart read the
+  // same few memory channels at a time: 4096 x 16384, one row, 39.7 us.
+  const int32_t count = s1 - s0;
+  const int32_t rot = count > 1 ? (int32_t)((((tile * 8u + wave) * 2654435761u) >> 16) % (uint32_t)count) : 0;
+
   const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)a.ldw * kSize);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x);
   uint32_t w_row[NBLK], x_row[MT];  // byte offsets of the lane's rows; past the matrix: out of range, read as zeros
@@ -62,7 +69,8 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // 16 bytes a lane: chunk `group` of the step's 64
-      const uint32_t at = (uint32_t)(s + u) * 64u + 16u * (uint32_t)group;
+      const int32_t i = s + u + rot;
+      const uint32_t at = (uint32_t)(i < s1 ? i : i - count) * 64u + 16u * (uint32_t)group;
       const bool in = s + u < s1 && at < (uint32_t)a.k * kSize;
 #pragma unroll
       for (int b = 0; b < NBLK; ++b)
@@ -159,19 +167,45 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 }
 
 // The shape of a call: 16-row blocks of x and w a workgroup takes, its waves, and
-// the workgroups that share a tile's k.
+// the workgroups that share a tile's k. Measured over n, k = 512 .. 16384 and 1,
+// 8, 16, 32 and 64 rows in both types:
+//   - a workgroup a CU (two with one block of w), of four waves (eight while
+//     there are fewer than 1024): more waves only shorten each one's run through
+//     memory (16384 x 4096 e4m3, one row: eight 18.6 us, four 15.9);
+//   - x is read again for every 16 NBLK rows of w, from L2, which shows from some
+//     ten rows on (from the first in e4m3, where it is widened again too): two
+//     blocks of w up to 16 rows, four for more, where w is large enough that the
+//     tiles still fill the machine (8192^2 bf16, 32 rows: two blocks 41 us, four
+//     39.8; 16 rows: one block 36, two 33 to 35; e4m3, 8 rows: one 18.7, two 16.9).
+//     Smaller w: one and two (4096^2, 32 rows: two 14.9, four 14.8; 2048^2: two
+//     9.0, one 8.7);
+//   - k is shared until there are as many workgroups as CUs, while a wave keeps
+//     four steps (1024 x 8192, one row: 12.6 us unshared, 9.1 with four).
 struct RowsShape { int mt, nblk, waves, split; };
 static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, bool e8, int cu_count) {
   RowsShape f;
+  const bool large = (int64_t)n * k >= (int64_t)32 << 20;
   f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-  f.nblk = f.mt == 1 ? 1 : 2;
+  f.nblk = m <= 16 ? (large && (e8 || m > 8) ? 2 : 1) : (large ? 4 : 2);
   const int64_t tiles = (n + 16 * f.nblk - 1) / (16 * f.nblk);
+  f.waves = f.nblk == 1 && tiles < 4 * cu_count ? 8 : 4;
   const int64_t steps = (k + (e8 ? 63 : 31)) / (e8 ? 64 : 32);
-  // 16 waves a CU, each with at least eight steps
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>((int64_t)cu_count * 16 / tiles, steps / 8));
-  f.waves = want >= 16 && f.mt < 4 ? 16 : want >= 8 ? 8 : 4;
-  f.split = (int)std::max<int64_t>(1, std::min<int64_t>(want / f.waves, 16));
+  f.split = (int)std::max<int64_t>(1, std::min<int64_t>({cu_count / tiles, steps / (4 * f.waves), 16}));
   return f;
+}
+
+// Few rows run here, except where the tiles are as fast: they read x once for 128
+// rows of w, and reach 3.5 TB/s whatever m. From 17 rows on for w of 32 Mi
+// elements (bf16, 8192^2: 16 rows 33 to 35 us here, 37 as tiles; 32 rows 40 and
+// 38; 64 rows 51 and 40; 4096^2: 64 rows 20 and 22), from 33 in e4m3 (8192^2: 32
+// rows 24 and 29, 64 rows 31 and 31), and from 5 where bf16 rows do not start on
+// 64-byte lines (5000^2: one row 21.8 and 23.0, 8 rows 25.5 and 23.8, 64 44 and 29).
+bool rows_preferred(const ProductArgs &p, bool e8) {
+  if (p.m > kRowsMost) return false;
+  const int64_t size = (int64_t)p.n * p.k;
+  if (e8) return p.m <= 32 || size < (int64_t)32 << 20;
+  if (p.m > 4 && p.ldb % 32 != 0 && size >= (int64_t)16 << 20) return false;
+  return p.m <= 16 || size < (int64_t)32 << 20;
 }
 
 int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t *tiles) {
@@ -180,18 +214,16 @@ int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t
   return *tiles * f.split * f.mt * f.nblk * 256;
 }
 
-template <bool E8, int MT, int NBLK, int U>
-static void rows_waves(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
-  if (f.waves == 4) hipLaunchKernelGGL((ptg_rows_kernel<E8, MT, NBLK, 4, U>), grid, dim3(256), 0, s, a);
-  else if (f.waves == 8) hipLaunchKernelGGL((ptg_rows_kernel<E8, MT, NBLK, 8, U>), grid, dim3(512), 0, s, a);
-  else if constexpr (MT < 4) hipLaunchKernelGGL((ptg_rows_kernel<E8, MT, NBLK, 16, U>), grid, dim3(1024), 0, s, a);
-}
-
 template <bool E8>
 static void rows_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
-  if (f.mt == 1) rows_waves<E8, 1, 1, 4>(f, a, grid, s);
-  else if (f.mt == 2) rows_waves<E8, 2, 2, 2>(f, a, grid, s);
-  else rows_waves<E8, 4, 2, 2>(f, a, grid, s);
+  const dim3 block(64 * f.waves);
+  if (f.mt == 1 && f.nblk == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 1, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1 && f.nblk == 1) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 1, 8, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 2, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 2 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 2, 2, 4, 2>), grid, block, 0, s, a);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 2, 4, 4, 2>), grid, block, 0, s, a);
+  else if (f.nblk == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 4, 2, 4, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((ptg_rows_kernel<E8, 4, 4, 4, 2>), grid, block, 0, s, a);
 }
 
 hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
