@@ -57,6 +57,11 @@ template <> __device__ __forceinline__ void store8<e4m3_t>(e4m3_t *p, const f32x
   *(int2 *)p = make_int2(lo, hi);
 }
 
+// z p for p in [0, 1] that vanishes as z goes to -infinity: the most negative
+// value stands in for -infinity, whose product with p = 0 would be NaN. (A NaN z
+// has a NaN p.)
+__device__ __forceinline__ float times_p(float z, float p) { return fmaxf(z, -3.402823466e38f) * p; }
+
 // exp through the hardware's 2^x: relative error about 2^-22 over the range the
 // activations use it on (the argument's own rounding, |t| 2^-24, dominates).
 __device__ __forceinline__ float exp_f32(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504088896341f); }
@@ -72,9 +77,7 @@ template <> __device__ __forceinline__ void store8_nt<__bf16>(__bf16 *p, const f
 }
 
 // Activations in fp32. The logistic function is 1 / (1 + e^-t): e^-t that
-// overflows to infinity gives 0, and the products with z below are then 0 z; for
-// z = -inf that is NaN where the limit is 0, so the result is selected, not
-// multiplied, there.
+// overflows to infinity gives 0.
 __device__ __forceinline__ float logistic(float t) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-t)); }
 
 template <> __device__ __forceinline__ void store8_nt<e4m3_t>(e4m3_t *p, const f32x8 &v) {
@@ -102,42 +105,29 @@ static constexpr float kGeluA = 0.044715f;
 __device__ __forceinline__ float act_f32(int32_t act, float z) {
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
-    case kActGelu: {
-      const float p = normal_cdf(z);
-      return p == 0.0f ? 0.0f : z * p;
-    }
-    case kActGeluTanh: {
-      // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
-      const float p = logistic(2.0f * kGeluC * (z + kGeluA * z * z * z));
-      return p == 0.0f ? 0.0f : z * p;
-    }
-    case kActSilu: {
-      const float p = logistic(z);
-      return p == 0.0f ? 0.0f : z * p;
-    }
+    case kActGelu: return times_p(z, normal_cdf(z));
+    // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+    case kActGeluTanh: return times_p(z, logistic(z * (2.0f * kGeluC + 2.0f * kGeluC * kGeluA * (z * z))));
+    case kActSilu: return times_p(z, logistic(z));
     default: return z;
   }
 }
 
-// act_f32 of eight values, the activation decided once.
-__device__ __forceinline__ void act8(int32_t act, f32x8 &v) {
+// act_f32 of two rows' eight values, the activation decided once.
+template <int ACT>
+__device__ __forceinline__ void act16_as(f32x8 &a, f32x8 &b) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    a[e] = act_f32(ACT, a[e]);
+    b[e] = act_f32(ACT, b[e]);
+  }
+}
+__device__ __forceinline__ void act16(int32_t act, f32x8 &a, f32x8 &b) {
   switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActRelu, v[e]);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActGelu, v[e]);
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActGeluTanh, v[e]);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = act_f32(kActSilu, v[e]);
-      break;
+    case kActRelu: act16_as<kActRelu>(a, b); break;
+    case kActGelu: act16_as<kActGelu>(a, b); break;
+    case kActGeluTanh: act16_as<kActGeluTanh>(a, b); break;
+    case kActSilu: act16_as<kActSilu>(a, b); break;
     default: break;
   }
 }

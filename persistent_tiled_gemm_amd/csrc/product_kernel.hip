@@ -59,21 +59,47 @@ __device__ __forceinline__ ColumnTerms column_terms(const EpilogueArgs &e, int32
   return t;
 }
 
-// z of row m, columns n .. n + 7, to out (and pre).
-template <bool E8>
-__device__ __forceinline__ void finish8(const EpilogueArgs &e, int64_t m, int32_t n, f32x8 z, const ColumnTerms &col, const RowTerms &row) {
-  if constexpr (E8) z = z * row.scale * col.scale;
-  z += col.bias;
-  if (e.pre) store8_nt((__bf16 *)e.pre + m * e.ldp + n, z);
-  act8(e.act, z);
-  if (e.residual) {
-    if (e.residual_type == kTypeF32)
-      z += __builtin_shufflevector(__builtin_bit_cast(f32x4, row.lo), __builtin_bit_cast(f32x4, row.hi), 0, 1, 2, 3, 4, 5, 6, 7);
-    else
-      z += __builtin_convertvector(__builtin_bit_cast(bf16x8, row.lo), f32x8);
+// z of rows m and (where `both`) m + step, columns n .. n + 7, to out (and pre).
+// TERMS: there is a residual or a row scale.
+template <bool E8, bool TERMS>
+__device__ __forceinline__ void finish_rows(const EpilogueArgs &e, int64_t m, int32_t step, bool both, int32_t n, f32x8 z0, f32x8 z1,
+                                            const ColumnTerms &col, const RowTerms &t0, const RowTerms &t1) {
+  if constexpr (E8) {
+    if constexpr (TERMS) {
+      z0 *= t0.scale;
+      z1 *= t1.scale;
+    }
+    z0 *= col.scale;
+    z1 *= col.scale;
   }
-  if (e.out_type == kTypeF32) store8_nt((float *)e.out + m * e.ldo + n, z);
-  else store8_nt((__bf16 *)e.out + m * e.ldo + n, z);
+  z0 += col.bias;
+  z1 += col.bias;
+  if (e.pre) {
+    __bf16 *p = (__bf16 *)e.pre + m * e.ldp + n;
+    store8_nt(p, z0);
+    if (both) store8_nt(p + step * e.ldp, z1);
+  }
+  act16(e.act, z0, z1);
+  if constexpr (TERMS) {
+    if (e.residual) {
+      if (e.residual_type == kTypeF32) {
+        z0 += __builtin_shufflevector(__builtin_bit_cast(f32x4, t0.lo), __builtin_bit_cast(f32x4, t0.hi), 0, 1, 2, 3, 4, 5, 6, 7);
+        z1 += __builtin_shufflevector(__builtin_bit_cast(f32x4, t1.lo), __builtin_bit_cast(f32x4, t1.hi), 0, 1, 2, 3, 4, 5, 6, 7);
+      } else {
+        z0 += __builtin_convertvector(__builtin_bit_cast(bf16x8, t0.lo), f32x8);
+        z1 += __builtin_convertvector(__builtin_bit_cast(bf16x8, t1.lo), f32x8);
+      }
+    }
+  }
+  if (e.out_type == kTypeF32) {
+    float *p = (float *)e.out + m * e.ldo + n;
+    store8_nt(p, z0);
+    if (both) store8_nt(p + step * e.ldo, z1);
+  } else {
+    __bf16 *p = (__bf16 *)e.out + m * e.ldo + n;
+    store8_nt(p, z0);
+    if (both) store8_nt(p + step * e.ldo, z1);
+  }
 }
 
 template <int FORM>
@@ -90,50 +116,68 @@ struct ProductOp {
   // 16)) to memory, first row m_base, first column n_base. A lane takes eight
   // consecutive columns, so a bf16 row leaves as whole 16-byte stores (256
   // contiguous bytes a row for the 256 x 256 tile) and the columns' bias and
-  // scale stay in registers. A lane's rows follow each other through one copy of
-  // the code (five activations of eight values: unrolled over the rows they
-  // outgrow the instruction cache and the registers), with the residuals and row
-  // scales of the next kAhead rows under way.
+  // scale stay in registers. A lane's rows follow each other two at a time
+  // through one copy of the code (five activations of 16 values: unrolled over all
+  // rows they outgrow the instruction cache and the registers). One wave a SIMD
+  // hides nothing by itself: the next two rows' sums are read from LDS, and with
+  // residuals or row scales the next four rows' are asked for, before two rows are
+  // finished.
   // slot: a K-chunk's sums go there unfinished, rows STRIDE floats apart.
   template <int RP, int ROW_B, int STRIDE>
   static __device__ __forceinline__ void flush(const Args &, const unsigned char *wl, uint32_t lane, int32_t m_base, int32_t n_base,
                                                int32_t M, int32_t N, float *slot) {
-    constexpr int LPR = ROW_B / 32, RPI = 64 / LPR, kRows = RP / RPI, kAhead = 4;
-    static_assert(kRows >= kAhead && (LPR == 16 || LPR == 8), "epilogue");
+    constexpr int LPR = ROW_B / 32, RPI = 64 / LPR, kRows = RP / RPI;
+    static_assert(kRows % 2 == 0 && (LPR == 16 || LPR == 8), "epilogue");
     const EpilogueArgs e = epilogue_args();
     // the lane's offsets are computed here, not kept over the main loop
     asm volatile("" : "+v"(lane));
     const uint32_t q = lane % LPR, r0 = lane / LPR;
     const int32_t n = n_base + (int32_t)(8u * q);
-    if (n >= N) return;
-    const ColumnTerms col = column_terms<E8>(e, n);
-    auto ask = [&](int i) -> RowTerms {
-      const int64_t m = (int64_t)m_base + (uint32_t)(i * RPI) + r0;
-      if (slot == nullptr && i < kRows && m < M) return row_terms<E8>(e, m, n);
-      return RowTerms{{0, 0, 0, 0}, {0, 0, 0, 0}, 1.0f};
-    };
-    RowTerms ahead[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) ahead[u] = ask(u);
-    // 16 lanes a row (32 chunks): lanes 8..15 read their odd chunk first, which
-    // spreads a read's 16 chunks over all banks; 8 lanes a row do so by the swizzle
-    const uint32_t odd = LPR == 16 ? q >> 3 : 0u;
-#pragma unroll 1
-    for (int i = 0; i < kRows; ++i) {
+    const int32_t left = M - m_base - (int32_t)r0;  // rows from the lane's first on
+    if (n >= N || left <= 0) return;
+    const int rows = left >= RP ? kRows : (left + RPI - 1) / RPI;  // of the lane's, how many exist
+    auto staged = [&](int i) -> f32x8 {
       const uint32_t row = (uint32_t)(i * RPI) + r0;
-      const int64_t m = (int64_t)m_base + row;
-      const f32x4 v0 = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + odd) ^ (row & 15u)) << 4));
-      const f32x4 v1 = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + 1u - odd) ^ (row & 15u)) << 4));
-      const f32x4 lo = odd ? v1 : v0, hi = odd ? v0 : v1;
-      const f32x8 z = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      const RowTerms now = ahead[0];
-#pragma unroll
-      for (int u = 0; u + 1 < kAhead; ++u) ahead[u] = ahead[u + 1];
-      ahead[kAhead - 1] = ask(i + kAhead);
-      if (m >= M) continue;
-      if (slot) store8(slot + row * STRIDE + 8u * q, z);
-      else finish8<E8>(e, m, n, z, col, now);
+      const f32x4 lo = *(const f32x4 *)(wl + row * ROW_B + (((2u * q) ^ (row & 15u)) << 4));
+      const f32x4 hi = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + 1u) ^ (row & 15u)) << 4));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    if (slot) {
+#pragma unroll 4
+      for (int i = 0; i < rows; ++i) store8(slot + ((uint32_t)(i * RPI) + r0) * STRIDE + 8u * q, staged(i));
+      return;
     }
+    const ColumnTerms col = column_terms<E8>(e, n);
+    const int64_t m0 = (int64_t)m_base + r0;
+    auto finish = [&](auto terms) {
+      constexpr bool kTerms = decltype(terms)::value;
+      const RowTerms none = {{0, 0, 0, 0}, {0, 0, 0, 0}, 1.0f};
+      auto ask = [&](int i) -> RowTerms { return i < rows ? row_terms<E8>(e, m0 + i * RPI, n) : none; };
+      RowTerms t[4] = {none, none, none, none};
+      if constexpr (kTerms) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t[u] = ask(u);
+      }
+      f32x8 z0 = staged(0), z1 = staged(1);
+#pragma unroll 1
+      for (int i = 0; i < rows; i += 2) {
+        const f32x8 a0 = z0, a1 = z1;
+        if (i + 2 < kRows) {
+          z0 = staged(i + 2);
+          z1 = staged(i + 3);
+        }
+        const RowTerms t0 = t[0], t1 = t[1];
+        if constexpr (kTerms) {
+          t[0] = t[2];
+          t[1] = t[3];
+          t[2] = ask(i + 4);
+          t[3] = ask(i + 5);
+        }
+        finish_rows<E8, kTerms>(e, m0 + i * RPI, RPI, i + 1 < rows, n, a0, a1, col, t0, t1);
+      }
+    };
+    if (e.residual || (E8 && e.row_scale)) finish(std::true_type{});
+    else finish(std::false_type{});
   }
 };
 
@@ -164,7 +208,7 @@ __global__ __launch_bounds__(256) void ptg_product_reduce_kernel(const ReduceArg
   const float *p = a.ws + (size_t)tile * a.chunks * (EDGE * EDGE) + r * EDGE + 8u * q;
   f32x8 z = load8(p);
   for (int32_t c = 1; c < a.chunks; ++c) z += load8(p + (size_t)c * (EDGE * EDGE));
-  finish8<E8>(a.ep, m, n, z, col, row);
+  finish_rows<E8, true>(a.ep, m, 0, false, n, z, z, col, row, row);
 }
 
 template <int EDGE>
