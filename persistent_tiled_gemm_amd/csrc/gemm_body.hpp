@@ -325,7 +325,7 @@ __device__ __forceinline__ uint32_t claim_next(const KernelArgs &a, uint32_t xcc
 template <bool BT_>
 struct PlainOp {
   struct Args {};
-  static constexpr bool AT = false, BT = BT_, E8 = false, kPlain = true;
+  static constexpr bool AT = false, BT = BT_, E8 = false, kPlain = true, kWide = false;
   template <int EDGE> using Tile = typename TileCfg<EDGE>::type;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &pb, const Args &) { return pb.K; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &pb, const Args &) { return BT_ ? pb.K : pb.N; }
@@ -335,6 +335,9 @@ template <int BM, int BN, int MODE, bool GROUPED, class OP>
 __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename OP::Args &op) {
   using CF = typename OP::template Tile<BM>;
   constexpr bool AT = OP::AT, BT = OP::BT, E8 = OP::E8;
+  // K-contiguous operands staged two k-steps (128 bytes of a row) at a time
+  constexpr bool WA = OP::kWide && !AT, WB = OP::kWide && BT, WIDE = WA || WB;
+  static_assert(!WIDE || CF::MB == 16, "wide stages are read in 16 x 16 blocks");
   static_assert(!E8 || (!AT && BT && CF::MB == 16), "e4m3 operands are both K-contiguous, in 16 x 16 blocks");
   static_assert(CF::BM_ == BM && CF::BN_ == BN, "config");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::LDS];  // the stage ring
@@ -556,8 +559,10 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     const int32_t nk = (K + CF::BK - 1) / CF::BK;
     const int32_t full = K / CF::BK;  // k-steps with no K tail
     // k-steps [kb, ke) of this unit: all of them, or an even share for a K-chunk
-    const int32_t kb = split ? (int32_t)((uint32_t)nk * chunk / (uint32_t)args.split_chunks) : 0;
-    const int32_t ke = split ? (int32_t)((uint32_t)nk * (chunk + 1u) / (uint32_t)args.split_chunks) : nk;
+    // (wide stages: an even k-step begins every range)
+    const uint32_t nr = WIDE ? (uint32_t)(nk + 1) / 2u : (uint32_t)nk;
+    const int32_t kb = split ? (int32_t)(nr * chunk / (uint32_t)args.split_chunks) * (WIDE ? 2 : 1) : 0;
+    const int32_t ke = split ? min(nk, (int32_t)(nr * (chunk + 1u) / (uint32_t)args.split_chunks) * (WIDE ? 2 : 1)) : nk;
     // K order of the unit: logical k-step kt (kb <= kt < ke) reads physical k-step
     // kb + ((kt - kb + rot) mod (ke - kb)). When every workgroup walks K from the
     // same end, all concurrent operand reads of the machine share their low
@@ -568,10 +573,22 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     // every scheduler still gives bitwise the same C). Off when K has a partial
     // k-step (the K-tail masking assumes that step comes last).
     const int32_t nsteps = ke - kb;
-    const int32_t rot = K % CF::BK == 0 ? k_rotation_of(args, rot_key, nsteps) : 0;
+    // Wide stages rotate their whole pairs of k-steps; a pair that K ends in keeps
+    // its place at the end.
+    const int32_t npf = WIDE ? (min(ke, K / (2 * CF::BK) * 2) - kb) / 2 : 0;  // whole pairs
+    const int32_t rot = WIDE ? (npf > 1 ? k_rotation_of(args, rot_key, npf) : 0)
+                             : K % CF::BK == 0 ? k_rotation_of(args, rot_key, nsteps) : 0;
     // physical k-step of logical k-step kt (logical steps past ke read zeros
     // through a dead resource, whatever their base)
-    auto phys = [&](int32_t kt) -> int32_t { return kt + rot >= ke ? kt + rot - nsteps : kt + rot; };
+    auto phys = [&](int32_t kt) -> int32_t {
+      if constexpr (WIDE) {
+        // (selects, not branches: a branch holds the wave until its MFMAs drain)
+        const int32_t i = kt - kb, p = i >> 1, t = p + rot, w = t - npf;
+        const int32_t q = w >= 0 ? w : t, f = p < npf ? q : p;
+        return kb + 2 * f + (i & 1);
+      }
+      return kt + rot >= ke ? kt + rot - nsteps : kt + rot;
+    };
 
     // voffset of load j of a k-step with no partial K: chunks outside the matrix
     // (row / column edges) read as zero via kBufOob. The A swizzle of load j's
@@ -623,6 +640,36 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       return j < CF::A_LOADS ? (uint32_t)CF::a_off(st) + (uint32_t)(j * CF::NW + (int)wave) * 1024u
                              : (uint32_t)CF::b_off(st) + (uint32_t)((j - CF::A_LOADS) * CF::NW + (int)wave) * 1024u;
     };
+    // Wide loads: a wave-load moves eight rows of 128 bytes (whole cache lines, where
+    // a k-step alone takes 64 bytes of 16 rows: from L2, 256 CUs at once, 103 ->
+    // 133 GB/s a CU, and with rows that do not start on 64-byte lines 46 -> 99).
+    // Chunk c of row r of a pair's 128-byte rows sits in slot c ^ ((r >> 1) & 7). Load j < A_LOADS 2 of a pair is A's,
+    // the rest B's; rows step by 32 a load, so a lane's chunk is the same for all.
+    constexpr int kWideA = WA ? 2 * CF::A_LOADS : 0, kWideB = WB ? 2 * CF::B_LOADS : 0, kWide = kWideA + kWideB;
+    // Rows past the matrix are out of the resource's range (its record count is the
+    // bytes of the rows there are), so an offset is one per-lane base plus a
+    // wave-uniform step; in the pair that K ends in, the bases of chunks past K are
+    // out of range themselves.
+    const uint32_t w_row0 = wave * 8u + (lane >> 3);
+    const uint32_t w_chunk = (lane & 7u) ^ ((w_row0 >> 1) & 7u);
+    const uint32_t w_base_a = w_row0 * (uint32_t)lda * 2u + w_chunk * 16u, w_base_b = w_row0 * (uint32_t)ldb * 2u + w_chunk * 16u;
+    const uint32_t w_records_a = (uint32_t)min(m_left, BM) * (uint32_t)lda * 2u, w_records_b = (uint32_t)min(n_left, BN) * (uint32_t)ldb * 2u;
+    auto wide_rsrc = [&](bool a, int32_t kt) -> i32x4 {  // of the pair that logical k-step kt begins
+      i32x4 r = make_rsrc_words(a ? a_kstep(phys(kt)) : b_kstep(phys(kt)));
+      r[2] = kt < ke ? (int32_t)(a ? w_records_a : w_records_b) : 0;
+      return r;
+    };
+    auto wide_voff = [&](int j) -> uint32_t {
+      return j < kWideA ? w_base_a + (uint32_t)(8 * CF::NW * j) * (uint32_t)lda * 2u
+                        : w_base_b + (uint32_t)(8 * CF::NW * (j - kWideA)) * (uint32_t)ldb * 2u;
+    };
+    auto wide_voff_tail = [&](int j, int32_t pair_kt) -> uint32_t {
+      return pair_kt * CF::BK + (int32_t)(w_chunk * 8u) >= K ? kBufOob : wide_voff(j);
+    };
+    auto wide_dst = [&](int j, int st) -> uint32_t {
+      return j < kWideA ? (uint32_t)CF::a_off(st & ~1) + (uint32_t)(j * CF::NW + (int)wave) * 1024u
+                        : (uint32_t)CF::b_off(st & ~1) + (uint32_t)((j - kWideA) * CF::NW + (int)wave) * 1024u;
+    };
     // all loads of k-step kt into stage dst, back to back (prologue)
     auto issue_all = [&](int st, int32_t kt) {
       const i32x4 ra = make_rsrc_words(a_kstep(phys(kt)), kt < ke);
@@ -630,7 +677,14 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       const uint32_t base = lds_addr(smem);
 #pragma unroll
       for (int j = 0; j < CF::A_LOADS + CF::B_LOADS; ++j)
-        load16_to_lds(j < CF::A_LOADS ? ra : rb, base + load_dst(j, st), load_voff(j, kt));
+        if (!(j < CF::A_LOADS ? WA : WB)) load16_to_lds(j < CF::A_LOADS ? ra : rb, base + load_dst(j, st), load_voff(j, kt));
+    };
+    // the wide loads of the pair that begins at kt
+    auto issue_pair = [&](int st, int32_t kt) {
+      const i32x4 ra = wide_rsrc(true, kt), rb = wide_rsrc(false, kt);
+      const uint32_t base = lds_addr(smem);
+#pragma unroll
+      for (int j = 0; j < kWide; ++j) load16_to_lds(j < kWideA ? ra : rb, base + wide_dst(j, st), wide_voff_tail(j, phys(kt)));
     };
 
     // fragment read offsets (bytes inside a stage). An MFMA operand is 8
@@ -641,8 +695,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
 #pragma unroll
     for (int mi = 0; mi < CF::MI; ++mi) {
       const uint32_t row = wm * CF::WM + mi * CF::MB + (lane % CF::MB);
-      off_a[mi] = row * (uint32_t)CF::A_ROW;
-      swa[mi] = swz_a<CF::MB>(row) ^ (lane / CF::MB);
+      off_a[mi] = row * (uint32_t)CF::A_ROW * (WA ? 2u : 1u);
+      swa[mi] = (WA ? (row >> 1) & 7u : swz_a<CF::MB>(row)) ^ (lane / CF::MB);
     }
     if constexpr (AT) {  // A read like B below: transposing reads of its k rows
       const uint32_t q = lane >> 4, i = lane & 15u;
@@ -661,8 +715,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
 #pragma unroll
       for (int ni = 0; ni < CF::NI; ++ni) {
         const uint32_t row = wn * CF::WN + ni * CF::MB + (lane % CF::MB);
-        off_b[ni] = row * (uint32_t)CF::A_ROW;
-        swb[ni] = swz_a<CF::MB>(row) ^ (lane / CF::MB);
+        off_b[ni] = row * (uint32_t)CF::A_ROW * (WB ? 2u : 1u);
+        swb[ni] = (WB ? (row >> 1) & 7u : swz_a<CF::MB>(row)) ^ (lane / CF::MB);
       }
     } else {
       // 32 x 32 blocks: lane group q = lane / 16 covers k half q / 2 and column
@@ -827,9 +881,16 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // wave finished reading it before the barrier that ended step kt-1), and
         // must have landed by the barrier that ends step kt+2: between two and
         // three k-steps in flight.
+        // loads of a k-step that are not wide, and of a pair of k-steps
+        constexpr int kNarrow = (WA ? 0 : CF::A_LOADS) + (WB ? 0 : CF::B_LOADS), kPair = kWide + 2 * kNarrow;
 #pragma unroll
-        for (int q = 0; q < NST; ++q) issue_all(q, kb + q);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");  // stages 0 and 1 landed
+        for (int q = 0; q < NST; ++q) {
+          if constexpr (WIDE) {
+            if ((q & 1) == 0) issue_pair(q, kb + q);
+          }
+          issue_all(q, kb + q);
+        }
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST / 2 - 1) * kPair) : "memory");  // stages 0 and 1 landed
         wg_barrier();
         frag a0[CF::MI], b0[CF::NI], a1[CF::MI], b1[CF::NI];
         // e4m3: the k-step's fragments as they lie in LDS, 16 values a lane: lane
@@ -838,10 +899,13 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // one's (the same k in A and B, whatever its order). a0, b0 hold the first
         // half as bf16, a1, b1 the second.
         i32x4 raw[CF::MI + CF::NI];
-        auto read_raw = [&](int st, int q) {
-          const unsigned char *row = q < CF::MI ? smem + CF::a_off(st) + off_a[q < CF::MI ? q : 0]
-                                                : smem + CF::b_off(st) + off_b[q < CF::MI ? 0 : q - CF::MI];
-          raw[q] = *(const i32x4 *)(row + ((q < CF::MI ? swa[q < CF::MI ? q : 0] : swb[q < CF::MI ? 0 : q - CF::MI]) << 4));
+        // odd: the stage is the second of its pair (chunks 4 to 7 of the wide rows)
+        auto read_raw = [&](int st, bool odd, int q) {
+          const int sp = WIDE ? st & ~1 : st;
+          const unsigned char *row = q < CF::MI ? smem + CF::a_off(sp) + off_a[q < CF::MI ? q : 0]
+                                                : smem + CF::b_off(sp) + off_b[q < CF::MI ? 0 : q - CF::MI];
+          const uint32_t sw = q < CF::MI ? swa[q < CF::MI ? q : 0] : swb[q < CF::MI ? 0 : q - CF::MI];
+          raw[q] = *(const i32x4 *)(row + ((sw ^ (WIDE && odd ? 4u : 0u)) << 4));
         };
         // two of the chunk's values (pair p of half h) to their fragment
         auto widen = [&](int q, int h, int p, frag(&af)[CF::MI], frag(&bfr)[CF::NI]) {
@@ -853,7 +917,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         };
         if constexpr (E8) {
 #pragma unroll
-          for (int q = 0; q < CF::MI + CF::NI; ++q) read_raw(0, q);
+          for (int q = 0; q < CF::MI + CF::NI; ++q) read_raw(0, false, q);
 #pragma unroll
           for (int c = 0; c < 4 * (CF::MI + CF::NI); ++c) widen(c >> 2, 0, c & 3, a0, b0);
         } else {
@@ -885,21 +949,63 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         uint32_t voff_fast[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) voff_fast[j] = load_voff_edge(j);
+        // the loads that go out at place `at` of `places` in a k-step: the narrow ones
+        // of step kt + NST, and in the second step of a pair, whose fragments have
+        // all been read, the wide ones of the pair NST steps after it. Those must
+        // have landed when the next even step but NST - 4 ends: they go out in the
+        // first half of theirs. (Waits below: all loads up to that step's narrow ones,
+        // which follow its wide ones, may be in flight.)
+        auto step_loads = [&](auto fast, bool odd, int32_t kt, int st, int at, int places, const i32x4 &ra, const i32x4 &rb, const i32x4 &wa,
+                              const i32x4 &wb, int32_t wide_kt) {
+          const uint32_t lbase = lds_addr(smem);
+          if constexpr (WIDE) {
+            const int every = places / (2 * kWide), j = at / every;
+            if (odd && at % every == 0 && j < kWide)
+              load16_to_lds(j < kWideA ? wa : wb, lbase + wide_dst(j, st),
+                            decltype(fast)::value ? wide_voff(j) : wide_voff_tail(j, wide_kt));
+            if constexpr (kNarrow > 0) {
+              const int gap = places / (2 * kNarrow), k = (at - places / 2) / gap + (WA ? CF::A_LOADS : 0);
+              if (at >= places / 2 && (at - places / 2) % gap == 0)
+                load16_to_lds(k < CF::A_LOADS ? ra : rb, lbase + load_dst(k, st), decltype(fast)::value ? voff_fast[k] : load_voff(k, kt + NST));
+            }
+          } else {
+            // (a spacing of eight, which lines the loads up with the rows of the
+            // accumulator grid, made the compiler give up unrolling the step)
+            const int first = places >= 64 ? 3 : 1, every = places >= 64 ? 7 : places / kLoads, j = (at - first) / every;
+            if (at >= first && (at - first) % every == 0 && j < kLoads)
+              load16_to_lds(j < CF::A_LOADS ? ra : rb, lbase + load_dst(j, st), decltype(fast)::value ? voff_fast[j] : load_voff(j, kt + NST));
+          }
+        };
+        // loads that may be in flight when a k-step ends. Wide: an even step s needs the
+        // pair s + 2, whose loads went out in step s + 3 - NST, before that step's narrow ones
+        auto step_wait = [&](bool odd) {
+          if constexpr (!WIDE) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
+          } else if (odd) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST / 2 - 1) * kPair) : "memory");
+          } else {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST / 2 - 2) * kPair + 2 * kNarrow) : "memory");
+          }
+        };
         // FAST: the k-step's loads read whole 32-deep slices (or lie past the
         // unit and read zeros through the resource), so the offsets above serve;
         // otherwise they are computed with the K-tail test.
         // st: the stage step kt's fragments came from, (kt - kb) mod 4; a compile-time
         // constant in the four-step trips, so every LDS address of the step is a
         // per-lane base plus an immediate offset
-        auto step = [&](auto fast, int32_t kt, int st, const frag(&ac)[CF::MI], const frag(&bc)[CF::NI],
+        // odd: the second step of a pair (known at compile time)
+        auto step = [&](auto fast, bool odd, int32_t kt, int st, const frag(&ac)[CF::MI], const frag(&bc)[CF::NI],
                         frag(&an)[CF::MI], frag(&bn)[CF::NI]) {
           const int rst = (st + 1) & kMask;
-          const unsigned char *sa = smem + CF::a_off(rst);
-          const unsigned char *sb = smem + CF::b_off(rst);
+          const unsigned char *sa = smem + CF::a_off(WA ? rst & ~1 : rst);
+          const unsigned char *sb = smem + CF::b_off(WB ? rst & ~1 : rst);
+          const uint32_t xa = WA && !odd ? 4u : 0u, xb = WB && !odd ? 4u : 0u;  // the step read is the pair's second when this is its first
           const int32_t kt_load = kt + NST;
           const i32x4 ra = make_rsrc_words(a_kstep(phys(kt_load)), kt_load < ke);
           const i32x4 rb = make_rsrc_words(b_kstep(phys(kt_load)), kt_load < ke);
-          const uint32_t lbase = lds_addr(smem);
+          // (st is its pair's second stage: the pair NST steps on begins at kt - 1 + NST)
+          const int32_t pair_load = phys(kt + NST - 1);
+          const i32x4 wa = WIDE && odd ? wide_rsrc(true, kt + NST - 1) : ra, wb = WIDE && odd ? wide_rsrc(false, kt + NST - 1) : rb;
           i16x4 alo[CF::MI], lo[CF::NI];
           auto read = [&](int r) {
             if (r < kReadsA) {
@@ -911,10 +1017,10 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
                   an[r >> 1] = join(alo[r >> 1], __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(pa0 + 4 * CF::B_ROW)));
                 }
               } else {
-                an[r] = *(const bf16x8 *)(sa + off_a[r] + (swa[r] << 4));
+                an[r] = *(const bf16x8 *)(sa + off_a[r] + ((swa[r] ^ xa) << 4));
               }
             } else if constexpr (BT) {
-              bn[r - kReadsA] = *(const bf16x8 *)(sb + off_b[r - kReadsA] + (swb[r - kReadsA] << 4));
+              bn[r - kReadsA] = *(const bf16x8 *)(sb + off_b[r - kReadsA] + ((swb[r - kReadsA] ^ xb) << 4));
             } else {
               const int ni = (r - kReadsA) >> 1;
               const unsigned char *pb0 = sb + off_b[ni];
@@ -925,23 +1031,16 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
               }
             }
           };
-          // (a spacing of eight, which lines the loads up with the rows of the
-          // accumulator grid, made the compiler give up unrolling the step)
-          constexpr int kLoadFirst = kMfma >= 64 ? 3 : 1, kLoadEvery = kMfma >= 64 ? 7 : kMfma / kLoads;
-          static_assert(kLoadFirst + kLoadEvery * (kLoads - 1) < kMfma && (kReads <= kMfma), "load placement");
+          static_assert(kReads <= kMfma, "read placement");
 #pragma unroll
           for (int i = 0; i < kMfma; ++i) {
             mfma16(i / CF::NI, i % CF::NI, ac[i / CF::NI], bc[i % CF::NI]);
             if (i < kReads) read(i);
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-              if (kLoadFirst + kLoadEvery * j == i)
-                load16_to_lds(j < CF::A_LOADS ? ra : rb, lbase + load_dst(j, st),
-                              decltype(fast)::value ? voff_fast[j] : load_voff(j, kt_load));
+            step_loads(fast, odd, kt, st, i, kMfma, ra, rb, wa, wb, pair_load);
           }
           if constexpr (OP::kPlain) wait_lds_all();
           else __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), known to the compiler: no waits for these reads in the next step
-          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
+          step_wait(odd);
           wg_barrier();
         };
         // The e4m3 k-step: the first half's MFMAs with the second half's widening
@@ -949,50 +1048,46 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // widening of their first half (64 conversions to 64 MFMAs in the 256 x 256
         // tile: they issue in the MFMAs' shadow). The conversions are pinned where
         // they stand; left free, they gather at the ends of the halves.
-        auto step8 = [&](auto fast, int32_t kt, int st) {
+        auto step8 = [&](auto fast, bool odd, int32_t kt, int st) {
           const int rst = (st + 1) & kMask;
           const int32_t kt_load = kt + NST;
           const i32x4 ra = make_rsrc_words(a_kstep(phys(kt_load)), kt_load < ke);
           const i32x4 rb = make_rsrc_words(b_kstep(phys(kt_load)), kt_load < ke);
-          const uint32_t lbase = lds_addr(smem);
+          const int32_t pair_load = phys(kt + NST - 1);
+          const i32x4 wa = WIDE && odd ? wide_rsrc(true, kt + NST - 1) : ra, wb = WIDE && odd ? wide_rsrc(false, kt + NST - 1) : rb;
           constexpr int kChunks = CF::MI + CF::NI, kWiden = 4 * kChunks;
-          constexpr int kLoadEvery = 2 * kMfma / kLoads;
           // second half: reads first (kReadEach after each MFMA), conversions from kFrom on
+          auto pair_of = [](int i, int c) { return i * (kWiden / kMfma) + c; };
           constexpr int kReadEach = kChunks / (kMfma / 4), kFrom = kMfma / 4 + kMfma / 8;
           static_assert(kReadEach * (kMfma / 4) == kChunks && kWiden % kMfma == 0 && 2 * (kMfma - kFrom) >= kWiden / (kWiden / kMfma), "step");
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            int next = 0;
+          auto half = [&](auto second) {
+            constexpr bool h = decltype(second)::value;
 #pragma unroll
             for (int i = 0; i < kMfma; ++i) {
-              if (h == 0) mfma16(i / CF::NI, i % CF::NI, a0[i / CF::NI], b0[i % CF::NI]);
-              else mfma16(i / CF::NI, i % CF::NI, a1[i / CF::NI], b1[i % CF::NI]);
+              if (h) mfma16(i / CF::NI, i % CF::NI, a1[i / CF::NI], b1[i % CF::NI]);
+              else mfma16(i / CF::NI, i % CF::NI, a0[i / CF::NI], b0[i % CF::NI]);
               __builtin_amdgcn_sched_barrier(0);
-              if (h == 0) {
+              if (!h) {
 #pragma unroll
-                for (int c = i * (kWiden / kMfma); c < (i + 1) * (kWiden / kMfma); ++c) widen(c >> 2, 1, c & 3, a1, b1);
+                for (int c = 0; c < kWiden / kMfma; ++c) widen(pair_of(i, c) >> 2, 1, pair_of(i, c) & 3, a1, b1);
               } else if (i < kMfma / 4) {
 #pragma unroll
-                for (int q = i * kReadEach; q < (i + 1) * kReadEach; ++q) read_raw(rst, q);
+                for (int q = 0; q < kReadEach; ++q) read_raw(rst, !odd, i * kReadEach + q);
               } else if (i >= kFrom) {
 #pragma unroll
-                for (int c = 0; c < 2 * (kWiden / kMfma); ++c)
-                  if (next < kWiden) {
-                    widen(next >> 2, 0, next & 3, a0, b0);
-                    ++next;
-                  }
+                for (int c = 0; c < 2 * (kWiden / kMfma); ++c) {
+                  const int next = 2 * pair_of(i - kFrom, 0) + c;
+                  if (next < kWiden) widen(next >> 2, 0, next & 3, a0, b0);
+                }
               }
-              const int at = h * kMfma + i;
-#pragma unroll
-              for (int j = 0; j < kLoads; ++j)
-                if (kLoadEvery * j + kLoadEvery / 2 == at)
-                  load16_to_lds(j < CF::A_LOADS ? ra : rb, lbase + load_dst(j, st),
-                                decltype(fast)::value ? voff_fast[j] : load_voff(j, kt_load));
+              step_loads(fast, odd, kt, st, (h ? kMfma : 0) + i, 2 * kMfma, ra, rb, wa, wb, pair_load);
               __builtin_amdgcn_sched_barrier(0);
             }
-          }
+          };
+          half(std::false_type{});
+          half(std::true_type{});
           __builtin_amdgcn_s_waitcnt(0xC07F);  // as in step
-          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * kLoads) : "memory");
+          step_wait(odd);
           wg_barrier();
         };
         // the zeroed accumulators in their registers, then 16 wait states, before
@@ -1012,7 +1107,9 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // t (t - kb even) with t + 5 >= full on; the trips before it use the fast
         // offsets.
         const int32_t slow_from =
-            (K % CF::BK != 0 && full < ke) ? kb + ((max(full - (NST + 1) - kb, 0) + 1) / 2) * 2 : ke + 2;
+            (WIDE ? K % (2 * CF::BK) != 0 && ke == nk : K % CF::BK != 0 && full < ke)
+                ? kb + ((max(full - (NST + 1) - kb, 0) + 1) / 2) * 2
+                : ke + 2;
         // Fast trips of four steps while whole ones fit (constant stages), then
         // two-step trips with the stage computed at run time. A run starts with
         // kt - kb a multiple of 4.
@@ -1021,30 +1118,34 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
           if constexpr (E8) {
             for (; kt + 4 <= fast_end; kt += 4) {
               const int st = NST == 4 ? 0 : (kt - kb) & kMask;
-              step8(std::true_type{}, kt, st);
-              step8(std::true_type{}, kt + 1, st + 1);
-              step8(std::true_type{}, kt + 2, st + 2);
-              step8(std::true_type{}, kt + 3, st + 3);
+              step8(std::true_type{}, false, kt, st);
+              step8(std::true_type{}, true, kt + 1, st + 1);
+              step8(std::true_type{}, false, kt + 2, st + 2);
+              step8(std::true_type{}, true, kt + 3, st + 3);
             }
-            for (; kt < end; ++kt) step8(std::false_type{}, kt, (kt - kb) & kMask);
+            for (; kt < end; kt += 2) {
+              const int st = (kt - kb) & kMask;
+              step8(std::false_type{}, false, kt, st);
+              step8(std::false_type{}, true, kt + 1, (st + 1) & kMask);
+            }
             return;
           }
           for (; kt + 4 <= fast_end; kt += 4) {
             const int st = NST == 4 ? 0 : (kt - kb) & kMask;
-            step(std::true_type{}, kt, st, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 1, st + 1, a1, b1, a0, b0);
-            step(std::true_type{}, kt + 2, st + 2, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 3, st + 3, a1, b1, a0, b0);
+            step(std::true_type{}, false, kt, st, a0, b0, a1, b1);
+            step(std::true_type{}, true, kt + 1, st + 1, a1, b1, a0, b0);
+            step(std::true_type{}, false, kt + 2, st + 2, a0, b0, a1, b1);
+            step(std::true_type{}, true, kt + 3, st + 3, a1, b1, a0, b0);
           }
           for (; kt < fast_end; kt += 2) {
             const int st = (kt - kb) & kMask;
-            step(std::true_type{}, kt, st, a0, b0, a1, b1);
-            step(std::true_type{}, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
+            step(std::true_type{}, false, kt, st, a0, b0, a1, b1);
+            step(std::true_type{}, true, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
           }
           for (; kt < end; kt += 2) {
             const int st = (kt - kb) & kMask;
-            step(std::false_type{}, kt, st, a0, b0, a1, b1);
-            step(std::false_type{}, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
+            step(std::false_type{}, false, kt, st, a0, b0, a1, b1);
+            step(std::false_type{}, true, kt + 1, (st + 1) & kMask, a1, b1, a0, b0);
           }
         };
         int32_t kt = kb;

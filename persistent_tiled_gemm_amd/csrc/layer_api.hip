@@ -105,55 +105,73 @@ gemm_status make_tiles(gemm_tile_cfg *out, int32_t edge, int32_t device) {
 // the K-chunks S that the tiles from `base` on are split into.
 struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 
-// The choice is the least of the times that two fits give, in microseconds (256
-// CUs; measured over m = 100 .. 4096, n = 1024 .. 16384, k = 776 .. 8192 in the
-// linear layer's and the weight gradient's layouts; within about 15% of them):
-//   128 x 128 tiles   a k-step takes 0.24 while a CU has one tile and 0.29 a tile
-//                     when it has more; 8 to fill and drain;
-//   256 x 256 tiles   a k-step takes 0.45 with few CUs at work and 0.7 with all of
-//                     them (power and memory shared), 22 to fill and drain;
-//   splitting         4 for the second launch, and each chunk's sums written and
-//                     read: 0.02 a chunk of 128 x 128, 0.06 of 256 x 256.
-// Both sides where it matters: 512 x 8192 x 8192, 256 tiles of 128: 72 us, 64 tiles
-// of 256 in 3 chunks: 86; 1024 x 8192 x 8192, 512 tiles of 128: 154, 128 tiles of
-// 256 in 2 chunks: 132; 256 x 4096 x 4096, 64 tiles of 128: 38, in 4 chunks: 26;
-// 100 x 1024 x 8192, 8 tiles of 128: 46, in 8 chunks: 21.
-TileChoice choose_tiles(int64_t m, int64_t n, int64_t nk, int64_t cus) {
+// The choice is the least of the times that these fits give, in microseconds (256
+// CUs; measured over m = 100 .. 4096, n = 1024 .. 16384, k = 768 .. 8192 in each
+// form; within about 15% of the times):
+//   - a k-step of a 128 x 128 tile: NT and NN 0.30 with one tile a CU at a time
+//     (their stages fill its LDS), e4m3 0.41; TN 0.23, and with two tiles a CU
+//     together 0.44; 8 to fill and drain;
+//   - a k-step of a 256 x 256 tile: from the first to the second figure as more
+//     CUs work (power and memory shared): 0.48 to 0.64, e4m3 0.9 to 1.12; 18 to
+//     fill and drain;
+//   - rows of a k-contiguous operand that do not start on 64-byte lines: 128 x 128
+//     steps 1.4 times as long, 256 x 256 ones 1.35 (NN, with one such operand, 1.1;
+//     e4m3, which takes half the bytes a product, 1.1);
+//   - splitting: 4 for the second launch, and each chunk's sums written and read,
+//     0.02 a chunk of 128 x 128, 0.06 of 256 x 256.
+// Both sides where it matters (NT): 512 x 8192 x 8192, 256 tiles of 128: 79 us, 64
+// of 256 in 4 chunks: 76; 1024 x 8192 x 8192, 512 of 128: 155, 128 of 256: 154, in
+// 2 chunks: 118; 1024 x 4096 x 4096, 256 of 128: 47, 64 of 256 in 4 chunks: 54;
+// 256 x 4096 x 4096, 64 of 128: 43, in 4 chunks: 26; 100 x 1024 x 8192, 8 of 128:
+// 62, in 8 chunks: 21; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
+// last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55.
+TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
+  const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN;
+  const int64_t nk = ceil_div(e8 ? a.k / 2 : a.k, 32), line = e8 ? 64 : 32;
+  const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (form != ptg::kFormNN && a.ldb % line != 0));
+  const double slow128 = off_line ? (e8 ? 1.1 : 1.4) : 1.0, slow256 = off_line ? (form == ptg::kFormNT ? 1.35 : 1.1) : 1.0;
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
-    const int64_t T = ceil_div(m, edge) * ceil_div(n, edge);
+    const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
     const int64_t slots = edge == 256 ? cus : 2 * cus;  // chunks the workspace holds
     // the time of `units` tiles or chunks of `steps` k-steps
-    auto run = [&](int64_t units, double steps) {
-      const double load = (double)units / (double)cus;
-      if (edge == 128) return steps * (load <= 1.0 ? 0.24 : std::max(0.58, 0.29 * load));
-      return steps * (load <= 1.0 ? 0.45 + 0.25 * load * load : 0.7 * (double)ceil_div(units, cus));
+    auto run = [&](int64_t units, int64_t steps) {
+      const double load = (double)units / (double)cus, rounds = (double)ceil_div(units, cus);
+      double step;
+      if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.16 * load * load) : (e8 ? 1.12 : 0.64) * rounds);
+      else if (tn) step = load <= 1.0 ? 0.23 : std::max(0.44, 0.23 * load);
+      else step = slow128 * (e8 ? 0.41 : 0.30) * rounds;
+      return (double)steps * step;
     };
-    const double fixed = edge == 256 ? 22.0 : 8.0, join = edge == 256 ? 0.06 : 0.02;
-    const double whole = fixed + run(T, (double)nk);
+    const double fixed = edge == 256 ? 18.0 : 8.0, join = edge == 256 ? 0.06 : 0.02;
+    const double whole = fixed + run(T, nk);
     if (whole < best.us) best = {edge, 1, 0, whole};
     // all tiles, or those of the partial last wave
     const int64_t waves = T / cus * cus;
     for (const int64_t base : {(int64_t)0, waves}) {
       const int64_t r = T - base;
-      if (r == 0 || (base != 0 && edge == 128)) continue;  // (small tiles' last wave shares the CUs of the wave before)
+      if (r == 0 || (base != 0 && edge == 128 && tn)) continue;  // (TN: small tiles' last wave shares the CUs of the wave before)
+      const double before = base ? run(base, nk) : 0.0;
       for (int32_t S = 2; S <= 32 && r * S <= slots && nk / S >= 4; ++S) {
-        const double us = fixed + (base ? run(base, (double)nk) : 0.0) + run(r * S, (double)ceil_div(nk, S)) + 4.0 + join * (double)(r * S);
+        const double us = fixed + before + run(r * S, ceil_div(nk, S)) + 4.0 + join * (double)(r * S);
         if (us < best.us) best = {edge, S, base, us};
       }
+      if (base == waves) break;  // fewer tiles than CUs: both are the same
     }
   }
   return best;
 }
 
 gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStream_t s) {
-  const int64_t nk = ceil_div(form == ptg::kFormNTE4m3 ? a.k / 2 : a.k, 32);
-  const TileChoice c = choose_tiles(a.m, a.n, nk, p->cu_count);
+  const TileChoice c = choose_tiles(a, form, p->cu_count);
   gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
   gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
   if (st == GEMM_E_HIP) p->last_error = gemm_last_hip_error(t);
   return st;
 }
+
+// The stride the kernels get: a matrix of one row has its row's length, whatever the caller said.
+int64_t stride_of(int64_t ld, int64_t m, int64_t n) { return m > 1 && n > 0 ? ld : std::max<int64_t>(n, 8); }
 
 // Partial sums of n columns over at most `wanted` rows: as many rows as the workspace holds.
 int64_t partial_rows(int64_t wanted, int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(wanted, kWsFloats / std::max<int64_t>(n, 1))); }
@@ -258,10 +276,10 @@ gemm_status layer_rmsnorm(const layer_rmsnorm_args *a, void *stream) {
   k.sum_out = a->sum_out;
   k.out = a->out;
   k.scale = a->scale;
-  k.ldx = a->ldx;
-  k.ldr = a->ldr;
-  k.lds = a->lds;
-  k.ldo = a->ldo;
+  k.ldx = stride_of(a->ldx, a->m, a->n);
+  k.ldr = stride_of(a->ldr, a->m, a->n);
+  k.lds = stride_of(a->lds, a->m, a->n);
+  k.ldo = stride_of(a->ldo, a->m, a->n);
   k.m = (int32_t)a->m;
   k.n = (int32_t)a->n;
   k.type = a->type;
@@ -300,10 +318,10 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p
     k.dsum = a->dsum;
     k.dx = a->dx;
     k.partial = a->dweight ? p->d_ws : nullptr;
-    k.lddy = a->lddy;
-    k.lds = a->lds;
-    k.lddsum = a->lddsum;
-    k.lddx = a->lddx;
+    k.lddy = stride_of(a->lddy, a->m, a->n);
+    k.lds = stride_of(a->lds, a->m, a->n);
+    k.lddsum = stride_of(a->lddsum, a->m, a->n);
+    k.lddx = stride_of(a->lddx, a->m, a->n);
     k.m = (int32_t)a->m;
     k.n = (int32_t)a->n;
     k.type = a->type;
@@ -350,8 +368,8 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   std::memset(&k, 0, sizeof(k));
   k.a = a->x;
   k.b = a->w;
-  k.lda = a->ldx;
-  k.ldb = a->ldw;
+  k.lda = stride_of(a->ldx, a->m, a->k);
+  k.ldb = stride_of(a->ldw, a->n, a->k);
   k.m = (int32_t)a->m;
   k.n = (int32_t)a->n;
   k.k = (int32_t)a->k;
@@ -361,9 +379,9 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual = a->residual;
   k.ep.pre = a->pre;
   k.ep.out = a->out;
-  k.ep.ldr = a->ldr;
-  k.ep.ldp = a->ldp;
-  k.ep.ldo = a->ldo;
+  k.ep.ldr = stride_of(a->ldr, a->m, a->n);
+  k.ep.ldp = stride_of(a->ldp, a->m, a->n);
+  k.ep.ldo = stride_of(a->ldo, a->m, a->n);
   k.ep.bias_type = a->bias_type;
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
@@ -403,9 +421,9 @@ gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer
     k.pre = a->pre;
     k.dpre = a->dpre;
     k.partial = a->dbias ? p->d_ws : nullptr;
-    k.lddo = a->lddo;
-    k.ldp = a->ldp;
-    k.lddp = a->lddp;
+    k.lddo = stride_of(a->lddo, a->m, a->n);
+    k.ldp = stride_of(a->ldp, a->m, a->n);
+    k.lddp = stride_of(a->lddp, a->m, a->n);
     k.m = (int32_t)a->m;
     k.n = (int32_t)a->n;
     k.act = a->activation;
@@ -447,13 +465,13 @@ gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, 
     std::memset(&k, 0, sizeof(k));
     k.a = a->dpre;
     k.b = a->w;
-    k.lda = a->lddp;
-    k.ldb = a->ldw;
+    k.lda = stride_of(a->lddp, a->m, a->n);
+    k.ldb = stride_of(a->ldw, a->n, a->k);
     k.m = (int32_t)a->m;
     k.n = (int32_t)a->k;
     k.k = (int32_t)a->n;
     k.ep.out = a->dx;
-    k.ep.ldo = a->lddx;
+    k.ep.ldo = stride_of(a->lddx, a->m, a->k);
     k.ep.out_type = a->dx_type;
     st = run_tiles(p, k, ptg::kFormNN, s);
     if (st != GEMM_OK) return st;
@@ -462,16 +480,16 @@ gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, 
     std::memset(&k, 0, sizeof(k));
     k.a = a->dpre;
     k.b = a->x;
-    k.lda = a->lddp;
-    k.ldb = a->ldx;
+    k.lda = stride_of(a->lddp, a->m, a->n);
+    k.ldb = stride_of(a->ldx, a->m, a->k);
     k.m = (int32_t)a->n;
     k.n = (int32_t)a->k;
     k.k = (int32_t)a->m;
     k.ep.out = a->dw;
-    k.ep.ldo = a->lddw;
+    k.ep.ldo = stride_of(a->lddw, a->n, a->k);
     k.ep.out_type = a->dw_type;
     k.ep.residual = a->accumulate ? a->dw : nullptr;
-    k.ep.ldr = a->lddw;
+    k.ep.ldr = stride_of(a->lddw, a->n, a->k);
     k.ep.residual_type = a->dw_type;
     st = run_tiles(p, k, ptg::kFormTN, s);
     if (st != GEMM_OK) return st;

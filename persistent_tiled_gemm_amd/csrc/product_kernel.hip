@@ -105,10 +105,15 @@ __device__ __forceinline__ void finish_rows(const EpilogueArgs &e, int64_t m, in
 template <int FORM>
 struct ProductOp {
   using Args = ProductOpArgs;
-  static constexpr bool AT = FORM == kFormTN, E8 = FORM == kFormNTE4m3, BT = FORM == kFormNT || E8, kPlain = false;
-  // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step ahead of their MFMAs (the 128 x 128
-  // tile's other form, 32 x 32 blocks read half a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192)
-  template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16>;
+  static constexpr bool AT = FORM == kFormTN, E8 = FORM == kFormNTE4m3, BT = FORM == kFormNT || E8, kPlain = false, kWide = !AT;
+  // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step
+  // ahead of their MFMAs (the 128 x 128 tile's other form, 32 x 32 blocks read half
+  // a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192). k-contiguous
+  // operands come two k-steps at a time (8192^3 NT 759 -> 742 us, NN 734 -> 700;
+  // 1000 x 4104 x 2056 61 -> 47); a pair's loads then have one to two steps to land
+  // in a ring of four stages, enough for the 256 x 256 tile's steps but not for the
+  // shorter ones of 128 x 128, which get eight (and one workgroup a CU).
+  template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16, EDGE == 128 && !AT ? 8 : 4>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
 
@@ -182,7 +187,7 @@ struct ProductOp {
 };
 
 template <int EDGE, int FORM>
-__global__ __launch_bounds__(256, EDGE == 128 ? 2 : 1) void ptg_product_kernel(const ProductKernelArgs a) {
+__global__ __launch_bounds__(256, EDGE == 128 && FORM == kFormTN ? 2 : 1) void ptg_product_kernel(const ProductKernelArgs a) {
   gemm_body<EDGE, EDGE, kDynamic, false, ProductOp<FORM>>(a.gemm, a.op);
 }
 
