@@ -155,53 +155,60 @@ def _prepare():
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _stream_of(stream, like):
-    return _raw_stream(like.get_device()) if stream is None else _stream_ptr(stream)
+def _stream_of(stream, at):
+    return _raw_stream(at) if stream is None else _stream_ptr(stream)
 
 
 def _first(name, t, device=None):
-    """Rows and columns of the operand that the others are measured by; it is on `device` (a plan's) or the current one."""
+    """(shape, device index) of the operand that the others are measured by; it is on `device` (a plan's) or the current
+    one."""
     if not _codes:
         _prepare()
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.get_device() != (_current_device() if device is None else device):
+    if at != (_current_device() if device is None else device):
         raise ValueError(f"{name} is on {t.device}, the call's device is another one")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return shape, at
 
 
-def _matrix(name, t, rows, cols, like, allowed):
-    """(pointer, row stride, type code) of an optional rows x cols matrix with dense rows."""
+def _refuse(name, t, shape, at, allowed):
+    """What is wrong with an argument that failed a check."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != at:
+        raise ValueError(f"{name} is on {t.device}, expected device {at}")
+    if _codes.get(t.dtype) not in allowed:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    raise ValueError(f"{name} must have dense rows (stride 1 along its columns)" if len(shape) == 2 else f"{name} must be contiguous")
+
+
+def _matrix(name, t, shape, at, allowed):
+    """(pointer, row stride, type code) of an optional matrix with dense rows."""
     if t is None:
         return 0, 0, LAYER_F32
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     code = _codes.get(t.dtype)
-    if code not in allowed:
-        raise ValueError(f"{name} has dtype {t.dtype}")
+    if t.shape != shape or t.get_device() != at or code not in allowed:
+        _refuse(name, t, shape, at, allowed)
+    rows, cols = shape
+    if t.is_contiguous():
+        return t.data_ptr(), cols, code
     row, col = t.stride()
     if col != 1 and cols > 1:
-        raise ValueError(f"{name} must have dense rows (stride 1 along its columns)")
+        _refuse(name, t, shape, at, allowed)
     return t.data_ptr(), row if rows > 1 else cols, code
 
 
-def _vector(name, t, n, like, allowed):
+def _vector(name, t, n, at, allowed):
     """(pointer, type code) of an optional dense vector of n elements."""
     if t is None:
         return 0, LAYER_F32
-    if t.shape != (n,):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     code = _codes.get(t.dtype)
-    if code not in allowed:
-        raise ValueError(f"{name} has dtype {t.dtype}")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
+    if t.shape != (n,) or t.get_device() != at or code not in allowed or not t.is_contiguous():
+        _refuse(name, t, (n,), at, allowed)
     return t.data_ptr(), code
 
 
@@ -212,21 +219,24 @@ def _activation(name) -> int:
 
 
 _STREAM = (LAYER_F32, LAYER_BF16)
+_ANY = (LAYER_F32, LAYER_BF16, LAYER_E4M3)
+_ONLY = {c: (c,) for c in _ANY}  # the types allowed beside one that is given
 
 
 def layer_rmsnorm(x, weight, out, *, residual=None, sum_out=None, scale=None, eps: float = 1e-6, stream=None) -> None:
     """layer_rmsnorm: out = s / sqrt(mean(s^2) + eps) * weight per row, s = x + residual (kept in sum_out, which
     may be x or residual). x, residual, sum_out: one dtype, bf16 or fp32. weight: bf16 or fp32, or None. out: fp32,
     bf16, or float8_e4m3fn with `scale` (fp32, one value a row): s's norm is then about out * scale[:, None]."""
-    m, n = _first("x", x)
-    px, ldx, ty = _matrix("x", x, m, n, x, _STREAM)
-    pr, ldr, _ = _matrix("residual", residual, m, n, x, (ty,))
-    ps, lds, _ = _matrix("sum_out", sum_out, m, n, x, (ty,))
-    pw, wt = _vector("weight", weight, n, x, _STREAM)
-    po, ldo, ot = _matrix("out", out, m, n, x, (LAYER_F32, LAYER_BF16, LAYER_E4M3))
-    pc, _ = _vector("scale", scale, m, x, (LAYER_F32,))
+    shape, at = _first("x", x)
+    m, n = shape
+    px, ldx, ty = _matrix("x", x, shape, at, _STREAM)
+    pr, ldr, _ = _matrix("residual", residual, shape, at, _ONLY[ty])
+    ps, lds, _ = _matrix("sum_out", sum_out, shape, at, _ONLY[ty])
+    pw, wt = _vector("weight", weight, n, at, _STREAM)
+    po, ldo, ot = _matrix("out", out, shape, at, _ANY)
+    pc, _ = _vector("scale", scale, m, at, _ONLY[LAYER_F32])
     a = _RMSNORM(px, pr, pw, ps, po, pc, m, n, ldx, ldr, lds, ldo, ty, wt, ot, eps)
-    st = _library().layer_rmsnorm(a, _stream_of(stream, x))
+    st = (_lib or _library()).layer_rmsnorm(a, _stream_of(stream, at))
     if st:
         _check(st, "layer_rmsnorm")
 
@@ -235,15 +245,16 @@ def layer_rmsnorm_backward(dy, s, weight, dx, dweight, plan: LayerPlan, *, dsum=
                            eps: float = 1e-6, stream=None) -> None:
     """layer_rmsnorm_backward: dx (of the sum s, so of x and of the residual) and dweight (fp32) from dy, at s.
     dsum: the gradient that reaches s from elsewhere, added to dx (dx may be dsum). dx or dweight may be None."""
-    m, n = _first("s", s, plan.device)
-    ps, lds, ty = _matrix("s", s, m, n, s, _STREAM)
-    pd, lddy, dt = _matrix("dy", dy, m, n, s, _STREAM)
-    pw, wt = _vector("weight", weight, n, s, _STREAM)
-    pu, lddsum, _ = _matrix("dsum", dsum, m, n, s, (ty,))
-    px, lddx, _ = _matrix("dx", dx, m, n, s, (ty,))
-    pg, _ = _vector("dweight", dweight, n, s, (LAYER_F32,))
+    shape, at = _first("s", s, plan.device)
+    m, n = shape
+    ps, lds, ty = _matrix("s", s, shape, at, _STREAM)
+    pd, lddy, dt = _matrix("dy", dy, shape, at, _STREAM)
+    pw, wt = _vector("weight", weight, n, at, _STREAM)
+    pu, lddsum, _ = _matrix("dsum", dsum, shape, at, _ONLY[ty])
+    px, lddx, _ = _matrix("dx", dx, shape, at, _ONLY[ty])
+    pg, _ = _vector("dweight", dweight, n, at, _ONLY[LAYER_F32])
     a = _RMSNORM_GRAD(pd, ps, pw, pu, px, pg, m, n, lddy, lds, lddsum, lddx, ty, dt, wt, 1 if accumulate else 0, eps)
-    st = _library().layer_rmsnorm_backward(a, plan.handle, _stream_of(stream, s))
+    st = (_lib or _library()).layer_rmsnorm_backward(a, plan.handle, _stream_of(stream, at))
     if st:
         _check(st, "layer_rmsnorm_backward", plan)
 
@@ -254,20 +265,23 @@ def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "no
     with row scales x_scale and w_scale, fp32). out and residual: bf16 or fp32; residual may be out. pre (bf16)
     keeps the activation's argument for layer_activation_backward."""
     act = _activation(activation)
-    m, k = _first("x", x, plan.device)
-    n, k2 = _first("w", w, plan.device)
+    x_shape, at = _first("x", x, plan.device)
+    w_shape, _ = _first("w", w, plan.device)
+    m, k = x_shape
+    n, k2 = w_shape
     if k2 != k:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
-    px, ldx, ty = _matrix("x", x, m, k, x, (LAYER_BF16, LAYER_E4M3))
-    pw, ldw, _ = _matrix("w", w, n, k, x, (ty,))
-    pxs, _ = _vector("x_scale", x_scale, m, x, (LAYER_F32,))
-    pws, _ = _vector("w_scale", w_scale, n, x, (LAYER_F32,))
-    pb, bt = _vector("bias", bias, n, x, _STREAM)
-    pr, ldr, rt = _matrix("residual", residual, m, n, x, _STREAM)
-    pz, ldp, _ = _matrix("pre", pre, m, n, x, (LAYER_BF16,))
-    po, ldo, ot = _matrix("out", out, m, n, x, _STREAM)
+    shape = (m, n)
+    px, ldx, ty = _matrix("x", x, x_shape, at, (LAYER_BF16, LAYER_E4M3))
+    pw, ldw, _ = _matrix("w", w, w_shape, at, _ONLY[ty])
+    pxs, _ = _vector("x_scale", x_scale, m, at, _ONLY[LAYER_F32])
+    pws, _ = _vector("w_scale", w_scale, n, at, _ONLY[LAYER_F32])
+    pb, bt = _vector("bias", bias, n, at, _STREAM)
+    pr, ldr, rt = _matrix("residual", residual, shape, at, _STREAM)
+    pz, ldp, _ = _matrix("pre", pre, shape, at, _ONLY[LAYER_BF16])
+    po, ldo, ot = _matrix("out", out, shape, at, _STREAM)
     a = _LINEAR(px, pw, pxs, pws, pb, pr, pz, po, m, n, k, ldx, ldw, ldr, ldp, ldo, ty, bt, rt, ot, act, 0)
-    st = _library().layer_linear(a, plan.handle, _stream_of(stream, x))
+    st = (_lib or _library()).layer_linear(a, plan.handle, _stream_of(stream, at))
     if st:
         _check(st, "layer_linear", plan)
 
@@ -277,13 +291,14 @@ def layer_activation_backward(dout, pre, dpre, plan: LayerPlan, *, activation: s
     """layer_activation_backward: dpre = dout * act'(pre) (bf16; dpre may be dout or pre, or None) and dbias = its
     column sums before rounding (fp32, or None). pre may be None with activation "none"."""
     act = _activation(activation)
-    m, n = _first("dout", dout, plan.device)
-    pd, lddo, _ = _matrix("dout", dout, m, n, dout, (LAYER_BF16,))
-    pz, ldp, _ = _matrix("pre", pre, m, n, dout, (LAYER_BF16,))
-    pg, lddp, _ = _matrix("dpre", dpre, m, n, dout, (LAYER_BF16,))
-    pb, _ = _vector("dbias", dbias, n, dout, (LAYER_F32,))
+    shape, at = _first("dout", dout, plan.device)
+    m, n = shape
+    pd, lddo, _ = _matrix("dout", dout, shape, at, _ONLY[LAYER_BF16])
+    pz, ldp, _ = _matrix("pre", pre, shape, at, _ONLY[LAYER_BF16])
+    pg, lddp, _ = _matrix("dpre", dpre, shape, at, _ONLY[LAYER_BF16])
+    pb, _ = _vector("dbias", dbias, n, at, _ONLY[LAYER_F32])
     a = _ACTIVATION_GRAD(pd, pz, pg, pb, m, n, lddo, ldp, lddp, act, 1 if accumulate else 0)
-    st = _library().layer_activation_backward(a, plan.handle, _stream_of(stream, dout))
+    st = (_lib or _library()).layer_activation_backward(a, plan.handle, _stream_of(stream, at))
     if st:
         _check(st, "layer_activation_backward", plan)
 
@@ -293,14 +308,16 @@ def layer_linear_backward(dpre, x, w, plan: LayerPlan, *, dx=None, dw=None, accu
     bf16 or fp32 and optional. dpre, x, w: bf16; x may be None without dw, w may be None without dx."""
     if (dx is None and dw is None) or (dx is not None and w is None) or (dw is not None and x is None):
         raise ValueError("layer_linear_backward needs dx or dw, w for dx and x for dw")
-    m, n = _first("dpre", dpre, plan.device)
-    k = _first("w", w, plan.device)[1] if w is not None else _first("x", x, plan.device)[1]
-    pd, lddp, _ = _matrix("dpre", dpre, m, n, dpre, (LAYER_BF16,))
-    px, ldx, _ = _matrix("x", x, m, k, dpre, (LAYER_BF16,))
-    pw, ldw, _ = _matrix("w", w, n, k, dpre, (LAYER_BF16,))
-    pdx, lddx, xt = _matrix("dx", dx, m, k, dpre, _STREAM)
-    pdw, lddw, wt = _matrix("dw", dw, n, k, dpre, _STREAM)
+    shape, at = _first("dpre", dpre, plan.device)
+    m, n = shape
+    k = _first("w", w, plan.device)[0][1] if w is not None else _first("x", x, plan.device)[0][1]
+    x_shape, w_shape = (m, k), (n, k)
+    pd, lddp, _ = _matrix("dpre", dpre, shape, at, _ONLY[LAYER_BF16])
+    px, ldx, _ = _matrix("x", x, x_shape, at, _ONLY[LAYER_BF16])
+    pw, ldw, _ = _matrix("w", w, w_shape, at, _ONLY[LAYER_BF16])
+    pdx, lddx, xt = _matrix("dx", dx, x_shape, at, _STREAM)
+    pdw, lddw, wt = _matrix("dw", dw, w_shape, at, _STREAM)
     a = _LINEAR_GRAD(pd, px, pw, pdx, pdw, m, n, k, lddp, ldx, ldw, lddx, lddw, xt, wt, 1 if accumulate else 0, 0)
-    st = _library().layer_linear_backward(a, plan.handle, _stream_of(stream, dpre))
+    st = (_lib or _library()).layer_linear_backward(a, plan.handle, _stream_of(stream, at))
     if st:
         _check(st, "layer_linear_backward", plan)
