@@ -343,3 +343,79 @@ def test_refusals_with_a_plan(plan):
     with pytest.raises(ptg.PtgError) as e:
         ptg.layer_activation_backward(out, None, out, plan, activation="relu")
     assert e.value.status == -1
+
+
+def sampled(m, tile, n=24):
+    """Rows in every part of the tiles: the first and last, tile borders, and some between."""
+    g = torch.Generator().manual_seed(m)
+    rows = {0, m - 1, *range(0, m, tile), *range(tile - 1, m, tile)} | set(torch.randint(0, m, (n,), generator=g).tolist())
+    return torch.tensor(sorted(r for r in rows if r < m))
+
+
+# 256 x 256 tiles: whole waves and a split partial one, one partial wave, a long split k; ragged edges and odd k-steps
+LARGE = [(4104, 4096, 1032), (1032, 8192, 4096), (520, 8200, 8208), (2049, 4104, 2056)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+@pytest.mark.parametrize("t", [BF16, E4M3])
+def test_linear_large_tiles(plan, m, n, k, t):
+    k = k // 16 * 16 if t == E4M3 else k
+    say("linear large", m, n, k, t)
+    x, w, xs, ws = operands(m, n, k, t)
+    b, r = normal(3, n), normal(4, m, n)
+    out, z_out = Out(m, n, BF16), Out(m, n, BF16)
+    ptg.layer_linear(x, w, out.t, plan, bias=b, activation="silu", residual=r, pre=z_out.t, x_scale=xs, w_scale=ws)
+    torch.cuda.synchronize()
+    out.check()
+    z_out.check()
+    assert torch.isfinite(out.t.float()).all()
+    rows = sampled(m, 256)
+    at = rows.cuda()
+    pick = (x.float()[at], w, b, "silu", r[at])
+    scales = (None if xs is None else xs[at], ws)
+    z, y = ref.linear(pick[0], w, b, "silu", pick[4], *scales)
+    bz, by = ref.linear_bounds(pick[0], w, b, "silu", pick[4], BF16, *scales)
+    within(out.t[at], y, by, "out")
+    within(z_out.t[at], z, bz, "pre")
+    again = torch.empty_like(out.t)
+    ptg.layer_linear(x, w, again, plan, bias=b, activation="silu", residual=r, x_scale=xs, w_scale=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out.t), "the same call twice gave different bits"
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_linear_backward_large_tiles(plan, m, n, k):
+    say("linear backward large", m, n, k)
+    dpre, x, w = normal(1, m, n, scale=0.1), normal(2, m, k), normal(3, n, k, scale=k ** -0.5)
+    dx, dw = Out(m, k, BF16), Out(n, k, F32)
+    ptg.layer_linear_backward(dpre, x, w, plan, dx=dx.t, dw=dw.t)
+    torch.cuda.synchronize()
+    dx.check()
+    dw.check()
+    assert torch.isfinite(dx.t.float()).all() and torch.isfinite(dw.t).all()
+    at, to = sampled(m, 256).cuda(), sampled(n, 256).cuda()
+    within(dx.t[at], *ref.product_bound(dpre[at], w, BF16), "dx")
+    within(dw.t[to], *ref.product_bound(dpre.t()[to], x, F32), "dw")
+
+
+@pytest.mark.parametrize("k", [32, 56, 64, 72, 96, 120, 128, 160, 192, 200, 264, 520])
+@pytest.mark.parametrize("m,n", [(130, 264), (300, 520)])
+def test_linear_short_and_odd_k(plan, m, n, k):
+    """k of one to nine k-steps: pairs of them whole, half empty and cut short, fewer than the ring holds."""
+    say("linear short k", m, n, k)
+    check_linear(plan, m, n, k)
+    check_linear(plan, m, n, (k + 15) // 16 * 16, E4M3, bias=None)
+    check_backward(plan, m, k, n)
+
+
+@pytest.mark.parametrize("m", [1, 17, 130])
+def test_linear_strides_that_are_not_looked_at(plan, m):
+    """Row strides far past the rows' length, and (one row) any stride at all."""
+    x, w = normal(1, m, 136, pad=4096), normal(2, 264, 136, pad=2048)
+    if m == 1:
+        x = torch.as_strided(x, (1, 136), (3, 1))
+    out = Out(m, 264, BF16, pad=512)
+    ptg.layer_linear(x, w, out.t, plan)
+    torch.cuda.synchronize()
+    within(out.t, ref.d(x) @ ref.d(w).t(), ref.linear_bounds(x, w, None, "none", None, BF16)[1], "out")
+    out.check()
