@@ -18,15 +18,29 @@ __global__ __launch_bounds__(256) void ptg_activation_backward_kernel(const ActG
   const int64_t r1 = r0 + a.rows_per_group < a.m ? r0 + a.rows_per_group : a.m;
   f32x8 sum = {};
   if (j < a.n) {
-    for (int64_t row = r0 + wave; row < r1; row += 4) {
-      f32x8 d = load8((const __bf16 *)a.dout + row * a.lddo + j);
-      if constexpr (ACT != kActNone) {
-        const f32x8 z = load8((const __bf16 *)a.pre + row * a.ldp + j);
+    // four rows at a time: their loads are all under way before the first is used
+    for (int64_t row = r0 + wave; row < r1; row += 16) {
+      bf16x8 d[4], z[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] *= act_grad_f32(ACT, z[e]);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t m = row + 4 * u;
+        if (m >= r1) continue;
+        d[u] = *(const bf16x8 *)((const __bf16 *)a.dout + m * a.lddo + j);
+        if constexpr (ACT != kActNone) z[u] = *(const bf16x8 *)((const __bf16 *)a.pre + m * a.ldp + j);
       }
-      if (a.dpre) store8((__bf16 *)a.dpre + row * a.lddp + j, d);
-      sum += d;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t m = row + 4 * u;
+        if (m >= r1) continue;
+        f32x8 g = widen(d[u]);
+        if constexpr (ACT != kActNone) {
+          const f32x8 v = widen(z[u]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] *= act_grad_f32(ACT, v[e]);
+        }
+        if (a.dpre) store8_nt((__bf16 *)a.dpre + m * a.lddp + j, g);
+        sum += g;
+      }
     }
   }
   if (a.partial) {
