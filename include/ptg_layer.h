@@ -20,7 +20,15 @@
  *
  * Types. Stream and operand types are named per argument. Sums, norms,
  * products and activations are held in fp32; each output is rounded once, to
- * the nearest value of its type, from the fp32 result.
+ * the nearest value of its type, from the fp32 result. e4m3 operands are
+ * widened to bf16 (exactly) before they are multiplied: the e4m3 matrix
+ * instructions would be faster, but they add eight products at a time and drop
+ * what lies 2^-13 below the largest of the eight.
+ *
+ * Speed. k-contiguous operands (x, w, dpre in layer_linear_backward's dx) are
+ * read 128 bytes of a row at a time: rows that start on 128-byte lines (strides
+ * that are multiples of 64 bf16 or 128 e4m3 elements) run fastest, rows off the
+ * 64-byte lines up to a third slower.
  *
  * Ownership, streams, errors. As in ptg_gemm.h: the caller owns every tensor
  * and keeps it alive until the stream has passed the call; calls are
@@ -77,7 +85,7 @@ typedef struct layer_plan *layer_cfg;
 
 /*
  * Build a plan on `device`, which must be the current device and gfx950. All
- * allocation happens here (about 100 MiB: the split products' partial sums for
+ * allocation happens here (about 96 MiB: the split products' partial sums for
  * both tile sizes, which the column sums share). Errors: GEMM_E_INVALID_ARG
  * (out NULL, no such device), GEMM_E_UNSUPPORTED, GEMM_E_DEVICE, GEMM_E_NOMEM,
  * GEMM_E_HIP.
@@ -142,8 +150,8 @@ gemm_status layer_rmsnorm(const layer_rmsnorm_args *args, void *stream);
  *   dweight_j = sum_m dy_mj h_mj                       (+ dweight_j with `accumulate`)
  * dsum: the gradient that reaches sum_out from the rest of the network (NULL:
  * none). dx (NULL: not wanted) may be dsum itself (same pointer and stride).
- * dweight (fp32, NULL: not wanted). With m == 0 dweight is zeroed (unless
- * accumulate is set). Errors as layer_rmsnorm, and GEMM_E_DEVICE.
+ * dweight (fp32, NULL: not wanted; a second launch). With m == 0 dweight is
+ * zeroed (unless accumulate is set). Errors as layer_rmsnorm, and GEMM_E_DEVICE.
  */
 typedef struct layer_rmsnorm_grad_args {
   const void *dy;     /* m x n, dy_type */
@@ -175,7 +183,8 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *args, layer_cf
  * nothing.
  * Few rows (a decode step) read every weight once and split k over the machine
  * when n alone does not fill it; many rows run as tiles under the dynamic tile
- * scheduler. One launch either way.
+ * scheduler, with k split as well where there are too few of them (then a second
+ * launch adds the parts).
  * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, an unknown type or
  * activation, a scale with bf16 operands), GEMM_E_SHAPE, GEMM_E_DEVICE,
  * GEMM_E_HIP.
@@ -204,9 +213,9 @@ gemm_status layer_linear(const layer_linear_args *args, layer_cfg cfg, void *str
 /*
  * dpre_mn = dout_mn act'(pre_mn), rounded to bf16, and dbias_n = sum_m of it
  * before that rounding (fp32; + dbias_n with `accumulate`). dpre or dbias may be
- * NULL (not wanted); dpre may be dout or pre itself (same stride). pre is not
- * read with LAYER_ACT_NONE and may be NULL then. With m == 0 dbias is zeroed
- * (unless accumulate is set). Errors as layer_linear.
+ * NULL (not wanted; dbias is a second launch); dpre may be dout or pre itself
+ * (same stride). pre is not read with LAYER_ACT_NONE and may be NULL then. With
+ * m == 0 dbias is zeroed (unless accumulate is set). Errors as layer_linear.
  */
 typedef struct layer_activation_grad_args {
   const void *dout; /* m x n, bf16 */
@@ -224,8 +233,9 @@ gemm_status layer_activation_backward(const layer_activation_grad_args *args, la
 /*
  * dx_mk = sum_n dpre_mn w_nk and dw_nk = sum_m dpre_mn x_mk (+ dw_nk with
  * `accumulate`, read in dw's type). dpre, x and w are bf16; dx and dw (NULL: not wanted)
- * fp32 or bf16. x is only read for dw, w only for dx. One launch each. With
- * m == 0 dw is zeroed (unless accumulate is set). Errors as layer_linear.
+ * fp32 or bf16. x is only read for dw, w only for dx. One launch each, or
+ * two where k is split. With m == 0 dw is zeroed (unless accumulate is set).
+ * Errors as layer_linear.
  */
 typedef struct layer_linear_grad_args {
   const void *dpre; /* m x n */

@@ -402,6 +402,11 @@ gemm_status noalloc_setup(int dev, hipStream_t s, NoallocDevice **out) {
 
 namespace ptg {
 
+float *plan_workspace(gemm_tile_cfg p, int64_t *floats) {
+  *floats = p->ws_tiles * p->desc.bm * p->desc.bn;
+  return p->d_ws;
+}
+
 gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s) {
   const int64_t units = form == kFormNTE4m3 ? 2 : 1;  // values per 16-bit unit along k
   const int64_t K = a.k / units;
@@ -421,9 +426,6 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, in
   op.ep = a.ep;
   op.lda = (int32_t)(a.lda / units);
   op.ldb = (int32_t)(a.ldb / units);
-  p->last_tile_start.assign(1, 0);
-  p->last_k.assign(1, (int32_t)K);
-  p->last_unit_map.clear();
   if (split > 1 && (tm * tn - split_base) * split > p->ws_tiles) return GEMM_E_SHAPE;
   const gemm_status st = launch(p, GEMM_SCHED_DYNAMIC, false, args, tm * tn, K, s, &op, form, split, split_base);
   if (st != GEMM_OK || split <= 1) return st;

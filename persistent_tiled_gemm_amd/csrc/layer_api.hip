@@ -3,9 +3,9 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdio>
 #include <cstring>
 #include <new>
-#include <string>
 
 #include "layer_internal.hpp"
 #include "ptg_layer.h"
@@ -18,21 +18,21 @@ struct layer_plan {
   int device = 0;
   int cu_count = 0;
   gemm_tile_cfg tiles256 = nullptr, tiles128 = nullptr;  // the tiled products' plans
-  float *d_ws = nullptr;  // partial sums
+  float *ws = nullptr;             // partial sums: the 256 x 256 plan's workspace
+  int64_t ws_floats = 0;
   uint32_t *d_arrivals = nullptr;  // arrival counts of the few-row product's shared tiles, zero between calls
   hipEvent_t stream_switch = nullptr;
   hipStream_t last_stream = nullptr;
   bool has_run = false;
-  std::string last_error;
+  char last_error[256] = "";  // of a fixed size: no call of the C ABI may throw
 };
 
 namespace {
 
-constexpr int64_t kWsFloats = 16 << 20;  // 64 MiB: 16 partial rows of the widest column sum
-constexpr int64_t kArrivals = 4096;      // a tile whose k is shared is one of fewer than 16 waves x CUs / 4
+constexpr int64_t kArrivals = 4096;  // a tile whose k is shared is one of fewer than 16 waves x CUs / 4
 
 gemm_status hip_fail(layer_plan *p, hipError_t e, const char *what) {
-  if (p) p->last_error = std::string(what) + ": " + hipGetErrorString(e);
+  if (p) std::snprintf(p->last_error, sizeof(p->last_error), "%s: %s", what, hipGetErrorString(e));
   return GEMM_E_HIP;
 }
 
@@ -166,15 +166,18 @@ gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStr
   const TileChoice c = choose_tiles(a, form, p->cu_count);
   gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
   gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
-  if (st == GEMM_E_HIP) p->last_error = gemm_last_hip_error(t);
+  if (st == GEMM_E_HIP) std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));
   return st;
 }
 
 // The stride the kernels get: a matrix of one row has its row's length, whatever the caller said.
 int64_t stride_of(int64_t ld, int64_t m, int64_t n) { return m > 1 && n > 0 ? ld : std::max<int64_t>(n, 8); }
 
-// Partial sums of n columns over at most `wanted` rows: as many rows as the workspace holds.
-int64_t partial_rows(int64_t wanted, int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(wanted, kWsFloats / std::max<int64_t>(n, 1))); }
+// Partial sums of n columns over at most `wanted` rows: as many rows as the
+// workspace holds (a chunk of 256 x 256 a CU: 16 rows of the widest matrix).
+int64_t partial_rows(const layer_plan *p, int64_t wanted, int64_t n) {
+  return std::max<int64_t>(1, std::min<int64_t>(wanted, p->ws_floats / std::max<int64_t>(n, 1)));
+}
 
 }  // namespace
 
@@ -195,11 +198,6 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
   if (!p) return GEMM_E_NOMEM;
   p->device = device;
   p->cu_count = cus;
-  if (hipMalloc(&p->d_ws, sizeof(float) * (size_t)kWsFloats) != hipSuccess) {
-    p->d_ws = nullptr;
-    layer_destroy(p);
-    return GEMM_E_NOMEM;
-  }
   if (hipMalloc(&p->d_arrivals, sizeof(uint32_t) * (size_t)kArrivals) != hipSuccess) {
     p->d_arrivals = nullptr;
     layer_destroy(p);
@@ -218,6 +216,7 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
     layer_destroy(p);
     return st;
   }
+  p->ws = ptg::plan_workspace(p->tiles256, &p->ws_floats);
   *out = p;
   return GEMM_OK;
 }
@@ -228,7 +227,6 @@ gemm_status layer_destroy(layer_cfg p) {
   (void)gemm_destroy(p->tiles256);
   (void)gemm_destroy(p->tiles128);
   if (p->stream_switch) (void)hipEventDestroy(p->stream_switch);
-  if (p->d_ws) (void)hipFree(p->d_ws);
   if (p->d_arrivals) (void)hipFree(p->d_arrivals);
   delete p;
   return GEMM_OK;
@@ -243,13 +241,13 @@ gemm_status layer_sync(layer_cfg p) {
   for (gemm_tile_cfg t : {p->tiles256, p->tiles128}) {
     const gemm_status one = gemm_sync(t);
     if (one == GEMM_OK) continue;
-    p->last_error = gemm_last_hip_error(t);
+    std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));
     st = one;
   }
   return st;
 }
 
-const char *layer_last_hip_error(layer_cfg p) { return p ? p->last_error.c_str() : ""; }
+const char *layer_last_hip_error(layer_cfg p) { return p ? p->last_error : ""; }
 
 gemm_status layer_rmsnorm(const layer_rmsnorm_args *a, void *stream) {
   if (!a) return GEMM_E_INVALID_ARG;
@@ -317,7 +315,7 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p
     k.weight = a->weight;
     k.dsum = a->dsum;
     k.dx = a->dx;
-    k.partial = a->dweight ? p->d_ws : nullptr;
+    k.partial = a->dweight ? p->ws : nullptr;
     k.lddy = stride_of(a->lddy, a->m, a->n);
     k.lds = stride_of(a->lds, a->m, a->n);
     k.lddsum = stride_of(a->lddsum, a->m, a->n);
@@ -331,12 +329,12 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p
     // at most 8 x CUs groups of rows of at most 1024, or 2 x CUs of 4096, or CUs
     // of 32768 elements: within the workspace
     rows = ptg::rmsnorm_partial_rows(k.m, k.n, p->cu_count);
-    if ((int64_t)rows * a->n > kWsFloats) return GEMM_E_SHAPE;
+    if ((int64_t)rows * a->n > p->ws_floats) return GEMM_E_SHAPE;
     e = ptg::launch_rmsnorm_backward(k, p->cu_count, s);
     if (e != hipSuccess) return hip_fail(p, e, "rmsnorm backward");
   }
   if (a->dweight) {
-    e = ptg::launch_column_sum(p->d_ws, rows, (int32_t)a->n, a->dweight, a->accumulate, s);
+    e = ptg::launch_column_sum(p->ws, rows, (int32_t)a->n, a->dweight, a->accumulate, s);
     if (e != hipSuccess) return hip_fail(p, e, "column sum");
   }
   return GEMM_OK;
@@ -388,8 +386,8 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.act = a->activation;
   if (ptg::rows_preferred(k, e8)) {
     int64_t tiles = 0;
-    if (ptg::rows_partial_floats(k, e8, p->cu_count, &tiles) > kWsFloats || tiles > kArrivals) return GEMM_E_SHAPE;
-    hipError_t e = ptg::launch_rows(k, e8, p->d_ws, p->d_arrivals, p->cu_count, s);
+    if (ptg::rows_partial_floats(k, e8, p->cu_count, &tiles) > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
+    hipError_t e = ptg::launch_rows(k, e8, p->ws, p->d_arrivals, p->cu_count, s);
     return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
   }
   return run_tiles(p, k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
@@ -420,7 +418,7 @@ gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer
     k.dout = a->dout;
     k.pre = a->pre;
     k.dpre = a->dpre;
-    k.partial = a->dbias ? p->d_ws : nullptr;
+    k.partial = a->dbias ? p->ws : nullptr;
     k.lddo = stride_of(a->lddo, a->m, a->n);
     k.ldp = stride_of(a->ldp, a->m, a->n);
     k.lddp = stride_of(a->lddp, a->m, a->n);
@@ -429,14 +427,14 @@ gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer
     k.act = a->activation;
     // eight workgroups a CU, each with 16 rows at least (four a wave)
     const int64_t strips = ceil_div(a->n, 512);
-    groups = partial_rows(std::min<int64_t>(ceil_div((int64_t)p->cu_count * 8, strips), ceil_div(a->m, 16)), a->n);
+    groups = partial_rows(p, std::min<int64_t>(ceil_div((int64_t)p->cu_count * 8, strips), ceil_div(a->m, 16)), a->n);
     k.rows_per_group = (int32_t)ceil_div(a->m, groups);
     groups = ceil_div(a->m, k.rows_per_group);
     e = ptg::launch_activation_backward(k, (int)groups, s);
     if (e != hipSuccess) return hip_fail(p, e, "activation backward");
   }
   if (a->dbias) {
-    e = ptg::launch_column_sum(p->d_ws, (int)groups, (int32_t)a->n, a->dbias, a->accumulate, s);
+    e = ptg::launch_column_sum(p->ws, (int)groups, (int32_t)a->n, a->dbias, a->accumulate, s);
     if (e != hipSuccess) return hip_fail(p, e, "column sum");
   }
   return GEMM_OK;

@@ -103,6 +103,8 @@ hipError_t launch_product(int tile_edge, int form, const KernelArgs &args, const
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s);
+// A plan's split-tail workspace, for other partial sums between its runs.
+float *plan_workspace(gemm_tile_cfg plan, int64_t *floats);
 // The product as a run of a GEMM plan: its tiles and dynamic scheduler; the tiles
 // from split_base on are split into `split` K-chunks each (1: none), which a
 // second kernel joins. The caller orders runs on different streams.
