@@ -136,9 +136,16 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
   __shared__ float lds[2][2][16];
   const int32_t t = (int32_t)threadIdx.x % T;
   const int32_t group = (int32_t)blockIdx.x * kGroups + (int32_t)threadIdx.x / T;
+  // First column of the thread's chunk c. With four chunks it is worked out where it
+  // is used: kept, with the addresses that follow from it, it would not fit.
+  auto at = [&](int c) -> int32_t {
+    int32_t mine = t;
+    if constexpr (T == 1024 && NCH == 4) asm volatile("" : "+v"(mine)::"memory");
+    return (c * T + mine) * 8;
+  };
   f32x8 kept[NCH], dw[NCH];  // the thread's columns of weight and its share of dweight
   auto weight = [&](int c) -> f32x8 {
-    const int32_t j = (c * T + t) * 8;
+    const int32_t j = at(c);
     if (j < a.n && a.weight) return load8_as(a.weight, a.weight_type, j);
     return f32x8{1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
   };
@@ -168,7 +175,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
   const float inv_n = 1.0f / (float)a.n;
   // registers: 16 a chunk for weight and dweight, kRaw for a row as loaded. A
   // workgroup of 1024 threads has 128 a thread: long rows are held without the
-  // next one, or not at all, nor the weight (the second look comes from the caches).
+  // next one, or not at all, nor the weight (the second look comes from the caches:
+  // 1000 x 32768, 95 us, 2.7 TB/s of what has to be moved).
   constexpr int kRaw = NCH * (4 * (int)sizeof(TS) + 2 * (int)sizeof(TD));
   constexpr bool kAhead = T < 1024 || NCH * 16 + 2 * kRaw <= 72, kHold = T < 1024 || NCH * 16 + kRaw <= 64;
   int buf = 0;
@@ -187,10 +195,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
         s = widen(f.s[c]);
         d = widen(f.d[c]);
       } else {
-        asm volatile("" ::: "memory");  // one chunk at a time
-        if ((c * T + t) * 8 < a.n) {
-          s = load8(sp + (c * T + t) * 8);
-          d = load8(dp + (c * T + t) * 8);
+        const int32_t j = at(c);
+        if (j < a.n) {
+          s = load8(sp + j);
+          d = load8(dp + j);
         }
       }
       const f32x8 w = kHold ? kept[c] : weight(c);
@@ -199,6 +207,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
         ss += s[e] * s[e];
         gs += d[e] * w[e] * s[e];
       }
+      if constexpr (!kHold) asm volatile("" : "+v"(ss), "+v"(gs));  // before the next chunk is asked for
     }
     if (kAhead && row + groups < a.m) ask(next, row + groups);
     ss = wave_sum(ss);
@@ -225,9 +234,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
     const float k = r * r * (gs * inv_n) * r;  // r h_j mean(g h) = s_j k
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int32_t j = (c * T + t) * 8;
+      const int32_t j = at(c);
       f32x8 s = {}, d = {};
-      if constexpr (!kHold) asm volatile("" ::: "memory");
       const f32x8 w = kHold ? kept[c] : weight(c);
       if constexpr (kHold) {
         s = widen(f.s[c]);
@@ -242,6 +250,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_backward_kernel
         store8((TS *)a.dx + row * a.lddx + j, dx);
       }
       dw[c] += d * (s * r);
+      if constexpr (!kHold) asm volatile("" : "+v"(dw[c]));
     }
   }
   if (a.partial) {

@@ -100,7 +100,7 @@ def test_no_product_kernel_uses_scratch(asm):
     assert not [k for k, s in sizes if int(s) != 0]
 
 
-@pytest.mark.parametrize("source", ["rows_kernel.hip", "act_kernel.hip"])
+@pytest.mark.parametrize("source", ["rows_kernel.hip", "act_kernel.hip", "norm_kernel.hip"])
 def test_no_other_kernel_uses_scratch(tmp_path, source):
     sizes = re.findall(r"\.amdhsa_kernel (\S+).*?\.amdhsa_private_segment_fixed_size (\d+)", compile_to_asm(tmp_path, source), re.S)
     assert sizes and not [k for k, s in sizes if int(s) != 0]
