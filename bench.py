@@ -32,8 +32,8 @@ if ROOT not in sys.path:
 PEAK_BF16_TFLOPS = 2500.0   # MI355X dense bf16 MFMA
 PEAK_HBM_GBS = 8000.0       # MI355X HBM3E
 METRIC = "bf16 GEMM TFLOP/s and % MFMA peak; tail makespan static vs dynamic"
-KERNEL_SOURCES = ("persistent_tiled_gemm_amd/csrc/gemm_kernel.hip", "persistent_tiled_gemm_amd/csrc/ptg_device.hpp",
-                  "persistent_tiled_gemm_amd/csrc/ptg_internal.hpp")
+KERNEL_SOURCES = ("persistent_tiled_gemm_amd/csrc/gemm_kernel.hip", "persistent_tiled_gemm_amd/csrc/gemm_body.hpp",
+                  "persistent_tiled_gemm_amd/csrc/ptg_device.hpp", "persistent_tiled_gemm_amd/csrc/ptg_internal.hpp")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemm_square_8192_traffic.json")
 
 

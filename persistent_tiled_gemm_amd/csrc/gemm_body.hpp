@@ -643,8 +643,9 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     // Wide loads: a wave-load moves eight rows of 128 bytes (whole cache lines, where
     // a k-step alone takes 64 bytes of 16 rows: from L2, 256 CUs at once, 103 ->
     // 133 GB/s a CU, and with rows that do not start on 64-byte lines 46 -> 99).
-    // Chunk c of row r of a pair's 128-byte rows sits in slot c ^ ((r >> 1) & 7). Load j < A_LOADS 2 of a pair is A's,
-    // the rest B's; rows step by 32 a load, so a lane's chunk is the same for all.
+    // Chunk c of row r of a pair's 128-byte rows sits in slot c ^ ((r >> 1) & 7).
+    // Of a pair's loads the first 2 A_LOADS are A's, the rest B's; rows step by 32 a
+    // load, so a lane's chunk is the same for all.
     constexpr int kWideA = WA ? 2 * CF::A_LOADS : 0, kWideB = WB ? 2 * CF::B_LOADS : 0, kWide = kWideA + kWideB;
     // Rows past the matrix are out of the resource's range (its record count is the
     // bytes of the rows there are), so an offset is one per-lane base plus a
@@ -952,14 +953,17 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // the loads that go out at place `at` of `places` in a k-step: the narrow ones
         // of step kt + NST, and in the second step of a pair, whose fragments have
         // all been read, the wide ones of the pair NST steps after it. Those must
-        // have landed when the next even step but NST - 4 ends: they go out in the
-        // first half of theirs. (Waits below: all loads up to that step's narrow ones,
-        // which follow its wide ones, may be in flight.)
+        // have landed when the next even step but NST - 4 ends, but evenly spread over
+        // their step they land soonest all the same: 8192^3 NT, one every four MFMAs
+        // 728 us, every third 733, every second 770, each 794. Beside narrow loads
+        // they take the first half of the step and those the second. (Waits below: all
+        // loads up to that step's narrow ones, which follow its wide ones, may be in
+        // flight.)
         auto step_loads = [&](auto fast, bool odd, int32_t kt, int st, int at, int places, const i32x4 &ra, const i32x4 &rb, const i32x4 &wa,
                               const i32x4 &wb, int32_t wide_kt) {
           const uint32_t lbase = lds_addr(smem);
           if constexpr (WIDE) {
-            const int every = places / (2 * kWide), j = at / every;
+            const int every = places / (kNarrow > 0 ? 2 * kWide : kWide), j = at / every;
             if (odd && at % every == 0 && j < kWide)
               load16_to_lds(j < kWideA ? wa : wb, lbase + wide_dst(j, st),
                             decltype(fast)::value ? wide_voff(j) : wide_voff_tail(j, wide_kt));

@@ -112,7 +112,7 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 //     (their stages fill its LDS), e4m3 0.41; TN 0.23, and with two tiles a CU
 //     together 0.44; 8 to fill and drain;
 //   - a k-step of a 256 x 256 tile: from the first to the second figure as more
-//     CUs work (power and memory shared): 0.48 to 0.64, e4m3 0.9 to 1.12; 18 to
+//     CUs work (power and memory shared): 0.48 to 0.62, e4m3 0.9 to 1.12; 18 to
 //     fill and drain;
 //   - rows of a k-contiguous operand that do not start on 64-byte lines: 128 x 128
 //     steps 1.4 times as long, 256 x 256 ones 1.35 (NN, with one such operand, 1.1;
@@ -138,7 +138,7 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
     auto run = [&](int64_t units, int64_t steps) {
       const double load = (double)units / (double)cus, rounds = (double)ceil_div(units, cus);
       double step;
-      if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.16 * load * load) : (e8 ? 1.12 : 0.64) * rounds);
+      if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.14 * load * load) : (e8 ? 1.12 : 0.62) * rounds);
       else if (tn) step = load <= 1.0 ? 0.23 : std::max(0.44, 0.23 * load);
       else step = slow128 * (e8 ? 0.41 : 0.30) * rounds;
       return (double)steps * step;

@@ -109,10 +109,11 @@ struct ProductOp {
   // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step
   // ahead of their MFMAs (the 128 x 128 tile's other form, 32 x 32 blocks read half
   // a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192). k-contiguous
-  // operands come two k-steps at a time (8192^3 NT 759 -> 742 us, NN 734 -> 700;
-  // 1000 x 4104 x 2056 61 -> 47); a pair's loads then have one to two steps to land
-  // in a ring of four stages, enough for the 256 x 256 tile's steps but not for the
-  // shorter ones of 128 x 128, which get eight (and one workgroup a CU).
+  // operands come two k-steps at a time (8192^3 NT 759 -> 742 us, and 785 -> 730 with
+  // their loads spread over the step; NN 734 -> 700; 1000 x 4104 x 2056 61 -> 47); a
+  // pair's loads then have one to two steps to land in a ring of four stages, enough
+  // for the 256 x 256 tile's steps but not for the shorter ones of 128 x 128, which
+  // get eight (and one workgroup a CU).
   template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16, EDGE == 128 && !AT ? 8 : 4>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
