@@ -249,7 +249,7 @@ void plan_units(const gemm_plan *p, bool grouped, int32_t mode, int64_t tiles, i
   *items = tiles - r + r * S;
 }
 
-// product, form: a layer operator's product instead of the plain GEMM (dynamic mode, one problem).
+// product, form: a layer operator's product instead of the plain GEMM (dynamic or non-persistent, one problem).
 gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, int64_t tiles, int64_t K,
                    hipStream_t s, const ptg::ProductOpArgs *product = nullptr, int form = 0, int32_t split = 1, int64_t split_base_ = 0) {
   if (mode < GEMM_SCHED_NONPERSISTENT || mode > GEMM_SCHED_DYNAMIC) return GEMM_E_INVALID_ARG;
@@ -323,7 +323,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
     args.self_clean = 0;
   }
   args.log = p->d_log;
-  e = product ? ptg::launch_product(p->desc.bm, form, args, *product, (int)grid, s)
+  e = product ? ptg::launch_product(p->desc.bm, form, mode, args, *product, (int)grid, s)
               : ptg::launch_gemm(p->desc.bm, mode, grouped, p->desc.b_layout == 1, args, (int)grid, p->dyn_lds, s);
   if (e != hipSuccess) return hip_fail(p, e, "kernel launch");
   if (!captured) ++p->runs;
@@ -427,7 +427,10 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, in
   op.lda = (int32_t)(a.lda / units);
   op.ldb = (int32_t)(a.ldb / units);
   if (split > 1 && (tm * tn - split_base) * split > p->ws_tiles) return GEMM_E_SHAPE;
-  const gemm_status st = launch(p, GEMM_SCHED_DYNAMIC, false, args, tm * tn, K, s, &op, form, split, split_base);
+  // one wave of workgroups needs no scheduler
+  const int64_t items = split > 1 ? split_base + (tm * tn - split_base) * split : tm * tn;
+  const int32_t mode = items <= (int64_t)p->cu_count * product_workgroups(p->desc.bm, form) ? GEMM_SCHED_NONPERSISTENT : GEMM_SCHED_DYNAMIC;
+  const gemm_status st = launch(p, mode, false, args, tm * tn, K, s, &op, form, split, split_base);
   if (st != GEMM_OK || split <= 1) return st;
   const hipError_t e = launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, (int32_t)split_base, (int32_t)(tm * tn - split_base),
                                              split, s);

@@ -110,7 +110,7 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // form; within about 15% of the times):
 //   - a k-step of a 128 x 128 tile: NT and NN 0.30 with one tile a CU at a time
 //     (their stages fill its LDS), e4m3 0.41; TN 0.23, and with two tiles a CU
-//     together 0.44; 8 to fill and drain;
+//     together 0.44; 8 to fill and drain, 2 less where one wave takes every unit;
 //   - a k-step of a 256 x 256 tile: from the first to the second figure as more
 //     CUs work (power and memory shared): 0.48 to 0.62, e4m3 0.9 to 1.12; 18 to
 //     fill and drain;
@@ -121,9 +121,9 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 //     0.02 a chunk of 128 x 128, 0.06 of 256 x 256.
 // Both sides where it matters (NT): 512 x 8192 x 8192, 256 tiles of 128: 79 us, 64
 // of 256 in 4 chunks: 76; 1024 x 8192 x 8192, 512 of 128: 155, 128 of 256: 154, in
-// 2 chunks: 118; 1024 x 4096 x 4096, 256 of 128: 47, 64 of 256 in 4 chunks: 54;
-// 256 x 4096 x 4096, 64 of 128: 43, in 4 chunks: 26; 100 x 1024 x 8192, 8 of 128:
-// 62, in 8 chunks: 21; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
+// 2 chunks: 118; 1024 x 4096 x 4096, 256 of 128: 44, 64 of 256 in 4 chunks: 54;
+// 256 x 4096 x 4096, 64 of 128: 43, in 4 chunks: 24; 100 x 1024 x 8192, 8 of 128:
+// 62, in 8 chunks: 20; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
 // last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55.
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN;
@@ -143,8 +143,10 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
       else step = slow128 * (e8 ? 0.41 : 0.30) * rounds;
       return (double)steps * step;
     };
-    const double fixed = edge == 256 ? 18.0 : 8.0, join = edge == 256 ? 0.06 : 0.02;
-    const double whole = fixed + run(T, nk);
+    const int64_t resident = cus * ptg::product_workgroups(edge, form);
+    auto fixed = [&](int64_t units) { return (edge == 256 ? 18.0 : 8.0) - (units <= resident ? 2.0 : 0.0); };
+    const double join = edge == 256 ? 0.06 : 0.02;
+    const double whole = fixed(T) + run(T, nk);
     if (whole < best.us) best = {edge, 1, 0, whole};
     // all tiles, or those of the partial last wave
     const int64_t waves = T / cus * cus;
@@ -153,7 +155,7 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
       if (r == 0 || (base != 0 && edge == 128 && tn)) continue;  // (TN: small tiles' last wave shares the CUs of the wave before)
       const double before = base ? run(base, nk) : 0.0;
       for (int32_t S = 2; S <= 32 && r * S <= slots && nk / S >= 4; ++S) {
-        const double us = fixed + before + run(r * S, ceil_div(nk, S)) + 4.0 + join * (double)(r * S);
+        const double us = fixed(base + r * S) + before + run(r * S, ceil_div(nk, S)) + 4.0 + join * (double)(r * S);
         if (us < best.us) best = {edge, S, base, us};
       }
       if (base == waves) break;  // fewer tiles than CUs: both are the same

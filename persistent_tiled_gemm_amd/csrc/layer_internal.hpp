@@ -99,7 +99,10 @@ struct ProductOpArgs {
   EpilogueArgs ep;
   int32_t lda, ldb;
 };
-hipError_t launch_product(int tile_edge, int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+// Workgroups of the tiled product that a CU holds at once.
+constexpr int product_workgroups(int tile_edge, int form) { return tile_edge == 128 && form == kFormTN ? 2 : 1; }
+// mode: kDynamic or kNonPersistent
+hipError_t launch_product(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s);

@@ -187,9 +187,12 @@ struct ProductOp {
   }
 };
 
-template <int EDGE, int FORM>
-__global__ __launch_bounds__(256, EDGE == 128 && FORM == kFormTN ? 2 : 1) void ptg_product_kernel(const ProductKernelArgs a) {
-  gemm_body<EDGE, EDGE, kDynamic, false, ProductOp<FORM>>(a.gemm, a.op);
+// MODE: kDynamic, or kNonPersistent where every unit's workgroup is resident at
+// once: there is then nothing to claim, and the first claim's round trip is saved
+// (1024^3 in 128 x 128 tiles 13.6 -> 11.3 us).
+template <int EDGE, int FORM, int MODE>
+__global__ __launch_bounds__(256, product_workgroups(EDGE, FORM)) void ptg_product_kernel(const ProductKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, ProductOp<FORM>>(a.gemm, a.op);
 }
 
 // The tiles that were split along k: their chunks' sums, added in chunk order,
@@ -231,22 +234,27 @@ hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &o
   return tile_edge == 256 ? launch_reduce_edge<256>(a, tiles, form == kFormNTE4m3, s) : launch_reduce_edge<128>(a, tiles, form == kFormNTE4m3, s);
 }
 
-template <int EDGE>
-static hipError_t launch_edge(int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+template <int EDGE, int MODE>
+static hipError_t launch_mode(int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
   const dim3 g((uint32_t)grid), b(256);
   const ProductKernelArgs a = {args, op};
   switch (form) {
-    case kFormNT: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNT>), g, b, 0, s, a); break;
-    case kFormNN: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNN>), g, b, 0, s, a); break;
-    case kFormTN: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormTN>), g, b, 0, s, a); break;
-    case kFormNTE4m3: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNTE4m3>), g, b, 0, s, a); break;
+    case kFormNT: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNT, MODE>), g, b, 0, s, a); break;
+    case kFormNN: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNN, MODE>), g, b, 0, s, a); break;
+    case kFormTN: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormTN, MODE>), g, b, 0, s, a); break;
+    case kFormNTE4m3: hipLaunchKernelGGL((ptg_product_kernel<EDGE, kFormNTE4m3, MODE>), g, b, 0, s, a); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }
 
-hipError_t launch_product(int tile_edge, int form, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
-  return tile_edge == 256 ? launch_edge<256>(form, args, op, grid, s) : launch_edge<128>(form, args, op, grid, s);
+template <int EDGE>
+static hipError_t launch_edge(int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+  return mode == kDynamic ? launch_mode<EDGE, kDynamic>(form, args, op, grid, s) : launch_mode<EDGE, kNonPersistent>(form, args, op, grid, s);
+}
+
+hipError_t launch_product(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+  return tile_edge == 256 ? launch_edge<256>(form, mode, args, op, grid, s) : launch_edge<128>(form, mode, args, op, grid, s);
 }
 
 }  // namespace ptg

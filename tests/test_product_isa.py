@@ -15,7 +15,7 @@ from tests import test_kernel_isa as isa
 pytestmark = isa.pytestmark
 
 FORMS = {0: "NT", 1: "NN", 2: "TN", 3: "NT e4m3"}
-CASES = [(edge, form) for edge in (256, 128) for form in FORMS]
+CASES = [(edge, form, mode) for edge in (256, 128) for form in FORMS for mode in (2, 0)]  # dynamic, non-persistent
 
 
 def compile_to_asm(tmp, source):
@@ -32,8 +32,8 @@ def asm(tmp_path_factory):
     return compile_to_asm(tmp_path_factory.mktemp("isa"), "product_kernel.hip")
 
 
-def kernel_text(asm_text, edge, form):
-    i = asm_text.index(f"\n_ZN3ptg18ptg_product_kernelILi{edge}ELi{form}EEE")
+def kernel_text(asm_text, edge, form, mode):
+    i = asm_text.index(f"\n_ZN3ptg18ptg_product_kernelILi{edge}ELi{form}ELi{mode}EEE")
     i = asm_text.index(":", i)
     return asm_text[i:asm_text.index(".Lfunc_end", i)]
 
@@ -43,13 +43,13 @@ def loops(text):
     return [b for b in blocks if sum(x.startswith("v_mfma") for x in b) > 0]
 
 
-@pytest.mark.parametrize("edge,form", CASES)
-def test_main_loop_is_one_block_without_copies(asm, edge, form):
+@pytest.mark.parametrize("edge,form,mode", CASES)
+def test_main_loop_is_one_block_without_copies(asm, edge, form, mode):
     step = (64 if edge == 256 else 16) * (2 if form == 3 else 1)  # MFMAs a k-step
-    bodies = loops(kernel_text(asm, edge, form))
+    bodies = loops(kernel_text(asm, edge, form, mode))
     counts = [sum(x.startswith("v_mfma") for x in b) for b in bodies]
-    # four-step and two-step trips (e4m3: the two-step ones are the K tail's), before and after the claim goes out
-    assert sorted(set(counts)) == [2 * step, 4 * step] and counts.count(4 * step) == 2, counts
+    # four-step and two-step trips (e4m3: the two-step ones are the K tail's), dynamic: before and after the claim goes out
+    assert sorted(set(counts)) == [2 * step, 4 * step] and counts.count(4 * step) == (2 if mode == 2 else 1), counts
     for body, n in zip(bodies, counts):
         assert not [x for x in body if x.startswith(("v_accvgpr", "scratch_"))]
         assert sum(x.startswith("s_barrier") for x in body) == n // step
@@ -58,11 +58,11 @@ def test_main_loop_is_one_block_without_copies(asm, edge, form):
             assert sum(x.startswith("v_") and not x.startswith("v_mfma") for x in body) <= 4
 
 
-@pytest.mark.parametrize("edge,form", CASES)
-def test_mfma_hazard_distances(asm, edge, form):
+@pytest.mark.parametrize("edge,form,mode", CASES)
+def test_mfma_hazard_distances(asm, edge, form, mode):
     """An MFMA result reaches any other reader only after at least the wait states the longest MFMA needs, and a
     vector write reaches an MFMA that reads it only after the two wait states that takes."""
-    f = isa.instructions(kernel_text(asm, edge, form))
+    f = isa.instructions(kernel_text(asm, edge, form, mode))
     first = next(n for n, x in enumerate(f) if x.startswith("v_mfma"))
     last_mfma, last_valu, pos, result, operand = {}, {}, 0, None, None
     for x in f[first - 64:]:
@@ -108,5 +108,5 @@ def test_no_other_kernel_uses_scratch(tmp_path, source):
 
 def test_small_tiles_leave_room_for_their_neighbours(asm):
     """TN's 128 x 128 tiles run two workgroups a CU: at most 256 registers (vector and accumulator) a lane."""
-    m = re.search(r"\.amdhsa_kernel _ZN3ptg18ptg_product_kernelILi128ELi2E\S+.*?\.amdhsa_next_free_vgpr (\d+)", asm, re.S)
+    m = re.search(r"\.amdhsa_kernel _ZN3ptg18ptg_product_kernelILi128ELi2ELi2E\S+.*?\.amdhsa_next_free_vgpr (\d+)", asm, re.S)
     assert int(m.group(1)) <= 256
