@@ -11,6 +11,7 @@ Modules
   sched_model discrete-event model of the three tile schedulers (non-persistent,
               static grid-stride, dynamic claim) over execution slots.
   ring_model  exhaustive interleaving checker for the claim / prefetch-ring protocol.
+  layer_ref   the layer operators' definitions in float64, and their error bounds.
   ownership   checks of a per-tile ownership log (exactly once, per-mode owner rules).
 
 Every function cites the passage of the source pages it follows. A page is named

@@ -11,6 +11,11 @@ gemm_test_preset_gate, gemm_test_stream_cu_mask, gemm_test_stream_destroy,
 gemm_test_spoiler, gemm_mfma_probe, gemm_hbm_probe. Tensors are torch device tensors: A and B
 bf16 (or int16 / uint16 views of bf16 bits), C float32, all contiguous; streams
 are torch.cuda streams (default: the current stream).
+
+The layer operators (include/ptg_layer.h) are bound in layer.py and re-exported
+here: layer_create, layer_destroy, layer_sync, layer_last_hip_error,
+layer_rmsnorm, layer_rmsnorm_backward, layer_linear, layer_activation_backward,
+layer_linear_backward.
 """
 
 from __future__ import annotations

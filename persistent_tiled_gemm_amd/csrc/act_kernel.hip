@@ -1,5 +1,6 @@
 // The activation's gradient: dpre = dout act'(pre), and its column sums (the
-// bias's gradient). Bound by memory: 6 bytes an element.
+// bias's gradient). Bound by memory: 6 bytes an element (8191 x 8192, gelu_tanh:
+// 79 us, 5.1 TB/s; with the column sums' launch 83.5. One row at a time: 90).
 //
 // A workgroup covers 512 columns (64 threads of eight, so a wave reads 1 KiB of
 // a row) and a range of rows, one row per wave at a time. A thread's columns do

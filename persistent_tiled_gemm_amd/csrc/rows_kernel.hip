@@ -10,7 +10,9 @@
 // registers: the next batch's loads are under way while one is multiplied. x
 // (whose rows the caches hold) is read beside w the same way. The waves' sums
 // meet in LDS, the workgroups' (S > 1) in the plan's workspace: the last one to
-// arrive adds the S parts in order and finishes the tile.
+// arrive adds the S parts in order and finishes the tile. 8192^2: one row in bf16
+// 26.8 us (5.0 TB/s of w, and some 4 us of launch, first loads and join in it), 24
+// rows in e4m3 21.7 (3.1 TB/s).
 #include <algorithm>
 
 #include "layer_device.hpp"
@@ -56,7 +58,8 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
   // Each wave starts part-way into its range and wraps around (a phase from its
   // place in the grid; the order of a sum depends on that alone). Started at
   // their first steps, waves whose ranges lie a multiple of 4 KiB apart read the
-  // same few memory channels at a time: 4096 x 16384, one row, 39.7 us.
+  // same few memory channels at a time: 4096 x 16384, one row, 39.7 us
+  // against 27.4.
   const int32_t count = s1 - s0;
   const int32_t rot = count > 1 ? (int32_t)((((tile * 8u + wave) * 2654435761u) >> 16) % (uint32_t)count & ~1u) : 0;
 
