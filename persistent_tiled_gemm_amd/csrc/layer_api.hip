@@ -108,15 +108,15 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // The choice is the least of the times that these fits give, in microseconds (256
 // CUs; measured over m = 100 .. 4096, n = 1024 .. 16384, k = 768 .. 8192 in each
 // form; within about 15% of the times):
-//   - a k-step of a 128 x 128 tile: NT and NN 0.30 with one tile a CU at a time
+//   - a k-step of a 128 x 128 tile: NT and NN 0.28 with one tile a CU at a time
 //     (their stages fill its LDS), e4m3 0.41; TN 0.23, and with two tiles a CU
 //     together 0.44; 8 to fill and drain, 2 less where one wave takes every unit;
 //   - a k-step of a 256 x 256 tile: from the first to the second figure as more
-//     CUs work (power and memory shared): 0.48 to 0.62, e4m3 0.9 to 1.12; 18 to
+//     CUs work (power and memory shared): 0.48 to 0.66, e4m3 0.9 to 1.12; 18 to
 //     fill and drain;
 //   - rows of a k-contiguous operand that do not start on 64-byte lines: 128 x 128
-//     steps 1.4 times as long, 256 x 256 ones 1.35 (NN, with one such operand, 1.1;
-//     e4m3, which takes half the bytes a product, 1.1);
+//     steps 1.33 times as long, 256 x 256 ones 1.13 (NN, with one such operand, 1.05;
+//     e4m3, which takes half the bytes a product, 1.1 in both);
 //   - splitting: 4 for the second launch, and each chunk's sums written and read,
 //     0.02 a chunk of 128 x 128, 0.06 of 256 x 256.
 // Both sides where it matters (NT): 512 x 8192 x 8192, 256 tiles of 128: 79 us, 64
@@ -129,7 +129,7 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN;
   const int64_t nk = ceil_div(e8 ? a.k / 2 : a.k, 32), line = e8 ? 64 : 32;
   const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (form != ptg::kFormNN && a.ldb % line != 0));
-  const double slow128 = off_line ? (e8 ? 1.1 : 1.4) : 1.0, slow256 = off_line ? (form == ptg::kFormNT ? 1.35 : 1.1) : 1.0;
+  const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : form == ptg::kFormNT ? 1.13 : 1.05) : 1.0;
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
     const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
@@ -138,9 +138,9 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
     auto run = [&](int64_t units, int64_t steps) {
       const double load = (double)units / (double)cus, rounds = (double)ceil_div(units, cus);
       double step;
-      if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.14 * load * load) : (e8 ? 1.12 : 0.62) * rounds);
+      if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.18 * load * load) : (e8 ? 1.12 : 0.66) * rounds);
       else if (tn) step = load <= 1.0 ? 0.23 : std::max(0.44, 0.23 * load);
-      else step = slow128 * (e8 ? 0.41 : 0.30) * rounds;
+      else step = slow128 * (e8 ? 0.41 : 0.28) * rounds;
       return (double)steps * step;
     };
     const int64_t resident = cus * ptg::product_workgroups(edge, form);

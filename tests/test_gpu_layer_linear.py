@@ -20,6 +20,13 @@ def plan():
     p.destroy()
 
 
+@pytest.fixture(scope="module")
+def streams():
+    """The two streams beside the default one that all tests here share (streams share few hardware queues: tests that
+    count on work under way at once fare better with fewer of them in a process)."""
+    return torch.cuda.Stream(), torch.cuda.Stream()
+
+
 def operands(m, n, k, t, pad=0):
     if t == E4M3:
         x, w = normal(1, m, k, scale=60.0, dtype=E4M3, pad=pad), normal(2, n, k, scale=60.0, dtype=E4M3, pad=pad)
@@ -246,7 +253,7 @@ def test_layer_gradient_against_differences(plan):
         assert abs(diff - got) <= size, (act, float(diff), float(got), float(size))
 
 
-def test_calls_on_two_streams_are_ordered(plan):
+def test_calls_on_two_streams_are_ordered(plan, streams):
     """One plan, two streams without a wait between them: the plan's scratch serves one call at a time."""
     m, n, k = 200, 520, 264
     x, w = normal(1, m, k), normal(2, n, k)
@@ -256,7 +263,7 @@ def test_calls_on_two_streams_are_ordered(plan):
     ptg.layer_linear_backward(dpre, x, None, plan, dw=dw_want)
     ptg.layer_activation_backward(dpre, pre, None, plan, activation="silu", dbias=db_want)
     torch.cuda.synchronize()
-    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = streams
     outs = []
     for i in range(6):
         s = a if i % 2 else b
@@ -273,7 +280,7 @@ def test_calls_on_two_streams_are_ordered(plan):
 
 
 @pytest.mark.parametrize("m", [1, 40, 300])
-def test_layer_step_replays_from_a_graph(plan, m):
+def test_layer_step_replays_from_a_graph(plan, streams, m):
     """Forward and backward calls captured once and replayed over changing inputs, with the plan's own uncaptured calls
     between the replays."""
     n, k = 520, 264
@@ -291,7 +298,7 @@ def test_layer_step_replays_from_a_graph(plan, m):
         ptg.layer_rmsnorm_backward(dy, x, g, dxn, dg, plan)
 
     results = (out, pre, dpre, dy, dxn, dw, db, dg)
-    s = torch.cuda.Stream()
+    s = streams[0]
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         step()
