@@ -112,7 +112,7 @@ const char *layer_last_hip_error(layer_cfg cfg);
  *
  * out_type LAYER_E4M3: `scale` receives one fp32 value a row, max_j |y_j| / 448
  * (at least 2^-126; 1 where the row's y is all zeros), and out the codes
- * y_j / scale. The scale's reader multiplies: y is about code * scale. A row
+ * y_j / scale (the fp32 quotient, rounded to nearest). The scale's reader multiplies: y is about code * scale. A row
  * whose y holds a NaN or an infinity gets a NaN scale and NaN codes. scale must
  * be NULL for the other types.
  *

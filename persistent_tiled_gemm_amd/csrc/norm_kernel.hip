@@ -104,14 +104,16 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const No
       }
     }
     const float r = 1.0f / sqrtf(sum / (float)a.n + a.eps);
-    float inv_scale = 1.0f;
+    float lift = 1.0f, lifted = 1.0f, inv_lifted = 1.0f;
     if constexpr (E8) {
       // the floor keeps 1 / scale finite (r / scale need not be: y is formed first)
       const float amax = __uint_as_float(top) * r;
       float scale = amax == 0.0f ? 1.0f : fmaxf(amax / kE4m3Max, 0x1p-126f);
       if (!(amax < INFINITY)) scale = __uint_as_float(0x7fc00000u);  // NaN or infinity in y
       if (t == 0) a.scale[row] = scale;
-      inv_scale = 1.0f / scale;
+      if (scale < 0x1p-60f) lift = 0x1p64f;  // the quotient's remainder stays above the subnormal numbers
+      lifted = scale * lift;
+      inv_lifted = 1.0f / lifted;
     }
     TO *out = (TO *)a.out + row * a.ldo;
 #pragma unroll
@@ -119,7 +121,17 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const No
       const int32_t j = (c * T + t) * 8;
       if (j < a.n) {
         f32x8 y = v[c] * w[c] * r;
-        if constexpr (E8) y *= inv_scale;
+        if constexpr (E8) {
+          // y / scale: the product with the reciprocal, put right by its remainder (the
+          // product alone is off by a step of fp32 now and then, and a code next to a
+          // tie then by a step of e4m3: 1 in 10^6. 16384 x 8192: 163.3 -> 164.5 us).
+          y *= lift;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float q = y[e] * inv_lifted;
+            y[e] = fmaf(fmaf(-q, lifted, y[e]), inv_lifted, q);
+          }
+        }
         store8_nt(out + j, y);
       }
     }
