@@ -542,7 +542,8 @@ gemm_status gemm_create(gemm_tile_cfg *out, const gemm_tile_desc *desc) {
     return GEMM_E_NOMEM;
   }
   p->d_status = reinterpret_cast<uint32_t *>(p->d_ctrl_block + 3 * p->ctrl_set_bytes);
-  if (hipMemset(p->d_ctrl_block, 0, 3 * p->ctrl_set_bytes + 256) != hipSuccess) {
+  // waited for: a first run's stream need not wait for the null stream
+  if (hipMemset(p->d_ctrl_block, 0, 3 * p->ctrl_set_bytes + 256) != hipSuccess || hipStreamSynchronize(nullptr) != hipSuccess) {
     gemm_destroy(p);
     return GEMM_E_HIP;
   }

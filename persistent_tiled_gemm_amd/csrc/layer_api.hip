@@ -205,7 +205,8 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
     layer_destroy(p);
     return GEMM_E_NOMEM;
   }
-  if (hipMemset(p->d_arrivals, 0, sizeof(uint32_t) * (size_t)kArrivals) != hipSuccess) {
+  // waited for: a first call's stream need not wait for the null stream
+  if (hipMemset(p->d_arrivals, 0, sizeof(uint32_t) * (size_t)kArrivals) != hipSuccess || hipStreamSynchronize(nullptr) != hipSuccess) {
     layer_destroy(p);
     return GEMM_E_HIP;
   }
