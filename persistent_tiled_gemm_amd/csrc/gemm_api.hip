@@ -65,6 +65,7 @@ struct gemm_plan {
   // last run
   hipStream_t last_stream = nullptr;
   bool has_run = false;
+  bool follow = false;  // last_stream is this plan's to wait for (not so for runs whose caller does, see plan_run_product)
   int64_t last_tiles = 0;
   int64_t last_units = 0;
   int64_t last_items = 0;
@@ -120,7 +121,7 @@ gemm_status check_current_device(gemm_plan *p) {
 // different stream than the last one first waits (on the device) for
 // everything enqueued on the last stream so far. No host synchronisation.
 gemm_status order_after_last_stream(gemm_plan *p, hipStream_t s) {
-  if (!p->has_run || s == p->last_stream) return GEMM_OK;
+  if (!p->follow || s == p->last_stream) return GEMM_OK;
   hipError_t e = hipEventRecord(p->stream_switch, p->last_stream);
   if (e != hipSuccess) return hip_fail(p, e, "hipEventRecord(stream switch)");
   e = hipStreamWaitEvent(s, p->stream_switch, 0);
@@ -128,13 +129,10 @@ gemm_status order_after_last_stream(gemm_plan *p, hipStream_t s) {
   return GEMM_OK;
 }
 
-// Synchronise the last run's stream, read the sticky device status and clear it.
-gemm_status take_device_status(gemm_plan *p) {
-  if (!p->has_run) return GEMM_OK;
-  hipError_t e = hipStreamSynchronize(p->last_stream);
-  if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
+// Read the sticky device status and clear it (the plan's runs are over).
+gemm_status read_device_status(gemm_plan *p) {
   uint32_t st = 0;
-  e = hipMemcpy(&st, p->d_status, sizeof(st), hipMemcpyDeviceToHost);
+  hipError_t e = hipMemcpy(&st, p->d_status, sizeof(st), hipMemcpyDeviceToHost);
   if (e != hipSuccess) return hip_fail(p, e, "hipMemcpy(status)");
   if (st == 0) return GEMM_OK;
   const uint32_t zero = 0;
@@ -144,6 +142,16 @@ gemm_status take_device_status(gemm_plan *p) {
                   ((st & 1u) ? " (a workgroup gave up waiting at the concurrency gate and computed nothing)" : "") +
                   ((st & 2u) ? " (a claim-ring record answered the wrong ordinal)" : "");
   return (st & 2u) ? GEMM_E_SCHED : GEMM_E_TIMEOUT;
+}
+
+// Synchronise the last run's stream, then the device status.
+gemm_status take_device_status(gemm_plan *p) {
+  if (!p->has_run) return GEMM_OK;
+  if (p->follow) {
+    hipError_t e = hipStreamSynchronize(p->last_stream);
+    if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
+  }
+  return read_device_status(p);
 }
 
 unsigned char *ctrl_set(gemm_plan *p, uint64_t run) { return p->d_ctrl_block + (run & 1u) * p->ctrl_set_bytes; }
@@ -330,6 +338,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
   p->last_set = cur;
   p->last_stream = s;
   p->has_run = true;
+  p->follow = true;
   p->last_tiles = tiles;
   p->last_units = units;
   p->last_items = items;
@@ -407,6 +416,8 @@ float *plan_workspace(gemm_tile_cfg p, int64_t *floats) {
   return p->d_ws;
 }
 
+gemm_status plan_status(gemm_tile_cfg p) { return read_device_status(p); }
+
 gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s) {
   const int64_t units = form == kFormNTE4m3 ? 2 : 1;  // values per 16-bit unit along k
   const int64_t K = a.k / units;
@@ -431,6 +442,8 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, in
   const int64_t items = split > 1 ? split_base + (tm * tn - split_base) * split : tm * tn;
   const int32_t mode = items <= (int64_t)p->cu_count * product_workgroups(p->desc.bm, form) ? GEMM_SCHED_NONPERSISTENT : GEMM_SCHED_DYNAMIC;
   const gemm_status st = launch(p, mode, false, args, tm * tn, K, s, &op, form, split, split_base);
+  // the caller orders and waits for the plan's runs; the stream may have ended when this plan is used again
+  p->follow = false;
   if (st != GEMM_OK || split <= 1) return st;
   const hipError_t e = launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, (int32_t)split_base, (int32_t)(tm * tn - split_base),
                                              split, s);
@@ -880,7 +893,7 @@ gemm_status gemm_plan_info_get(gemm_tile_cfg tile_cfg, gemm_plan_info *out) {
 gemm_status gemm_destroy(gemm_tile_cfg tile_cfg) {
   gemm_plan *p = tile_cfg;
   if (!p) return GEMM_OK;
-  if (p->has_run) (void)hipStreamSynchronize(p->last_stream);
+  if (p->follow) (void)hipStreamSynchronize(p->last_stream);
   if (p->groups_event_pending && p->groups_uploaded) (void)hipEventSynchronize(p->groups_uploaded);
   if (p->d_ctrl_block) (void)hipFree(p->d_ctrl_block);
   if (p->d_log) (void)hipFree(p->d_log);

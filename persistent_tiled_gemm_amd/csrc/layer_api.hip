@@ -242,7 +242,7 @@ gemm_status layer_sync(layer_cfg p) {
   if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
   gemm_status st = GEMM_OK;
   for (gemm_tile_cfg t : {p->tiles256, p->tiles128}) {
-    const gemm_status one = gemm_sync(t);
+    const gemm_status one = ptg::plan_status(t);
     if (one == GEMM_OK) continue;
     std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));
     st = one;

@@ -110,7 +110,10 @@ hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &o
 float *plan_workspace(gemm_tile_cfg plan, int64_t *floats);
 // The product as a run of a GEMM plan: its tiles and dynamic scheduler; the tiles
 // from split_base on are split into `split` K-chunks each (1: none), which a
-// second kernel joins. The caller orders runs on different streams.
+// second kernel joins. The caller orders runs on different streams and waits for
+// them: the plan keeps no stream of theirs, so that they may end once they are over.
 gemm_status plan_run_product(gemm_tile_cfg plan, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s);
+// The device status of a plan's runs, which are over; it is cleared.
+gemm_status plan_status(gemm_tile_cfg plan);
 
 }  // namespace ptg

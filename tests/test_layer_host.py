@@ -27,3 +27,32 @@ result = dict(status=status, left=left, early=hip.stand_in_early_launches(), lau
 """)
     assert got["status"] == [0, 0, 0] and "ptg_rows_kernel" in got["launches"]
     assert got["left"] == [0, 0] and got["early"] == 0
+
+
+# a product in 256 x 256 tiles on stream A, then a call that runs no such tiles on stream B
+TWO_STREAMS = """
+assert lib.layer_create(ctypes.byref(plan), 0) == 0
+product = layer.LinearArgs(x=P, w=P, out=P, m=8192, n=8192, k=8192, ldx=8192, ldw=8192, ldo=8192, in_type=1, out_type=1)
+norm = layer.RmsnormGradArgs(dy=P, s=P, dx=P, dweight=P, m=64, n=512, lddy=512, lds=512, lddx=512, type=1, dy_type=1, eps=1e-6)
+status = [call(lib.layer_linear, product, A), call(lib.layer_rmsnorm_backward, norm, B)]
+launches = hip.stand_in_launches().decode()
+hip.stand_in_end_stream(A)
+"""
+
+
+def test_a_stream_may_end_after_the_plans_next_call(stand_in):
+    got = hip_stand_in.run(stand_in, TWO_STREAMS + """
+status += [lib.layer_sync(plan), lib.layer_destroy(plan)]
+result = dict(status=status, dead=hip.stand_in_dead_uses(), launches=launches)
+""")
+    assert "ptg_product_kernelILi256" in got["launches"] and "ptg_rmsnorm_backward" in got["launches"]
+    assert got["status"] == [0, 0, 0, 0] and got["dead"] == 0
+
+
+def test_layer_sync_reports_the_status_of_products_on_earlier_streams(stand_in):
+    got = hip_stand_in.run(stand_in, TWO_STREAMS + """
+hip.stand_in_device_status(1)
+status += [lib.layer_sync(plan), lib.layer_sync(plan), lib.layer_destroy(plan)]
+result = dict(status=status, dead=hip.stand_in_dead_uses())
+""")
+    assert got["status"] == [0, 0, -7, 0, 0] and got["dead"] == 0  # GEMM_E_TIMEOUT once, then cleared
