@@ -63,7 +63,8 @@
  * streams are ordered on the device (a run waits for the plan's previous
  * stream). The plan keeps the stream of its last run: that stream must stay
  * valid until the plan's next run, gemm_sync, gemm_read_log or gemm_destroy,
- * which use it. A plan is not thread-safe.
+ * which use it (once a run was captured, gemm_sync and gemm_read_log do not let
+ * go of it: replays may follow). A plan is not thread-safe.
  *
  * Graph capture. gemm_run and gemm_run_noalloc enqueue one kernel and nothing
  * else. A gemm_run made while its stream is capturing (hipStreamIsCapturing)

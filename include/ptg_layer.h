@@ -37,7 +37,8 @@
  * schedulers' state, the split products' partial sums and the partial column
  * sums. Calls of one plan on different streams are ordered on the device (a
  * call waits for the plan's previous stream), so that stream must stay valid
- * until the plan's next call, layer_sync or layer_destroy. A plan is not
+ * until the plan's next call, layer_sync or layer_destroy (layer_sync does not
+ * let go of it once a call was captured: replays may follow). A plan is not
  * thread-safe. layer_rmsnorm needs no plan.
  *
  * Graph capture. Every call may be captured once the plan's last call was made

@@ -65,7 +65,9 @@ struct gemm_plan {
   // last run
   hipStream_t last_stream = nullptr;
   bool has_run = false;
-  bool follow = false;  // last_stream is this plan's to wait for (not so for runs whose caller does, see plan_run_product)
+  // last_stream may hold runs and is this plan's to wait for (not so for runs whose caller waits, see plan_run_product)
+  bool follow = false;
+  bool captured = false;  // a run was captured: replays may follow on its stream at any time
   int64_t last_tiles = 0;
   int64_t last_units = 0;
   int64_t last_items = 0;
@@ -150,6 +152,7 @@ gemm_status take_device_status(gemm_plan *p) {
   if (p->follow) {
     hipError_t e = hipStreamSynchronize(p->last_stream);
     if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
+    p->follow = p->captured;  // nothing left to wait for: the stream may end
   }
   return read_device_status(p);
 }
@@ -339,6 +342,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
   p->last_stream = s;
   p->has_run = true;
   p->follow = true;
+  p->captured = p->captured || captured;
   p->last_tiles = tiles;
   p->last_units = units;
   p->last_items = items;

@@ -23,7 +23,8 @@ struct layer_plan {
   uint32_t *d_arrivals = nullptr;  // arrival counts of the few-row product's shared tiles, zero between calls
   hipEvent_t stream_switch = nullptr;
   hipStream_t last_stream = nullptr;
-  bool has_run = false;
+  bool has_run = false;   // last_stream may hold work of the plan
+  bool captured = false;  // a call was captured: replays may follow on its stream at any time
   char last_error[256] = "";  // of a fixed size: no call of the C ABI may throw
 };
 
@@ -74,6 +75,10 @@ gemm_status order_after_last_stream(layer_plan *p, hipStream_t s) {
     e = hipStreamWaitEvent(s, p->stream_switch, 0);
     if (e != hipSuccess) return hip_fail(p, e, "hipStreamWaitEvent(stream switch)");
   }
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  const hipError_t e = hipStreamIsCapturing(s, &capture);
+  if (e != hipSuccess) return hip_fail(p, e, "hipStreamIsCapturing");
+  p->captured = p->captured || capture != hipStreamCaptureStatusNone;
   p->last_stream = s;
   p->has_run = true;
   return GEMM_OK;
@@ -240,6 +245,7 @@ gemm_status layer_sync(layer_cfg p) {
   if (!p->has_run) return GEMM_OK;
   hipError_t e = hipStreamSynchronize(p->last_stream);
   if (e != hipSuccess) return hip_fail(p, e, "hipStreamSynchronize");
+  p->has_run = p->captured;  // nothing left to wait for: the stream may end
   gemm_status st = GEMM_OK;
   for (gemm_tile_cfg t : {p->tiles256, p->tiles128}) {
     const gemm_status one = ptg::plan_status(t);

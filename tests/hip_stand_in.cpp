@@ -16,7 +16,8 @@ namespace {
 std::map<const void *, std::string> kernels;  // host stub -> mangled name
 std::set<void *> ended;                       // streams whose handles are dead
 bool unwaited = false;                        // memory was set on the null stream and nothing has waited for it
-int dead_uses = 0, early_launches = 0;
+int dead_uses = 0, early_launches = 0, waits = 0;
+bool capturing = false;
 int next_status = 0;  // what the next four-byte read of device memory returns
 std::string log;
 dim3 grid_, block_;
@@ -33,8 +34,10 @@ extern "C" {
 // ---- for the tests
 int stand_in_unwaited() { return unwaited; }
 int stand_in_dead_uses() { return dead_uses; }
+int stand_in_waits() { return waits; }  // of one stream for another
 int stand_in_early_launches() { return early_launches; }
 void stand_in_end_stream(void *s) { ended.insert(s); }
+void stand_in_capture(int on) { capturing = on; }
 void stand_in_device_status(int v) { next_status = v; }
 // One line a launch since the last call: mangled name, grid, block and, of the kernels that join split tiles, the first split
 // tile and the chunks.
@@ -132,8 +135,10 @@ hipError_t hipStreamSynchronize(hipStream_t s) {
   return ended.count(s) ? hipErrorInvalidHandle : hipSuccess;
 }
 hipError_t hipDeviceSynchronize() { return unwaited = false, hipSuccess; }
-hipError_t hipStreamWaitEvent(hipStream_t s, hipEvent_t, unsigned) { return use(s), hipSuccess; }
-hipError_t hipStreamIsCapturing(hipStream_t s, hipStreamCaptureStatus *c) { return use(s), *c = hipStreamCaptureStatusNone, hipSuccess; }
+hipError_t hipStreamWaitEvent(hipStream_t s, hipEvent_t, unsigned) { return use(s), ++waits, hipSuccess; }
+hipError_t hipStreamIsCapturing(hipStream_t s, hipStreamCaptureStatus *c) { 
+  return use(s), *c = capturing ? hipStreamCaptureStatusActive : hipStreamCaptureStatusNone, hipSuccess;
+}
 hipError_t hipStreamDestroy(hipStream_t) { return hipSuccess; }
 hipError_t hipExtStreamCreateWithCUMask(hipStream_t *s, uint32_t, const uint32_t *) { return *s = nullptr, hipSuccess; }
 hipError_t hipEventCreate(hipEvent_t *e) { return *e = (hipEvent_t)std::malloc(1), hipSuccess; }

@@ -56,3 +56,39 @@ status += [lib.layer_sync(plan), lib.layer_sync(plan), lib.layer_destroy(plan)]
 result = dict(status=status, dead=hip.stand_in_dead_uses())
 """)
     assert got["status"] == [0, 0, -7, 0, 0] and got["dead"] == 0  # GEMM_E_TIMEOUT once, then cleared
+
+
+# the plain plan's run or the layer plan's call on stream A, and its synchronisation
+SYNCED = """
+d, g = ptg.TileDesc(), ctypes.c_void_p()
+assert lib.gemm_default_desc(ctypes.byref(d), 256, 0) == 0 and lib.gemm_create(ctypes.byref(g), ctypes.byref(d)) == 0
+assert lib.layer_create(ctypes.byref(plan), 0) == 0
+lib.gemm_run.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int64] * 3 + [ctypes.c_int32] + [ctypes.c_void_p] * 2
+norm = layer.RmsnormGradArgs(dy=P, s=P, dx=P, m=64, n=512, lddy=512, lds=512, lddx=512, type=1, dy_type=1, eps=1e-6)
+def run(s):
+    return lib.gemm_run(P, P, P, 512, 512, 512, 2, g, s), call(lib.layer_rmsnorm_backward, norm, s)
+hip.stand_in_capture({captured})
+status = [*run(A), lib.gemm_sync(g), lib.layer_sync(plan)]
+hip.stand_in_capture(0)
+"""
+
+
+def test_a_stream_may_end_after_a_sync(stand_in):
+    got = hip_stand_in.run(stand_in, SYNCED.format(captured=0) + """
+hip.stand_in_end_stream(A)
+status += [lib.gemm_sync(g), lib.layer_sync(plan), *run(B), *run(A.__class__(0x3000))]
+dead = hip.stand_in_dead_uses()
+status += [lib.gemm_destroy(g), lib.layer_destroy(plan)]
+result = dict(status=status, dead=[dead, hip.stand_in_dead_uses()])
+""")
+    assert got["status"] == [0] * 12 and got["dead"] == [0, 0]
+
+
+def test_a_captured_stream_is_kept(stand_in):
+    """Replays may be under way on it after a sync: a run on another stream still waits for them."""
+    got = hip_stand_in.run(stand_in, SYNCED.format(captured=1) + """
+before = hip.stand_in_waits()
+status += [*run(B)]
+result = dict(status=status, waits=hip.stand_in_waits() - before)
+""")
+    assert got["status"] == [0] * 6 and got["waits"] == 2
