@@ -183,9 +183,10 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 //   - x is read again for every 16 NBLK rows of w, from L2, which shows from some
 //     ten rows on (from the first in e4m3, where it is widened again too): two
 //     blocks of w up to 16 rows, four for more, where w is large enough that the
-//     tiles still fill the machine (8192^2 bf16, 32 rows: two blocks 41 us, four
-//     39.8; 16 rows: one block 36, two 33 to 35; e4m3, 8 rows: one 18.7, two 16.9).
-//     Smaller w: one and two (4096^2, 32 rows: two 14.9, four 14.8; 2048^2: two
+//     tiles still fill the machine (8192^2 bf16, 16 rows: one block 36 us, two 33 to
+//     35; e4m3, 8 rows: one 18.7, two 16.9). More than 16 rows of so large a w come
+//     here in e4m3 alone, and 32 at most (rows_preferred). Smaller w: one block up
+//     to 16 rows, two for more (4096^2, 32 rows: two 14.9, four 14.8; 2048^2: two
 //     9.0, one 8.7);
 //   - k is shared until there are as many workgroups as CUs, while a wave keeps
 //     four steps (1024 x 8192, one row: 12.6 us unshared, 9.1 with four).
@@ -194,7 +195,7 @@ static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, bool e8, int cu_cou
   RowsShape f;
   const bool large = (int64_t)n * k >= (int64_t)32 << 20;
   f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-  f.nblk = m <= 16 ? (large && (e8 || m > 8) ? 2 : 1) : (large ? 4 : 2);
+  f.nblk = m <= 16 ? (large && (e8 || m > 8) ? 2 : 1) : (large && e8 ? 4 : 2);
   const int64_t tiles = (n + 16 * f.nblk - 1) / (16 * f.nblk);
   f.waves = f.nblk == 1 && tiles < 4 * cu_count ? 8 : 4;
   const int64_t steps = (k + (e8 ? 63 : 31)) / (e8 ? 64 : 32);
@@ -223,15 +224,21 @@ int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t
 }
 
 template <bool E8>
-static void rows_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
+static hipError_t rows_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
   const dim3 block(64 * f.waves);
+  if constexpr (E8) {
+    if (f.mt == 2 && f.nblk == 4) {
+      hipLaunchKernelGGL((ptg_rows_kernel<E8, 2, 4, 4, 2>), grid, block, 0, s, a);
+      return hipGetLastError();
+    }
+  }
   if (f.mt == 1 && f.nblk == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 1, 4, 4>), grid, block, 0, s, a);
   else if (f.mt == 1 && f.nblk == 1) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 1, 8, 4>), grid, block, 0, s, a);
   else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_kernel<E8, 1, 2, 4, 4>), grid, block, 0, s, a);
   else if (f.mt == 2 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 2, 2, 4, 2>), grid, block, 0, s, a);
-  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 2, 4, 4, 2>), grid, block, 0, s, a);
-  else if (f.nblk == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 4, 2, 4, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((ptg_rows_kernel<E8, 4, 4, 4, 2>), grid, block, 0, s, a);
+  else if (f.mt == 4 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_kernel<E8, 4, 2, 4, 2>), grid, block, 0, s, a);
+  else return hipErrorInvalidValue;  // rows_preferred sends no such call here
+  return hipGetLastError();
 }
 
 hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
@@ -248,9 +255,7 @@ hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *
   a.arrivals = arrivals;
   a.ep = p.ep;
   const dim3 grid((uint32_t)((p.n + 16 * f.nblk - 1) / (16 * f.nblk)), (uint32_t)f.split);
-  if (e8) rows_blocks<true>(f, a, grid, s);
-  else rows_blocks<false>(f, a, grid, s);
-  return hipGetLastError();
+  return e8 ? rows_blocks<true>(f, a, grid, s) : rows_blocks<false>(f, a, grid, s);
 }
 
 }  // namespace ptg
