@@ -325,7 +325,7 @@ template <int T, typename TS>
 static void rmsnorm_chunks(const NormArgs &a, int chunks, int groups, hipStream_t s) {
   if (chunks == 1) rmsnorm_out<T, 1, TS>(a, groups, s);
   else if (chunks == 2) rmsnorm_out<T, 2, TS>(a, groups, s);
-  else rmsnorm_out<T, 4, TS>(a, groups, s);
+  else if constexpr (T == 1024) rmsnorm_out<T, 4, TS>(a, groups, s);  // the others change to more threads first
 }
 
 template <typename TS>
@@ -363,7 +363,7 @@ template <int T, typename TS>
 static void backward_chunks(const NormGradArgs &a, int chunks, int groups, hipStream_t s) {
   if (chunks == 1) backward_dy<T, 1, TS>(a, groups, s);
   else if (chunks == 2) backward_dy<T, 2, TS>(a, groups, s);
-  else backward_dy<T, 4, TS>(a, groups, s);
+  else if constexpr (T == 1024) backward_dy<T, 4, TS>(a, groups, s);  // the others change to more threads first
 }
 
 template <typename TS>
