@@ -8,7 +8,7 @@ The function names are the C ABI's: gemm_default_desc, gemm_create, gemm_run,
 gemm_run_noalloc, gemm_run_grouped, gemm_read_log, gemm_sync, gemm_plan_info_get, gemm_destroy,
 gemm_status_str, gemm_last_hip_error, gemm_test_preset_counter,
 gemm_test_preset_gate, gemm_test_stream_cu_mask, gemm_test_stream_destroy,
-gemm_test_spoiler, gemm_mfma_probe, gemm_hbm_probe. Tensors are torch device tensors: A and B
+gemm_test_spoiler, gemm_mfma_probe, gemm_e4m3_probe, gemm_hbm_probe. Tensors are torch device tensors: A and B
 bf16 (or int16 / uint16 views of bf16 bits), C float32, all contiguous; streams
 are torch.cuda streams (default: the current stream).
 
@@ -48,7 +48,7 @@ STATUS_NAMES = {0: "GEMM_OK", -1: "GEMM_E_INVALID_ARG", -2: "GEMM_E_SHAPE", -3: 
 ABI_FUNCTIONS = ("gemm_default_desc", "gemm_create", "gemm_run", "gemm_run_noalloc", "gemm_run_grouped", "gemm_read_log",
                  "gemm_sync", "gemm_plan_info_get", "gemm_destroy", "gemm_status_str", "gemm_last_hip_error",
                  "gemm_test_preset_counter", "gemm_test_preset_gate", "gemm_test_stream_cu_mask",
-                 "gemm_test_stream_destroy", "gemm_test_spoiler", "gemm_mfma_probe", "gemm_hbm_probe")
+                 "gemm_test_stream_destroy", "gemm_test_spoiler", "gemm_mfma_probe", "gemm_e4m3_probe", "gemm_hbm_probe")
 
 
 class PtgError(RuntimeError):
@@ -134,6 +134,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.gemm_test_spoiler.argtypes = [i32, i32, i64, vp, vp, ctypes.c_double]
     lib.gemm_mfma_probe.argtypes = [i32, i32, i32, i32, ctypes.POINTER(ctypes.c_double),
                                     ctypes.POINTER(ctypes.c_double)]
+    lib.gemm_e4m3_probe.argtypes = [i32, i32, ctypes.c_char_p, ctypes.c_char_p, i32, ctypes.POINTER(ctypes.c_float)]
     lib.gemm_hbm_probe.argtypes = [i32, i64, i32, i32, ctypes.POINTER(ctypes.c_double)]
     for name in ABI_FUNCTIONS:
         if name not in ("gemm_status_str", "gemm_last_hip_error"):
@@ -394,6 +395,19 @@ def gemm_mfma_probe(iters: int = 20000, random_operands: bool = True, mfma_block
                                         ctypes.byref(tf), ctypes.byref(ghz))
     _check(st, "gemm_mfma_probe")
     return {"tflops": tf.value, "clock_ghz": ghz.value}
+
+
+def gemm_e4m3_probe(a, b, form: int = 0, device: int = 0) -> float:
+    """gemm_e4m3_probe: sum of a_i b_i (values that e4m3 holds) as one e4m3 matrix instruction adds it. form: 0
+    16x16x32, 1 32x32x16, 2 16x16x128, 3 32x32x64."""
+    import torch
+    if len(a) != len(b):
+        raise ValueError("a and b differ in length")
+    codes = [torch.tensor(v, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8).tolist() for v in (a, b)]
+    out = ctypes.c_float(0.0)
+    st = load_library().gemm_e4m3_probe(int(device), int(form), bytes(codes[0]), bytes(codes[1]), len(a), ctypes.byref(out))
+    _check(st, "gemm_e4m3_probe")
+    return out.value
 
 
 def gemm_hbm_probe(bytes_: int = 1 << 30, kind: str = "read", reps: int = 20, device: int = 0) -> float:

@@ -1045,6 +1045,27 @@ gemm_status gemm_mfma_probe(int32_t device, int32_t iters, int32_t random_operan
   return st;
 }
 
+gemm_status gemm_e4m3_probe(int32_t device, int32_t form, const uint8_t *a, const uint8_t *b, int32_t n, float *sum_out) {
+  constexpr int32_t kTerms[4] = {32, 16, 128, 64};
+  if (!a || !b || !sum_out || form < 0 || form > 3 || n < 0 || n > kTerms[form]) return GEMM_E_INVALID_ARG;
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) return GEMM_E_HIP;
+  if (cur != device) return GEMM_E_DEVICE;
+  hipDeviceProp_t prop;
+  if (hipGetDeviceProperties(&prop, device) != hipSuccess) return GEMM_E_HIP;
+  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return GEMM_E_UNSUPPORTED;
+  uint8_t h[256] = {0}, *d = nullptr;  // a and b, 128 values each
+  std::memcpy(h, a, (size_t)n);
+  std::memcpy(h + 128, b, (size_t)n);
+  if (hipMalloc(&d, sizeof(h) + sizeof(float)) != hipSuccess) return GEMM_E_NOMEM;
+  float *out = reinterpret_cast<float *>(d + sizeof(h));
+  const bool ok = hipMemcpy(d, h, sizeof(h), hipMemcpyHostToDevice) == hipSuccess &&
+                  ptg::launch_e4m3_probe(form, d, d + 128, out, nullptr) == hipSuccess &&
+                  hipMemcpy(sum_out, out, sizeof(float), hipMemcpyDeviceToHost) == hipSuccess;
+  (void)hipFree(d);
+  return ok ? GEMM_OK : GEMM_E_HIP;
+}
+
 gemm_status gemm_hbm_probe(int32_t device, int64_t bytes, int32_t kind, int32_t reps, double *gbs_out) {
   if (!gbs_out || kind < 0 || kind > 1 || reps < 1 || reps > 1000) return GEMM_E_INVALID_ARG;
   if (bytes < (1 << 20) || bytes > (int64_t)16 << 30 || (bytes % 4096) != 0) return GEMM_E_INVALID_ARG;

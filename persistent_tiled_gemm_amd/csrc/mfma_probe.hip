@@ -65,6 +65,33 @@ __global__ __launch_bounds__(256, 1) void ptg_mfma_probe_kernel(int32_t iters, f
   }
 }
 
+// One e4m3 MFMA of one wave: every row of A holds the same k values, every column
+// of B too, so that every element of the result is sum_k a_k b_k as the
+// instruction adds it. Lane group g (of `edge` lanes) holds the g-th 8 (or 32) k.
+__global__ void ptg_e4m3_probe_kernel(int32_t form, const uint8_t *a, const uint8_t *b, float *out) {
+  typedef __attribute__((ext_vector_type(8))) int i32x8;
+  const uint32_t lane = threadIdx.x;
+  float sum;
+  if (form < 2) {
+    const uint32_t g = lane / (form == 0 ? 16u : 32u);
+    const long x = ((const long *)a)[g], y = ((const long *)b)[g];
+    sum = form == 0 ? __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(x, y, f32x4{}, 0, 0, 0)[0]
+                    : __builtin_amdgcn_mfma_f32_32x32x16_fp8_fp8(x, y, f32x16{}, 0, 0, 0)[0];
+  } else {
+    const uint32_t g = lane / (form == 2 ? 16u : 32u);
+    const i32x8 x = ((const i32x8 *)a)[g], y = ((const i32x8 *)b)[g];
+    const int one = 0x7f7f7f7f;  // block scales of 2^0
+    sum = form == 2 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{}, 0, 0, 0, one, 0, one)[0]
+                    : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, f32x16{}, 0, 0, 0, one, 0, one)[0];
+  }
+  if (lane == 0) *out = sum;
+}
+
+hipError_t launch_e4m3_probe(int32_t form, const uint8_t *a, const uint8_t *b, float *out, hipStream_t s) {
+  hipLaunchKernelGGL(ptg_e4m3_probe_kernel, dim3(1), dim3(64), 0, s, form, a, b, out);
+  return hipGetLastError();
+}
+
 hipError_t launch_mfma_probe(int grid, int32_t iters, bool vary, int mfma_block, float *sink, uint64_t *ticks,
                              hipStream_t s) {
   if (mfma_block == 32) {

@@ -121,4 +121,8 @@ hipError_t launch_spoiler(int n_wgs, uint64_t spin_ticks, uint32_t *resident, ui
 hipError_t launch_mfma_probe(int grid, int32_t iters, bool vary, int mfma_block, float *sink, uint64_t *ticks,
                              hipStream_t s);
 
+// One e4m3 MFMA; a and b: 128 values each, of which the form (see
+// gemm_e4m3_probe) takes the first 16 to 128.
+hipError_t launch_e4m3_probe(int32_t form, const uint8_t *a, const uint8_t *b, float *out, hipStream_t s);
+
 }  // namespace ptg

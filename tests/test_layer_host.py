@@ -92,3 +92,14 @@ status += [*run(B)]
 result = dict(status=status, waits=hip.stand_in_waits() - before)
 """)
     assert got["status"] == [0] * 6 and got["waits"] == 2
+
+
+def test_the_e4m3_probe_refuses(stand_in):
+    got = hip_stand_in.run(stand_in, """
+c, out = bytes(256), ctypes.c_float()
+def f(device, form, a, b, n):
+    return lib.gemm_e4m3_probe(device, form, a, b, n, ctypes.byref(out))
+result = [f(0, 4, c, c, 1), f(0, -1, c, c, 1), f(0, 0, None, c, 1), f(0, 0, c, None, 1), f(0, 0, c, c, -1), f(1, 0, c, c, 1)] + \\
+    [f(0, form, c, c, n) for form, n in ((0, 33), (1, 17), (2, 129), (3, 65))] + [f(0, 2, c, c, 128)]
+""")
+    assert got == [-1, -1, -1, -1, -1, -4, -1, -1, -1, -1, 0]
