@@ -30,7 +30,7 @@ struct layer_plan {
 
 namespace {
 
-constexpr int64_t kArrivals = 4096;  // a tile whose k is shared is one of fewer than 16 waves x CUs / 4
+constexpr int64_t kArrivals = 4096;  // tiles whose k is shared: CUs / 2 at most (rows_shape), checked at each call
 
 gemm_status hip_fail(layer_plan *p, hipError_t e, const char *what) {
   if (p) std::snprintf(p->last_error, sizeof(p->last_error), "%s: %s", what, hipGetErrorString(e));
@@ -111,8 +111,15 @@ gemm_status make_tiles(gemm_tile_cfg *out, int32_t edge, int32_t device) {
 struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 
 // The choice is the least of the times that these fits give, in microseconds (256
-// CUs; measured over m = 100 .. 4096, n = 1024 .. 16384, k = 768 .. 8192 in each
-// form; within about 15% of the times):
+// CUs; fitted over m = 100 .. 4096, n = 1024 .. 16384, k = 768 .. 8192 in each
+// form). They compare choices and do not foretell a call: of 86 products over twice
+// that range (bf16, e4m3, dx and dw; no epilogue terms) the measured time was 1.11
+// times the fit at the median, 0.95 and 2.0 at the first and last tenth, and within
+// 15% for 56% of them. What they leave out: a unit's fill, drain and writes are
+// counted once a launch and not again for the further units of a CU, nor are the
+// bytes of a large output, so that few k-steps a tile take up to 2.5 times the fit
+// (8418 x 8912 x 136: 37 and 87) and dw over few rows, which writes fp32, up to 6.5;
+// nor are the terms of the epilogue. 8192^3: 694 and 728, in e4m3 591 and 636.
 //   - a k-step of a 128 x 128 tile: NT and NN 0.28 with one tile a CU at a time
 //     (their stages fill its LDS), e4m3 0.41; TN 0.23, and with two tiles a CU
 //     together 0.44; 8 to fill and drain, 2 less where one wave takes every unit;
@@ -129,7 +136,8 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // 2 chunks: 118; 1024 x 4096 x 4096, 256 of 128: 44, 64 of 256 in 4 chunks: 54;
 // 256 x 4096 x 4096, 64 of 128: 43, in 4 chunks: 24; 100 x 1024 x 8192, 8 of 128:
 // 62, in 8 chunks: 20; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
-// last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55.
+// last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55 (chosen: the last eight in 13
+// chunks, whose fit is 40 and whose time 49).
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN;
   const int64_t nk = ceil_div(e8 ? a.k / 2 : a.k, 32), line = e8 ? 64 : 32;

@@ -7,7 +7,8 @@
 // after the row's sums works on registers. Groups stride over the rows and ask for
 // the next row before the present one's sums are known. Two chunks a thread
 // rather than four: 16384 x 8192 to e4m3, 174 us with 256 threads and four
-// chunks, 163 with 1024 and one (5.8 TB/s; a large copy reaches 4.7, a read 5.8).
+// chunks, 163 with 1024 and one (164.5 with the codes' exact quotient: 5.7 TB/s; a
+// large copy reaches 4.7, a read 5.8).
 #include "layer_device.hpp"
 
 namespace ptg {

@@ -4,7 +4,7 @@
 // out = act(z scales + bias) + residual. Bound by MFMA issue and power, then by the
 // epilogue. 8192^3 to bf16: NT 716 us (1535 TFLOP/s; the vendor library's 689), and 8
 // more with pre, 17 with gelu_tanh, 19 with silu, 51 with gelu, 38 with a residual; both
-// gradients (NN, TN) 1459; e4m3 with a residual 678.
+// gradients (NN, TN) 1459 to 1468; e4m3 with a residual 678 to 686.
 #include "gemm_body.hpp"
 #include "layer_device.hpp"
 
