@@ -11,10 +11,16 @@
  *   layer_linear_backward      dx = dpre . w, dw = dpre^T . x
  *   layer_rmsnorm_backward     dx (of x and of residual alike), dweight
  *
+ * and, at the ends of a stack of such layers, what serves it in 8 bits and what trains it:
+ *
+ *   layer_quantize                rows to int8 or e4m3 codes with one scale each
+ *   layer_cross_entropy           log sum exp and loss of an output head, without its logits
+ *   layer_cross_entropy_backward  dx and dw of that loss
+ *
  * Layouts. Matrices are row-major with a row stride in elements (ld*), rows
  * dense; a weight is n x k as a linear layer keeps it. Device pointers only,
  * 16-byte aligned. Row lengths and strides are multiples of 8 elements (16 for
- * e4m3 operands of a product); the number of rows m is arbitrary, 0 included.
+ * e4m3 and int8 operands of a product); the number of rows m is arbitrary, 0 included.
  * A stride is at least the row's length; with m <= 1, or rows of no elements, it is
  * not looked at.
  *
@@ -25,11 +31,12 @@
  * 31, tanh-gelu 9 and 6.25 for each unit of the logistic function's argument.) e4m3 operands are
  * widened to bf16 (exactly) before they are multiplied: the e4m3 matrix
  * instructions would be faster, but they add eight products at a time and drop
- * what lies 2^-13 below the largest of the eight.
+ * what lies 2^-13 below the largest of the eight. int8 operands are multiplied as
+ * they are, twice as many in the same time, and their sums are 32-bit integers, exact.
  *
  * Speed. k-contiguous operands (x, w, dpre in layer_linear_backward's dx) are
  * read 128 bytes of a row at a time: rows that start on 128-byte lines (strides
- * that are multiples of 64 bf16 or 128 e4m3 elements) run fastest, rows off the
+ * that are multiples of 64 bf16 or 128 e4m3 or int8 elements) run fastest, rows off the
  * 64-byte lines up to a third slower.
  *
  * Ownership, streams, errors. As in ptg_gemm.h: the caller owns every tensor
@@ -41,7 +48,7 @@
  * call waits for the plan's previous stream), so that stream must stay valid
  * until the plan's next call, layer_sync or layer_destroy (layer_sync does not
  * let go of it once a call was captured: replays may follow). A plan is not
- * thread-safe. layer_rmsnorm needs no plan.
+ * thread-safe. layer_rmsnorm and layer_quantize need no plan.
  *
  * Graph capture. Every call may be captured once the plan's last call was made
  * on the capture stream (a call on a new stream waits with an event for the
@@ -64,6 +71,7 @@ extern "C" {
 #define LAYER_F32 0
 #define LAYER_BF16 1
 #define LAYER_E4M3 2 /* 8 bits, 4 exponent and 3 mantissa bits, largest value 448, no infinities */
+#define LAYER_I8 3   /* 8-bit integers, two's complement */
 
 /*
  * Activations of a pre-activation z:
@@ -82,6 +90,7 @@ extern "C" {
 #define LAYER_MAX_ROWS (1 << 30)
 #define LAYER_MAX_COLS (1 << 20)     /* n, k and row strides */
 #define LAYER_MAX_NORM_COLS (1 << 15) /* n of the norm: a row is held in one workgroup's registers */
+#define LAYER_MAX_I8_K 131056        /* k of an int8 product: 2^14 k stays under 2^31 */
 
 /* Opaque plan: owns all scratch. */
 typedef struct layer_plan *layer_cfg;
@@ -178,8 +187,10 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *args, layer_cf
  * z_mn = x_scale_m w_scale_n sum_k x_mk w_nk + bias_n;  pre = z;
  * out = act(z) + residual.
  * in_type LAYER_BF16: x and w are bf16, x_scale and w_scale NULL.
- * in_type LAYER_E4M3: x and w are e4m3; x_scale (m, fp32; NULL: 1) and w_scale
- * (n, fp32; NULL: 1) are their row scales. k is then a multiple of 16.
+ * in_type LAYER_E4M3 or LAYER_I8: x and w are e4m3 or int8; x_scale (m, fp32; NULL: 1)
+ * and w_scale (n, fp32; NULL: 1) are their row scales (each token's and each output
+ * channel's). k is then a multiple of 16, in int8 at most LAYER_MAX_I8_K; the sum of
+ * int8 products is exact and rounded to fp32 before it meets the scales.
  * pre (bf16, NULL: not kept) receives z for layer_activation_backward. The
  * activation is taken of the unrounded z. residual may be out itself (same
  * pointer, stride and type). k == 0 gives z = bias. m == 0 or n == 0 enqueues
@@ -203,7 +214,7 @@ typedef struct layer_linear_args {
   void *out;             /* m x n, out_type */
   int64_t m, n, k;
   int64_t ldx, ldw, ldr, ldp, ldo;
-  int32_t in_type;       /* LAYER_BF16 or LAYER_E4M3 */
+  int32_t in_type;       /* LAYER_BF16, LAYER_E4M3 or LAYER_I8 */
   int32_t bias_type;     /* LAYER_F32 or LAYER_BF16 */
   int32_t residual_type; /* LAYER_F32 or LAYER_BF16 */
   int32_t out_type;      /* LAYER_F32 or LAYER_BF16 */
@@ -255,6 +266,103 @@ typedef struct layer_linear_grad_args {
 } layer_linear_grad_args;
 
 gemm_status layer_linear_backward(const layer_linear_grad_args *args, layer_cfg cfg, void *stream);
+
+/*
+ * Rows to 8-bit codes with one scale each: scale_m = max_j |x_mj| / top (the fp32
+ * quotient, at least 2^-126; 1 where the row is all zeros), out = x / scale (the
+ * fp32 quotient, rounded to nearest, ties to even); top is 127 for LAYER_I8 (codes
+ * -127 .. 127) and 448 for LAYER_E4M3. The scale's reader multiplies: x is about
+ * code * scale. A row that holds a NaN or an infinity gets a NaN scale (and NaN
+ * codes, or zeros in int8). These are the operands and scales of layer_linear: of x a
+ * scale for each token, of w one for each of its n rows.
+ * One launch, no plan. m == 0 or n == 0 enqueues nothing (and writes no scale).
+ * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, an unknown type),
+ * GEMM_E_SHAPE, GEMM_E_UNSUPPORTED (current device not gfx950), GEMM_E_HIP.
+ */
+typedef struct layer_quantize_args {
+  const void *x; /* m x n, type */
+  void *out;     /* m x n, out_type */
+  float *scale;  /* m */
+  int64_t m, n;
+  int64_t ldx, ldo;
+  int32_t type;     /* LAYER_F32 or LAYER_BF16 */
+  int32_t out_type; /* LAYER_I8 or LAYER_E4M3 */
+} layer_quantize_args;
+
+gemm_status layer_quantize(const layer_quantize_args *args, void *stream);
+
+/*
+ * Softmax cross entropy of an output head, without its logits: with z = x . w^T
+ * (m tokens, n entries of the vocabulary),
+ *   lse_m = log sum_v exp z_mv,  loss_m = lse_m - z_m,label.
+ * A negative label: the row is not counted, its loss is 0 (its lse is written all
+ * the same). A label of n or more is a mistake that no call can see in time: its
+ * loss is NaN, and so are its gradients. Logits, maxima and sums are fp32; they
+ * are taken tile by tile, 8 bytes a row and block of the vocabulary reach memory.
+ * loss may be NULL. lse holds other values while the call runs. A logit of NaN
+ * gives the row NaN; w rows of -infinity work where the logit is -infinity.
+ * Two launches (more where a workspace of 8 bytes a row and 64 entries does not
+ * hold all rows). m == 0 enqueues nothing.
+ * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, loss and lse the same),
+ * GEMM_E_SHAPE (also n == 0 with rows), GEMM_E_DEVICE, GEMM_E_HIP.
+ */
+typedef struct layer_cross_entropy_args {
+  const void *x;        /* m x k, bf16 */
+  const void *w;        /* n x k, bf16 */
+  const int64_t *label; /* m */
+  float *lse;           /* m */
+  float *loss;          /* m, or NULL */
+  int64_t m, n, k;
+  int64_t ldx, ldw;
+} layer_cross_entropy_args;
+
+gemm_status layer_cross_entropy(const layer_cross_entropy_args *args, layer_cfg cfg, void *stream);
+
+/*
+ * The gradient of dloss sum_m weight_m loss_m, from the forward pass's lse: with
+ *   dz_mv = weight_m (exp(z_mv - lse_m) - [v = label_m])   (0 in rows not counted)
+ * rounded to bf16 (the logits are computed again),
+ *   dx = dloss dz . w,  dw = dloss dz^T . x (+ dw with `accumulate`, in dw's type).
+ * weight (fp32, NULL: ones): one factor a token, e.g. an incoming gradient. dloss:
+ * one fp32 value on the device (NULL: 1), e.g. the 1 / count of a mean; it is applied
+ * in fp32 after the products. dx and dw: fp32 or bf16, NULL: not wanted. Rows that
+ * are not counted, or weigh 0, have dz = 0 whatever their logits are; x must hold
+ * finite values there all the same (0 times NaN is NaN in dw).
+ *
+ * scratch: dz is made and used in pieces of the vocabulary, whole 256s of its
+ * entries, as large as scratch_bytes allow: 2 m bytes an entry and, with more than
+ * one piece and a bf16 dx, 4 m k bytes before them for dx's sum.
+ * layer_cross_entropy_scratch gives the bytes for (at most) `pieces` pieces; the
+ * fewer, the faster: each costs dx's sum once through memory. It is at the call's
+ * disposal while the call runs, and any two calls may share it in turn.
+ * Three launches a piece, six where products are split along k. With m == 0 dw is
+ * zeroed (unless accumulate is set). No result depends on the order in which
+ * workgroups run; the pieces' size changes the order of dx's sum.
+ * Errors: as layer_cross_entropy; GEMM_E_SHAPE where scratch_bytes hold no piece.
+ */
+typedef struct layer_cross_entropy_grad_args {
+  const void *x;        /* m x k, bf16 */
+  const void *w;        /* n x k, bf16 */
+  const int64_t *label; /* m */
+  const float *lse;     /* m */
+  const float *weight;  /* m, or NULL */
+  const float *dloss;   /* 1, or NULL */
+  void *dx;             /* m x k, dx_type, or NULL */
+  void *dw;             /* n x k, dw_type, or NULL */
+  void *scratch;        /* 16-byte aligned */
+  int64_t scratch_bytes;
+  int64_t m, n, k;
+  int64_t ldx, ldw, lddx, lddw;
+  int32_t dx_type;      /* LAYER_F32 or LAYER_BF16 */
+  int32_t dw_type;      /* LAYER_F32 or LAYER_BF16 */
+  int32_t accumulate;
+  int32_t pad;
+} layer_cross_entropy_grad_args;
+
+/* Bytes of scratch for at most `pieces` pieces (-1: a size or `pieces` out of range). */
+int64_t layer_cross_entropy_scratch(int64_t m, int64_t n, int64_t k, int32_t pieces);
+
+gemm_status layer_cross_entropy_backward(const layer_cross_entropy_grad_args *args, layer_cfg cfg, void *stream);
 
 #ifdef __cplusplus
 }

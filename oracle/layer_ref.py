@@ -140,3 +140,90 @@ def product_bound(a, b, dtype, old=None):
     if old is not None:
         exact, size = exact + d(old), size + d(old).abs()
     return exact, rounded(exact, dtype, size * (a.shape[1] + 8) * U32)
+
+
+# ---- rows in 8 bits, and the cross entropy of an output head
+
+TOPS = {torch.int8: 127.0, torch.float8_e4m3fn: E4M3_MAX}
+
+
+def quantise_rows(x, dtype):
+    """(scale, codes) of layer_quantize, which defines both by fp32 quotients: IEEE divisions here."""
+    x = x.detach().cpu().to(torch.float32)
+    top = x.abs().amax(dim=1)
+    bad = ~torch.isfinite(x).all(dim=1)
+    scale = torch.where(top == 0, torch.ones_like(top), (top / torch.full_like(top, TOPS[dtype])).clamp(min=2.0 ** -126))
+    scale[bad] = float("nan")
+    q = x / scale[:, None]
+    if dtype == torch.int8:
+        return scale, torch.where(bad[:, None], torch.zeros_like(q), q.round()).to(torch.int8)
+    return scale, q.to(dtype)
+
+
+def cross_entropy(x, w, label):
+    """(lse, loss); a negative label's loss is 0, one past the vocabulary NaN."""
+    z = d(x) @ d(w).t()
+    label = label.cpu()
+    lse = torch.logsumexp(z, dim=1)
+    past = label >= z.shape[1]
+    at = torch.where(past, torch.zeros_like(label), label).clamp(min=0)
+    loss = torch.where(label < 0, torch.zeros_like(lse), lse - z.gather(1, at[:, None])[:, 0])
+    return lse, torch.where(past, torch.full_like(loss, float("nan")), loss)
+
+
+def _logits_error(x, w):
+    """How far a logit may be off: an fp32 sum of k products."""
+    return (d(x).abs() @ d(w).abs().t()) * (x.shape[1] + 8) * U32
+
+
+def cross_entropy_bounds(x, w, label):
+    """(bound of lse, bound of loss). A row's logits move lse by at most the largest of their errors. A sum of n
+    exponentials: chains of 32 in a lane and of n / 16 / 8 blocks in the join, and the trees; 2^-23 and |t| 2^-24 of each
+    exponential e^t, |t| e^t below 0.4. lse is the maximum plus a logarithm: a step of each."""
+    e = _logits_error(x, w)
+    z = d(x) @ d(w).t()
+    lse, loss = cross_entropy(x, w, label)
+    n = z.shape[1]
+    lse_err = e.amax(dim=1) + (n / 128 + 128) * U32 + 4 * U32 * (lse.abs() + z.amax(dim=1).abs())
+    at = label.cpu().clamp(min=0, max=n - 1)[:, None]
+    loss_err = torch.where(label.cpu() < 0, torch.zeros_like(lse), lse_err + e.gather(1, at)[:, 0] + 2 * U32 * loss.abs())
+    return lse_err, loss_err
+
+
+def logit_grad(x, w, label, lse, weight=None):
+    """dz at a given lse."""
+    p = torch.exp(d(x) @ d(w).t() - d(lse)[:, None])
+    label = label.cpu()
+    rows = torch.arange(p.shape[0])[label >= 0]
+    p[rows, label[label >= 0]] -= 1.0
+    if weight is not None:
+        p = p * d(weight)[:, None]
+    p[label < 0] = 0.0
+    return p
+
+
+def cross_entropy_backward(x, w, label, lse, weight=None, dloss=None):
+    """(dx, dw)."""
+    dz = logit_grad(x, w, label, lse, weight) * (1.0 if dloss is None else d(dloss).reshape(()))
+    return dz @ d(w), dz.t() @ d(x)
+
+
+def cross_entropy_backward_bounds(x, w, label, lse, dx_dtype, dw_dtype, weight=None, dloss=None, old=None):
+    """(bound of dx, bound of dw). exp(z - lse): its argument is off by the logit's error and by steps of z and lse, the
+    exponential by 2^-23; dz is then rounded to bf16 and multiplied in fp32."""
+    g = 1.0 if dloss is None else d(dloss).reshape(()).abs()
+    z = d(x) @ d(w).t()
+    dz = logit_grad(x, w, label, lse, weight)
+    size = torch.ones(z.shape[0], dtype=torch.float64) if weight is None else d(weight).abs()
+    size = torch.where(label.cpu() < 0, torch.zeros_like(size), size)[:, None]
+    t = _logits_error(x, w) + 3 * U32 * (z.abs() + d(lse).abs()[:, None])
+    p_err = torch.exp(z - d(lse)[:, None]) * (torch.expm1(t) + 4 * U32) + 2 * U32
+    err = size * p_err
+    err = err + HALF_STEP[torch.bfloat16] * (dz.abs() + err) + TINY[torch.bfloat16]
+    m, n = z.shape
+    dx, dw = cross_entropy_backward(x, w, label, lse, weight, dloss)
+    dx_err = g * (err @ d(w).abs() + (dz.abs() @ d(w).abs()) * (n + 64) * U32)
+    dw_err = g * (err.t() @ d(x).abs() + (dz.t().abs() @ d(x).abs()) * (m + 64) * U32)
+    if old is not None:
+        dw, dw_err = dw + d(old), dw_err + d(old).abs() * 2 * U32
+    return (dx, rounded(dx, dx_dtype, dx_err)), (dw, rounded(dw, dw_dtype, dw_err))

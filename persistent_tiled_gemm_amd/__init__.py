@@ -15,7 +15,8 @@ are torch.cuda streams (default: the current stream).
 The layer operators (include/ptg_layer.h) are bound in layer.py and re-exported
 here: layer_create, layer_destroy, layer_sync, layer_last_hip_error,
 layer_rmsnorm, layer_rmsnorm_backward, layer_linear, layer_activation_backward,
-layer_linear_backward.
+layer_linear_backward, layer_quantize, layer_cross_entropy,
+layer_cross_entropy_scratch, layer_cross_entropy_backward.
 """
 
 from __future__ import annotations
@@ -468,5 +469,7 @@ def matmul(A, B, mode="dynamic", plan: Optional[Plan] = None, stream=None):
     return C
 
 
-from .layer import (ACTIVATIONS, LAYER_ABI_FUNCTIONS, LayerPlan, layer_activation_backward, layer_create, layer_destroy,  # noqa: E402,F401
-                    layer_last_hip_error, layer_linear, layer_linear_backward, layer_rmsnorm, layer_rmsnorm_backward, layer_sync)
+from .layer import (ACTIVATIONS, LAYER_ABI_FUNCTIONS, LayerPlan, layer_activation_backward, layer_create,  # noqa: E402,F401
+                    layer_cross_entropy, layer_cross_entropy_backward, layer_cross_entropy_scratch, layer_destroy,
+                    layer_last_hip_error, layer_linear, layer_linear_backward, layer_quantize, layer_rmsnorm,
+                    layer_rmsnorm_backward, layer_sync)

@@ -260,9 +260,22 @@ void plan_units(const gemm_plan *p, bool grouped, int32_t mode, int64_t tiles, i
   *items = tiles - r + r * S;
 }
 
-// product, form: a layer operator's product instead of the plain GEMM (dynamic or non-persistent, one problem).
-gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, int64_t tiles, int64_t K,
-                   hipStream_t s, const ptg::ProductOpArgs *product = nullptr, int form = 0, int32_t split = 1, int64_t split_base_ = 0) {
+hipError_t launch_form(int edge, int form, int mode, const KernelArgs &args, const ptg::ProductOpArgs &op, const ptg::LossTerms &loss, int grid,
+                       hipStream_t s) {
+  switch (form) {
+    case ptg::kFormNTI8: return ptg::launch_product_i8(edge, mode, args, op, grid, s);
+    case ptg::kFormNNScaled:
+    case ptg::kFormTNScaled: return ptg::launch_product_scaled(edge, form, mode, args, op, grid, s);
+    case ptg::kFormLoss:
+    case ptg::kFormLogitGrad: return ptg::launch_product_loss(edge, form, mode, args, op, loss, grid, s);
+    default: return ptg::launch_product(edge, form, mode, args, op, grid, s);
+  }
+}
+
+// product, operands, form: a layer operator's product instead of the plain GEMM (dynamic or non-persistent, one problem).
+gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, int64_t tiles, int64_t K, hipStream_t s,
+                   const ptg::ProductOpArgs *product = nullptr, const ptg::ProductArgs *operands = nullptr, int form = 0, int32_t split = 1,
+                   int64_t split_base_ = 0) {
   if (mode < GEMM_SCHED_NONPERSISTENT || mode > GEMM_SCHED_DYNAMIC) return GEMM_E_INVALID_ARG;
   int64_t items = tiles, split_base = tiles;
   int32_t chunks = 1, group = 1;
@@ -294,7 +307,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
   args.ring_depth = p->desc.ring_depth;
   args.claim_lead = p->desc.claim_lead;
   args.claim_policy = p->desc.claim_policy;
-  args.raster_group = p->desc.raster == 1 ? p->desc.raster_group : 1;
+  args.raster_group = operands && operands->raster_group > 1 ? operands->raster_group : p->desc.raster == 1 ? p->desc.raster_group : 1;
   args.k_rotation = resolve_k_rotation(p->desc.k_rotation, grouped, args.single.N, p->desc.bn);
   args.counter_base = 0;
   if (mode == GEMM_SCHED_DYNAMIC && p->preset_pending) {
@@ -334,7 +347,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
     args.self_clean = 0;
   }
   args.log = p->d_log;
-  e = product ? ptg::launch_product(p->desc.bm, form, mode, args, *product, (int)grid, s)
+  e = product ? launch_form(p->desc.bm, form, mode, args, *product, operands->loss, (int)grid, s)
               : ptg::launch_gemm(p->desc.bm, mode, grouped, p->desc.b_layout == 1, args, (int)grid, p->dyn_lds, s);
   if (e != hipSuccess) return hip_fail(p, e, "kernel launch");
   if (!captured) ++p->runs;
@@ -423,7 +436,7 @@ float *plan_workspace(gemm_tile_cfg p, int64_t *floats) {
 gemm_status plan_status(gemm_tile_cfg p) { return read_device_status(p); }
 
 gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, int32_t split, int64_t split_base, hipStream_t s) {
-  const int64_t units = form == kFormNTE4m3 ? 2 : 1;  // values per 16-bit unit along k
+  const int64_t units = form_units(form);
   const int64_t K = a.k / units;
   const int64_t tm = ceil_div(a.m, p->desc.bm), tn = ceil_div(a.n, p->desc.bn);
   if (tm * tn > GEMM_MAX_TILES) return GEMM_E_SHAPE;
@@ -445,12 +458,15 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, in
   // one wave of workgroups needs no scheduler
   const int64_t items = split > 1 ? split_base + (tm * tn - split_base) * split : tm * tn;
   const int32_t mode = items <= (int64_t)p->cu_count * product_workgroups(p->desc.bm, form) ? GEMM_SCHED_NONPERSISTENT : GEMM_SCHED_DYNAMIC;
-  const gemm_status st = launch(p, mode, false, args, tm * tn, K, s, &op, form, split, split_base);
+  const gemm_status st = launch(p, mode, false, args, tm * tn, K, s, &op, &a, form, split, split_base);
   // the caller orders and waits for the plan's runs; the stream may have ended when this plan is used again
   p->follow = false;
   if (st != GEMM_OK || split <= 1) return st;
-  const hipError_t e = launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, (int32_t)split_base, (int32_t)(tm * tn - split_base),
-                                             split, s);
+  const int32_t first = (int32_t)split_base, tiles = (int32_t)(tm * tn - split_base);
+  const hipError_t e = form_is_loss(form) ? launch_reduce_loss(p->desc.bm, form, a.loss, p->d_ws, a.m, a.n, args.raster_group, first, tiles, split, s)
+                       : form == kFormNTI8 ? launch_reduce_i8(p->desc.bm, op, p->d_ws, a.m, a.n, first, tiles, split, s)
+                       : product_scales(form) == kScalesOne ? launch_reduce_scaled(p->desc.bm, op, p->d_ws, a.m, a.n, first, tiles, split, s)
+                                                            : launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, first, tiles, split, s);
   return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "split product");
 }
 

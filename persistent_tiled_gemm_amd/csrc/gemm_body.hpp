@@ -25,6 +25,9 @@
 //            ds_read_b64_tr_b16 delivers them from the row-major (n-contiguous)
 //            tile: in each 16-lane group, lane L reads 4 n values of row L/4 and
 //            lane i receives column i of the 4 x 16 block.
+// int8 operands (I8) are two values a 16-bit unit too, and their MFMA, 16 x 16 x 64,
+// takes a lane's 16 values where the bf16 one takes 8: nothing else in the main loop
+// differs. Their sums are 32-bit integers, exact.
 // An operand given the other way round takes the other one's layout: B as N x K
 // rows (BT) is staged and read like A, A as K x M rows (AT) like B. e4m3 operands
 // (E8, both K-contiguous) use A's layout byte for byte: the body counts K and the
@@ -319,13 +322,19 @@ __device__ __forceinline__ uint32_t claim_next(const KernelArgs &a, uint32_t xcc
   return claim_resolve(a, xcc, lane, raw, region);
 }
 
+// What an operation does with a whole tile's accumulators in registers: nothing
+// (they are staged for flush), or its own work on them in place of flush (stats:
+// nothing is staged) or before they are staged (values).
+enum DirectEpilogue { kDirectNone = 0, kDirectStats = 1, kDirectValues = 2 };
+
 // The plain product: fp32 C, row strides as long as the rows. BT: B is given as
 // N x K row-major (C = A . B^T); its stage then holds BN rows x 32 k like A's, and
 // its fragments are read like A's.
 template <bool BT_>
 struct PlainOp {
   struct Args {};
-  static constexpr bool AT = false, BT = BT_, E8 = false, kPlain = true, kWide = false;
+  static constexpr bool AT = false, BT = BT_, E8 = false, I8 = false, kPlain = true, kWide = false;
+  static constexpr int kDirect = kDirectNone;
   template <int EDGE> using Tile = typename TileCfg<EDGE>::type;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &pb, const Args &) { return pb.K; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &pb, const Args &) { return BT_ ? pb.K : pb.N; }
@@ -334,11 +343,12 @@ struct PlainOp {
 template <int BM, int BN, int MODE, bool GROUPED, class OP>
 __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename OP::Args &op) {
   using CF = typename OP::template Tile<BM>;
-  constexpr bool AT = OP::AT, BT = OP::BT, E8 = OP::E8;
+  constexpr bool AT = OP::AT, BT = OP::BT, E8 = OP::E8, I8 = OP::I8;
   // K-contiguous operands staged two k-steps (128 bytes of a row) at a time
   constexpr bool WA = OP::kWide && !AT, WB = OP::kWide && BT, WIDE = WA || WB;
   static_assert(!WIDE || CF::MB == 16, "wide stages are read in 16 x 16 blocks");
   static_assert(!E8 || (!AT && BT && CF::MB == 16), "e4m3 operands are both K-contiguous, in 16 x 16 blocks");
+  static_assert(!I8 || (!AT && BT && CF::MB == 16), "int8 operands are both K-contiguous, in 16 x 16 blocks");
   static_assert(CF::BM_ == BM && CF::BN_ == BN, "config");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::LDS];  // the stage ring
   __shared__ RingRec ring[kRingDepth];
@@ -791,14 +801,15 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       }
     };
 
-    typedef float accv __attribute__((ext_vector_type(CF::ACC_N)));
+    typedef typename std::conditional<I8, int, float>::type acc_t;
+    typedef acc_t accv __attribute__((ext_vector_type(CF::ACC_N)));
     accv acc[CF::MI][CF::NI];
 #pragma unroll
     for (int mi = 0; mi < CF::MI; ++mi)
 #pragma unroll
       for (int ni = 0; ni < CF::NI; ++ni)
 #pragma unroll
-        for (int e = 0; e < CF::ACC_N; ++e) acc[mi][ni][e] = 0.0f;
+        for (int e = 0; e < CF::ACC_N; ++e) acc[mi][ni][e] = 0;
 
     // the MFMAs of one 16-deep k slice, 32 x 32 blocks (the 16 x 16 main loop
     // issues its own)
@@ -944,7 +955,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // only by MFMAs; the fences before and after the loop give the wait
         // states the compiler cannot see.
         auto mfma16 = [&](int mi, int ni, const frag &a, const frag &b) {
-          asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[mi][ni]) : "v"(b), "v"(a) : "memory");
+          if constexpr (I8) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc[mi][ni]) : "v"(b), "v"(a) : "memory");
+          else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[mi][ni]) : "v"(b), "v"(a) : "memory");
         };
         // per-lane load offsets of a k-step with no partial K (see load_voff_edge)
         uint32_t voff_fast[kLoads];
@@ -1274,19 +1286,54 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     };
     auto epi_end = [&]() { wg_barrier(); };
 
-    if (!OP::kPlain || !split) {
+    // a group of four sums as the staging carries them (bits, where they are integers)
+    auto sums = [&](int mi, int ni, int qd) -> f32x4 {
+      typedef acc_t acc4 __attribute__((ext_vector_type(4)));
+      return __builtin_bit_cast(f32x4, acc4{acc[mi][ni][4 * qd + 0], acc[mi][ni][4 * qd + 1], acc[mi][ni][4 * qd + 2], acc[mi][ni][4 * qd + 3]});
+    };
+    bool staged = !OP::kPlain || !split;
+    if constexpr (OP::kDirect == kDirectStats) {
+      if (!split) {
+        // nothing is staged, but loads past the unit still write the stages that the next one fills
+        epi_begin();
+        OP::template stats<CF>(acc, lane, m0 + (int32_t)(wm * CF::WM), n0 + (int32_t)(wn * CF::WN), M, N);
+        staged = false;
+      }
+    }
+    if (staged) {
+      auto stage_row = [&](int p, int mi) {
+#pragma unroll
+        for (int ni = 0; ni < CF::NI; ++ni)
+#pragma unroll
+          for (int qd = 0; qd < CF::QUADS; ++qd) stage(p, mi, ni, qd, sums(mi, ni, qd));
+      };
       epi_begin();
+      if constexpr (OP::kDirect == kDirectValues) {
+        if (!split) {
+          const auto rows = OP::template rows<CF>(lane, m0 + (int32_t)(wm * CF::WM), n0 + (int32_t)(wn * CF::WN), M);
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
+          for (int p = 0; p < PASSES; ++p) {
 #pragma unroll
-        for (int mi = p * MI_PASS; mi < (p + 1) * MI_PASS; ++mi)
+            for (int mi = p * MI_PASS; mi < (p + 1) * MI_PASS; ++mi)
+              OP::template values<CF>(rows, mi, [&](int ni) { asm volatile("" : "+a"(acc[mi][ni])); }, [&](int ni) { return sums(mi, ni, 0); }, [&](int ni, const f32x4 &v) { stage(p, mi, ni, 0, v); });
+            flush(p);
+          }
+          staged = false;
+        }
+      }
+      if (staged) {
 #pragma unroll
-          for (int ni = 0; ni < CF::NI; ++ni)
+        for (int p = 0; p < PASSES; ++p) {
 #pragma unroll
-            for (int qd = 0; qd < CF::QUADS; ++qd)
-              stage(p, mi, ni, qd, f32x4{acc[mi][ni][4 * qd + 0], acc[mi][ni][4 * qd + 1], acc[mi][ni][4 * qd + 2],
-                                         acc[mi][ni][4 * qd + 3]});
-        flush(p);
+          for (int mi = p * MI_PASS; mi < (p + 1) * MI_PASS; ++mi) {
+            if constexpr (OP::kDirect != kDirectNone) {
+#pragma unroll
+              for (int ni = 0; ni < CF::NI; ++ni) asm volatile("" : "+a"(acc[mi][ni]));
+            }
+            stage_row(p, mi);
+          }
+          flush(p);
+        }
       }
       epi_end();
     } else if constexpr (OP::kPlain) {

@@ -10,7 +10,8 @@
 #include "layer_internal.hpp"
 #include "ptg_layer.h"
 
-static_assert(LAYER_F32 == ptg::kTypeF32 && LAYER_BF16 == ptg::kTypeBf16 && LAYER_E4M3 == ptg::kTypeE4m3, "types");
+static_assert(LAYER_F32 == ptg::kTypeF32 && LAYER_BF16 == ptg::kTypeBf16 && LAYER_E4M3 == ptg::kTypeE4m3 &&
+                  LAYER_I8 == ptg::kTypeI8, "types");
 static_assert(LAYER_ACT_NONE == ptg::kActNone && LAYER_ACT_RELU == ptg::kActRelu && LAYER_ACT_GELU == ptg::kActGelu &&
                   LAYER_ACT_GELU_TANH == ptg::kActGeluTanh && LAYER_ACT_SILU == ptg::kActSilu, "activations");
 
@@ -20,6 +21,8 @@ struct layer_plan {
   gemm_tile_cfg tiles256 = nullptr, tiles128 = nullptr;  // the tiled products' plans
   float *ws = nullptr;             // partial sums: the 256 x 256 plan's workspace
   int64_t ws_floats = 0;
+  float *ws128 = nullptr;          // and the 128 x 128 plan's
+  int64_t ws128_floats = 0;
   uint32_t *d_arrivals = nullptr;  // arrival counts of the few-row product's shared tiles, zero between calls
   hipEvent_t stream_switch = nullptr;
   hipStream_t last_stream = nullptr;
@@ -139,10 +142,11 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55 (chosen: the last eight in 13
 // chunks, whose fit is 40 and whose time 49).
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
-  const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN;
-  const int64_t nk = ceil_div(e8 ? a.k / 2 : a.k, 32), line = e8 ? 64 : 32;
-  const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (form != ptg::kFormNN && a.ldb % line != 0));
-  const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : form == ptg::kFormNT ? 1.13 : 1.05) : 1.0;
+  const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN || form == ptg::kFormTNScaled;
+  const bool nn = form == ptg::kFormNN || form == ptg::kFormNNScaled;
+  const int64_t units = ptg::form_units(form), nk = ceil_div(a.k / units, 32), line = 32 * units;
+  const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (!nn && a.ldb % line != 0));
+  const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : nn ? 1.05 : 1.13) : 1.0;
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
     const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
@@ -177,16 +181,36 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   return best;
 }
 
-gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStream_t s) {
-  const TileChoice c = choose_tiles(a, form, p->cu_count);
+gemm_status run_choice(layer_plan *p, const ptg::ProductArgs &a, int form, const TileChoice &c, hipStream_t s) {
   gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
   gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
   if (st == GEMM_E_HIP) std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));
   return st;
 }
 
+gemm_status run_tiles(layer_plan *p, const ptg::ProductArgs &a, int form, hipStream_t s) {
+  return run_choice(p, a, form, choose_tiles(a, form, p->cu_count), s);
+}
+
 // The stride the kernels get: a matrix of one row has its row's length, whatever the caller said.
 int64_t stride_of(int64_t ld, int64_t m, int64_t n) { return m > 1 && n > 0 ? ld : std::max<int64_t>(n, 8); }
+
+// The logits of a cross entropy, m x n, as a product.
+ptg::ProductArgs loss_product(const void *x, const void *w, int64_t ldx, int64_t ldw, int64_t m, int64_t n, int64_t kk) {
+  ptg::ProductArgs k;
+  std::memset(&k, 0, sizeof(k));
+  k.a = x;
+  k.b = w;
+  k.lda = stride_of(ldx, m, kk);
+  k.ldb = stride_of(ldw, n, kk);
+  k.m = (int32_t)m;
+  k.n = (int32_t)n;
+  k.k = (int32_t)kk;
+  // w is many times the caches: all of x's rows of tiles, up to 32, meet a column of w's
+  // together, so that w comes from memory once
+  k.raster_group = 32;
+  return k;
+}
 
 // Partial sums of n columns over at most `wanted` rows: as many rows as the
 // workspace holds (a chunk of 256 x 256 a CU: 16 rows of the widest matrix).
@@ -233,6 +257,7 @@ gemm_status layer_create(layer_cfg *out, int32_t device) {
     return st;
   }
   p->ws = ptg::plan_workspace(p->tiles256, &p->ws_floats);
+  p->ws128 = ptg::plan_workspace(p->tiles128, &p->ws128_floats);
   *out = p;
   return GEMM_OK;
 }
@@ -359,7 +384,7 @@ gemm_status layer_rmsnorm_backward(const layer_rmsnorm_grad_args *a, layer_cfg p
 
 gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) {
   if (!a || !p) return GEMM_E_INVALID_ARG;
-  const bool e8 = a->in_type == LAYER_E4M3;
+  const bool e8 = a->in_type == LAYER_E4M3 || a->in_type == LAYER_I8;  // one byte, with scales
   if ((!e8 && a->in_type != LAYER_BF16) || (a->bias && !stream_type(a->bias_type)) ||
       (a->residual && !stream_type(a->residual_type)) || !stream_type(a->out_type) || a->activation < LAYER_ACT_NONE ||
       a->activation > LAYER_ACT_SILU || (!e8 && (a->x_scale || a->w_scale)))
@@ -367,7 +392,8 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   const int64_t step = e8 ? 16 : 8;
   if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, step) || a->n > LAYER_MAX_COLS || bad_stride(a->ldx, a->m, a->k, step) ||
       bad_stride(a->ldw, a->n, a->k, step) || bad_stride(a->ldo, a->m, a->n, 8) ||
-      (a->residual && bad_stride(a->ldr, a->m, a->n, 8)) || (a->pre && bad_stride(a->ldp, a->m, a->n, 8)))
+      (a->residual && bad_stride(a->ldr, a->m, a->n, 8)) || (a->pre && bad_stride(a->ldp, a->m, a->n, 8)) ||
+      (a->in_type == LAYER_I8 && a->k > LAYER_MAX_I8_K))
     return GEMM_E_SHAPE;
   if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->x_scale) || !aligned16(a->w_scale) || !aligned16(a->bias) ||
       !aligned16(a->residual) || !aligned16(a->pre) || !aligned16(a->out))
@@ -401,13 +427,13 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
-  if (ptg::rows_preferred(k, e8)) {
+  if (ptg::rows_preferred(k, a->in_type)) {
     int64_t tiles = 0;
-    if (ptg::rows_partial_floats(k, e8, p->cu_count, &tiles) > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
-    hipError_t e = ptg::launch_rows(k, e8, p->ws, p->d_arrivals, p->cu_count, s);
+    if (ptg::rows_partial_floats(k, a->in_type, p->cu_count, &tiles) > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
+    hipError_t e = ptg::launch_rows(k, a->in_type, p->ws, p->d_arrivals, p->cu_count, s);
     return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
   }
-  return run_tiles(p, k, e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
+  return run_tiles(p, k, a->in_type == LAYER_I8 ? ptg::kFormNTI8 : e8 ? ptg::kFormNTE4m3 : ptg::kFormNT, s);
 }
 
 gemm_status layer_activation_backward(const layer_activation_grad_args *a, layer_cfg p, void *stream) {
@@ -508,6 +534,182 @@ gemm_status layer_linear_backward(const layer_linear_grad_args *a, layer_cfg p, 
     k.ep.residual_type = a->dw_type;
     st = run_tiles(p, k, ptg::kFormTN, s);
     if (st != GEMM_OK) return st;
+  }
+  return GEMM_OK;
+}
+
+gemm_status layer_quantize(const layer_quantize_args *a, void *stream) {
+  if (!a) return GEMM_E_INVALID_ARG;
+  if (!stream_type(a->type) || (a->out_type != LAYER_I8 && a->out_type != LAYER_E4M3)) return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || bad_stride(a->ldx, a->m, a->n, 8) || bad_stride(a->ldo, a->m, a->n, 8)) return GEMM_E_SHAPE;
+  if (a->m == 0 || a->n == 0) return GEMM_OK;
+  if (!a->x || !a->out || !a->scale || !aligned16(a->x) || !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->scale) & 3u))
+    return GEMM_E_INVALID_ARG;
+  int cus = 0;
+  const gemm_status st = current_gfx950(&cus);
+  if (st != GEMM_OK) return st;
+  ptg::QuantiseArgs k;
+  std::memset(&k, 0, sizeof(k));
+  k.x = a->x;
+  k.out = a->out;
+  k.scale = a->scale;
+  k.ldx = stride_of(a->ldx, a->m, a->n);
+  k.ldo = stride_of(a->ldo, a->m, a->n);
+  k.m = (int32_t)a->m;
+  k.n = (int32_t)a->n;
+  k.type = a->type;
+  k.out_type = a->out_type;
+  return ptg::launch_quantise(k, cus, static_cast<hipStream_t>(stream)) == hipSuccess ? GEMM_OK : GEMM_E_HIP;
+}
+
+gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
+      (a->m > 0 && a->n == 0))
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->x) || !aligned16(a->w) || (reinterpret_cast<uintptr_t>(a->label) & 7u) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a->loss) & 3u))
+    return GEMM_E_INVALID_ARG;
+  if (a->m > 0 && (!a->label || !a->lse || a->lse == a->loss || (a->k > 0 && (!a->x || !a->w)))) return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK || a->m == 0) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  ptg::ProductArgs k = loss_product(a->x, a->w, a->ldx, a->ldw, a->m, a->n, a->k);
+  k.loss.label = a->label;
+  k.loss.picked = a->lse;
+  k.loss.entries = a->n;
+  hipError_t e;
+  if (ptg::rows_preferred(k, LAYER_BF16)) {
+    int64_t tiles = 0;
+    const int64_t parts = ceil_div(ptg::rows_partial_floats(k, LAYER_BF16, p->cu_count, &tiles), 2) * 2;
+    const int64_t blocks = ceil_div(a->n, ptg::rows_loss_block(k, p->cu_count));
+    if (parts + 2 * blocks * a->m > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
+    k.loss.partial = reinterpret_cast<float2 *>(p->ws + parts);
+    e = ptg::launch_rows_loss(k, p->ws, p->d_arrivals, p->cu_count, s);
+    if (e != hipSuccess) return hip_fail(p, e, "cross entropy");
+    e = ptg::launch_loss_join(k.loss.partial, (int32_t)blocks, a->label, a->n, a->lse, a->loss, k.m, s);
+    return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "cross entropy");
+  }
+  // Tiles, in as many runs over the rows as the blocks' partial sums need. Those lie in the
+  // workspace that the run's own split tiles leave free.
+  const int64_t blocks128 = ceil_div(a->n, ptg::loss_block(128));
+  const int64_t most = std::max<int64_t>(256, std::min(p->ws_floats, p->ws128_floats * 2) / (2 * blocks128) / 256 * 256);
+  const int64_t runs = ceil_div(a->m, most), rows = ceil_div(ceil_div(a->m, runs), 256) * 256;
+  for (int64_t first = 0; first < a->m; first += rows) {
+    k.m = (int32_t)std::min(rows, a->m - first);
+    k.a = static_cast<const uint16_t *>(a->x) + first * k.lda;
+    k.loss.label = a->label + first;
+    k.loss.picked = a->lse + first;
+    const TileChoice c = choose_tiles(k, ptg::kFormLoss, p->cu_count);
+    const int64_t blocks = ceil_div(a->n, ptg::loss_block(c.edge));
+    float *at = c.edge == 256 && c.split > 1 ? p->ws128 : p->ws;
+    if (2 * blocks * k.m > (at == p->ws ? p->ws_floats : p->ws128_floats)) return GEMM_E_SHAPE;
+    k.loss.partial = reinterpret_cast<float2 *>(at);
+    st = run_choice(p, k, ptg::kFormLoss, c, s);
+    if (st != GEMM_OK) return st;
+    e = ptg::launch_loss_join(k.loss.partial, (int32_t)blocks, k.loss.label, a->n, a->lse + first, a->loss ? a->loss + first : nullptr, k.m, s);
+    if (e != hipSuccess) return hip_fail(p, e, "cross entropy");
+  }
+  return GEMM_OK;
+}
+
+int64_t layer_cross_entropy_scratch(int64_t m, int64_t n, int64_t k, int32_t pieces) {
+  if (bad_size(m, n, 8) || bad_size(m, k, 8) || pieces < 1) return -1;
+  // pieces of whole 256s of the vocabulary: no more of them than asked for
+  const int64_t piece = std::min(ceil_div(ceil_div(n, pieces), 256) * 256, n);
+  return 2 * m * piece + (piece < n ? 4 * m * k : 0);
+}
+
+gemm_status layer_cross_entropy_backward(const layer_cross_entropy_grad_args *a, layer_cfg p, void *stream) {
+  if (!a || !p) return GEMM_E_INVALID_ARG;
+  if ((a->dx && !stream_type(a->dx_type)) || (a->dw && !stream_type(a->dw_type)) || a->accumulate < 0 || a->accumulate > 1)
+    return GEMM_E_INVALID_ARG;
+  if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
+      (a->dx && bad_stride(a->lddx, a->m, a->k, 8)) || (a->dw && bad_stride(a->lddw, a->n, a->k, 8)) || (a->m > 0 && a->n == 0) ||
+      a->scratch_bytes < 0)
+    return GEMM_E_SHAPE;
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->dx) || !aligned16(a->dw) || !aligned16(a->scratch) ||
+      (reinterpret_cast<uintptr_t>(a->label) & 7u) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(a->weight) & 3u) || (reinterpret_cast<uintptr_t>(a->dloss) & 3u))
+    return GEMM_E_INVALID_ARG;
+  const bool any_dx = a->dx && a->m > 0 && a->k > 0;
+  const bool any_dw = a->dw && a->n > 0 && a->k > 0 && !(a->m == 0 && a->accumulate);
+  if ((any_dx || any_dw) && a->m > 0 && (!a->x || !a->w || !a->label || !a->lse || !a->scratch)) return GEMM_E_INVALID_ARG;
+  gemm_status st = check_device(p);
+  if (st != GEMM_OK || (!any_dx && !any_dw)) return st;
+  // The piece: as many whole 256s of the vocabulary as the scratch holds. With more than
+  // one, dx is added up in fp32: in dx itself, or before the pieces in the scratch.
+  const int64_t all = 2 * a->m * a->n;
+  int64_t piece = a->n, sums = 0;
+  if (a->m > 0 && a->scratch_bytes < all) {
+    sums = any_dx && a->dx_type == LAYER_BF16 ? 4 * a->m * a->k : 0;
+    piece = (a->scratch_bytes - sums) / (2 * a->m) / 256 * 256;
+    if (a->scratch_bytes < sums || piece < 256) return GEMM_E_SHAPE;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  st = order_after_last_stream(p, s);
+  if (st != GEMM_OK) return st;
+  if (a->m == 0) piece = a->n;  // dw = 0, in one go
+  uint16_t *dz = a->m > 0 ? reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(a->scratch) + sums) : nullptr;
+  const int64_t ldx = stride_of(a->ldx, a->m, a->k), ldw = stride_of(a->ldw, a->n, a->k);
+  const int64_t lddx = stride_of(a->lddx, a->m, a->k), lddw = stride_of(a->lddw, a->n, a->k);
+  for (int64_t first = 0; first < a->n; first += piece) {
+    const int64_t cols = std::min(piece, a->n - first);
+    const uint16_t *w = static_cast<const uint16_t *>(a->w) + first * ldw;
+    ptg::ProductArgs k;
+    if (a->m > 0) {
+      k = loss_product(a->x, w, a->ldx, ldw, a->m, cols, a->k);
+      k.loss.label = a->label;
+      k.loss.lse = a->lse;
+      k.loss.weight = a->weight;
+      k.loss.dz = dz;
+      k.loss.lddz = piece;
+      k.loss.first = first;
+      k.loss.entries = a->n;
+      st = run_tiles(p, k, ptg::kFormLogitGrad, s);
+      if (st != GEMM_OK) return st;
+    }
+    if (any_dx) {
+      const bool last = first + cols == a->n, in_dx = sums == 0;
+      std::memset(&k, 0, sizeof(k));
+      k.a = dz;
+      k.b = w;
+      k.lda = piece;
+      k.ldb = ldw;
+      k.m = (int32_t)a->m;
+      k.n = (int32_t)a->k;
+      k.k = (int32_t)cols;
+      k.ep.row_scale = a->dloss;
+      k.ep.residual = first == 0 ? nullptr : in_dx ? a->dx : a->scratch;
+      k.ep.residual_type = LAYER_F32;
+      k.ep.ldr = in_dx ? lddx : a->k;
+      k.ep.out = last || in_dx ? a->dx : a->scratch;
+      k.ep.out_type = last || in_dx ? a->dx_type : LAYER_F32;
+      k.ep.ldo = last || in_dx ? lddx : a->k;
+      st = run_tiles(p, k, ptg::kFormNNScaled, s);
+      if (st != GEMM_OK) return st;
+    }
+    if (any_dw) {
+      std::memset(&k, 0, sizeof(k));
+      k.a = dz;
+      k.b = a->x;
+      k.lda = piece;
+      k.ldb = ldx;
+      k.m = (int32_t)cols;
+      k.n = (int32_t)a->k;
+      k.k = (int32_t)a->m;
+      k.ep.row_scale = a->m > 0 ? a->dloss : nullptr;  // (0 times an infinity)
+      k.ep.out = static_cast<unsigned char *>(a->dw) + first * lddw * (a->dw_type == LAYER_F32 ? 4 : 2);
+      k.ep.ldo = lddw;
+      k.ep.out_type = a->dw_type;
+      k.ep.residual = a->accumulate ? k.ep.out : nullptr;
+      k.ep.ldr = lddw;
+      k.ep.residual_type = a->dw_type;
+      st = run_tiles(p, k, ptg::kFormTNScaled, s);
+      if (st != GEMM_OK) return st;
+    }
   }
   return GEMM_OK;
 }

@@ -10,7 +10,7 @@
 
 namespace ptg {
 
-enum LayerType { kTypeF32 = 0, kTypeBf16 = 1, kTypeE4m3 = 2 };
+enum LayerType { kTypeF32 = 0, kTypeBf16 = 1, kTypeE4m3 = 2, kTypeI8 = 3 };
 enum LayerAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
 struct NormArgs {
@@ -21,6 +21,15 @@ struct NormArgs {
   int32_t m, n;
   int32_t type, weight_type, out_type;
   float eps;
+};
+
+struct QuantiseArgs {
+  const void *x;
+  void *out;
+  float *scale;
+  int64_t ldx, ldo;
+  int32_t m, n;
+  int32_t type, out_type;
 };
 
 struct NormGradArgs {
@@ -53,6 +62,19 @@ struct EpilogueArgs {
   int32_t act;
 };
 
+// What the products of a cross entropy make of their logits z (m rows, a column for each of the vocabulary's entries).
+struct LossTerms {
+  const int64_t *label;  // m; negative: the row is not counted
+  const float *lse;      // gradient: m
+  const float *weight;   // gradient: m, or NULL
+  float *picked;         // loss: m, the label's logit
+  float2 *partial;       // loss: [column block][m], each block's largest logit and the sum of exp(z - it)
+  void *dz;              // gradient: m x n, bf16
+  int64_t lddz;
+  int64_t first;         // the vocabulary's entry of column 0
+  int64_t entries;       // of the whole vocabulary
+};
+
 // The operands of a product out[m][n] = sum_k A(m, k) B(n, k), each with the
 // contracted index along its rows ("k-contiguous") or down its columns.
 struct ProductArgs {
@@ -60,6 +82,8 @@ struct ProductArgs {
   int64_t lda, ldb;
   int32_t m, n, k;
   EpilogueArgs ep;
+  LossTerms loss;        // the loss forms', in the epilogue's place
+  int32_t raster_group;  // tile rows that are walked together, column by column (0: rows of tiles one by one)
 };
 
 // Forms of a product, by operand layout and type.
@@ -67,10 +91,23 @@ enum ProductForm {
   kFormNT = 0,     // A m x k, B n x k, bf16: a linear layer
   kFormNN = 1,     // A m x k, B k x n, bf16: the gradient of x
   kFormTN = 2,     // A k x m, B k x n, bf16: the gradient of w
-  kFormNTE4m3 = 3  // A m x k, B n x k, e4m3
+  kFormNTE4m3 = 3, // A m x k, B n x k, e4m3
+  kFormNTI8 = 4,   // A m x k, B n x k, int8
+  kFormNNScaled = 5,  // kFormNN and kFormTN with one factor, read from the device, for all sums
+  kFormTNScaled = 6,
+  kFormLoss = 7,      // kFormNT's sums as logits: each row's maximum and sum of exponentials by column blocks
+  kFormLogitGrad = 8  // kFormNT's sums as logits: their gradient
 };
+constexpr bool form_is_loss(int form) { return form == kFormLoss || form == kFormLogitGrad; }
+constexpr int64_t form_units(int form) { return form == kFormNTE4m3 || form == kFormNTI8 ? 2 : 1; }  // values per 16 bits along k
+// The factors that a form's epilogue takes: of each row and column, or one (at row_scale).
+enum ProductScales { kScalesNone = 0, kScalesRowCol = 1, kScalesOne = 2 };
+constexpr int product_scales(int form) {
+  return form == kFormNTE4m3 || form == kFormNTI8 ? kScalesRowCol : form == kFormNNScaled || form == kFormTNScaled ? kScalesOne : kScalesNone;
+}
 
 hipError_t launch_rmsnorm(const NormArgs &a, int cu_count, hipStream_t s);
+hipError_t launch_quantise(const QuantiseArgs &a, int cu_count, hipStream_t s);
 // Rows of the partial sums that launch_rmsnorm_backward writes for m x n.
 int rmsnorm_partial_rows(int32_t m, int32_t n, int cu_count);
 hipError_t launch_rmsnorm_backward(const NormGradArgs &a, int cu_count, hipStream_t s);
@@ -88,10 +125,14 @@ struct RowsArgs {
   int32_t ldx, ldw, m, n, k;
 };
 // Whether a product (k-contiguous operands) runs there rather than as tiles.
-bool rows_preferred(const ProductArgs &p, bool e8);
+// (type: of both operands)
+bool rows_preferred(const ProductArgs &p, int type);
 // Workspace of a call, floats; *tiles: the arrival counts it uses.
-int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t *tiles);
-hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
+int64_t rows_partial_floats(const ProductArgs &p, int type, int cu_count, int64_t *tiles);
+hipError_t launch_rows(const ProductArgs &p, int type, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
+// A cross entropy's end of the same product (bf16): p.loss, in column blocks of rows_loss_block.
+int32_t rows_loss_block(const ProductArgs &p, int cu_count);
+hipError_t launch_rows_loss(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
 
 // What a tiled product takes beside the GEMM's own arguments. Row strides in
 // 16-bit units (two e4m3 values), as the GEMM's body counts them.
@@ -100,12 +141,30 @@ struct ProductOpArgs {
   int32_t lda, ldb;
 };
 // Workgroups of the tiled product that a CU holds at once.
-constexpr int product_workgroups(int tile_edge, int form) { return tile_edge == 128 && form == kFormTN ? 2 : 1; }
+constexpr int product_workgroups(int tile_edge, int form) {
+  return tile_edge == 128 && (form == kFormTN || form == kFormTNScaled) ? 2 : 1;
+}
 // mode: kDynamic or kNonPersistent
 hipError_t launch_product(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+// The same for the int8 form, the scaled forms and the loss forms.
+hipError_t launch_product_i8(int tile_edge, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+hipError_t launch_product_scaled(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
+                               int grid, hipStream_t s);
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s);
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
+                            int32_t chunks, hipStream_t s);
+hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
+                                int32_t chunks, hipStream_t s);
+hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+                              int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
+// Columns of a block that leaves one partial maximum and sum: the tiles' and the few-row kernel's.
+constexpr int32_t loss_block(int tile_edge) { return tile_edge / 2; }
+// lse and loss of m rows from `blocks` partial maxima and sums each; lse holds the labels' logits before.
+hipError_t launch_loss_join(const float2 *partial, int32_t blocks, const int64_t *label, int64_t entries, float *lse, float *loss, int32_t m,
+                            hipStream_t s);
 // A plan's split-tail workspace, for other partial sums between its runs.
 float *plan_workspace(gemm_tile_cfg plan, int64_t *floats);
 // The product as a run of a GEMM plan: its tiles and dynamic scheduler; the tiles

@@ -1,0 +1,337 @@
+// Softmax cross entropy of an output head, z = x w^T with a column for each of the
+// vocabulary's entries, without the logits z reaching memory.
+//
+// Loss: the product's tiles (gemm_body.hpp, both operands k-contiguous) end in each
+// row's maximum and sum of exp(z - maximum) over the wave's columns, taken from the
+// accumulators as they lie in registers: a lane holds a quarter of a row's columns,
+// two exchanges between lanes join the quarters. 8 bytes a row and block of 128 columns
+// go to memory in place of 256 or 512; a second launch joins the blocks,
+//   lse = M + log sum_b s_b exp(m_b - M),  loss = lse - z_label,
+// in block order, so nothing depends on the order of workgroups. The wave that holds a
+// label's column writes its logit.
+//
+// Gradient: the same tiles, computed again, end in dz = weight (exp(z - lse) - [label]),
+// rounded to bf16, for the two products that follow. Half a step of bf16 is 2^-9 to 2^-8
+// of each dz; the loss's own factor (a mean's 1 / count) is left to those products'
+// epilogues, so that it is not rounded with dz, and the label's entry of an
+// unpredicted token, -1 + p, is exact to p.
+//
+// Bound by MFMA issue, as the product is.
+#include "loss_device.hpp"
+#include "product_op.hpp"
+
+namespace ptg {
+
+struct LossKernelArgs {
+  KernelArgs gemm;
+  ProductOpArgs op;
+  LossTerms loss;
+};
+
+__device__ __forceinline__ LossTerms loss_terms() { return late_args<LossTerms, offsetof(LossKernelArgs, loss)>(); }
+
+// What the gradient takes of a row: exp(z - lse) = 2^(z log2 e - offset), dz = factor (that
+// - [column == at]). A row that is not counted has factor 0, and its dz are zeros whatever
+// its logits are, NaN included. A label past the vocabulary is a mistake, shown as NaN.
+struct RowGrad { float offset, factor; int32_t at; };
+__device__ __forceinline__ RowGrad row_grad(const LossTerms &l, int64_t m) {
+  const int64_t label = l.label[m];
+  RowGrad r;
+  r.offset = l.lse[m] * kLog2E;
+  r.factor = label < 0 ? 0.0f : label >= l.entries ? __uint_as_float(0x7fc00000u) : l.weight ? l.weight[m] : 1.0f;
+  const int64_t at = label - l.first;
+  r.at = at < 0 || at >= (int64_t)1 << 30 ? -1 : (int32_t)at;
+  return r;
+}
+__device__ __forceinline__ float probability(float z, const RowGrad &r) { return __builtin_amdgcn_exp2f(fmaf(z, kLog2E, -r.offset)); }
+__device__ __forceinline__ float times_factor(float factor, float v) { return factor == 0.0f ? 0.0f : factor * v; }
+
+template <int FORM>
+struct LossOp {
+  using Args = ProductOpArgs;
+  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true;
+  static constexpr int kDirect = FORM == kFormLoss ? kDirectStats : kDirectValues;
+  template <int EDGE> using Tile = ProductOp<kFormNT>::Tile<EDGE>;
+  static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
+  static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
+
+  // The wave's WM x WN accumulators: lane l holds, of row l mod 16 of its MI blocks of
+  // rows, the columns 16 ni + 4 (l / 16) + 0..3. Two blocks at a time (their exchanges
+  // between lanes overlap; more do not fit the registers).
+  template <class CF, class Acc>
+  static __device__ __forceinline__ void stats(Acc &acc, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+    static_assert(CF::MB == 16 && CF::WN == loss_block(CF::BN_), "blocks");
+    if (n_base >= N) return;  // a block past the vocabulary
+    if (n_base + CF::WN > N) stats_of<CF, true>(acc, lane, m_base, n_base, M, N);
+    else stats_of<CF, false>(acc, lane, m_base, n_base, M, N);
+  }
+  template <class CF, bool EDGE, class Acc>
+  static __device__ __forceinline__ void stats_of(Acc &acc, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+    constexpr int MI = CF::MI, NI = CF::NI, G = 2;
+    const LossTerms l = loss_terms();
+    asm volatile("" : "+v"(lane));
+    const uint32_t quarter = lane >> 4;
+    const int32_t row = m_base + (int32_t)(lane & 15u), left = N - n_base - (int32_t)(4u * quarter);
+    int32_t at[MI];  // the row's label, from the lane's first column on, where it is one of the lane's
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int32_t m = row + 16 * mi;
+      const int64_t label = m < M ? l.label[m] : -1;
+      const int64_t off = label - l.first - n_base;
+      at[mi] = label >= 0 && off >= 0 && off < CF::WN && (((uint32_t)off >> 2) & 3u) == quarter ? (int32_t)off - (int32_t)(4u * quarter) : -1;
+    }
+    float2 *out = l.partial + (size_t)(n_base / CF::WN) * (size_t)M;
+#pragma unroll
+    for (int g = 0; g < MI; g += G) {
+      // the sums leave their accumulator registers here, a group at a time
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) asm volatile("" : "+a"(acc[g + u][ni]));
+      // columns past the vocabulary add nothing
+      auto logit = [&](int u, int ni, int e) -> float {
+        const float z = acc[g + u][ni][e];
+        return !EDGE || 16 * ni + e < left ? z : -INFINITY;
+      };
+      float top[G], sum[G];
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        top[u] = -INFINITY;
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[u] = fmaxf(top[u], logit(u, ni, e));
+      }
+#pragma unroll
+      for (int o = 16; o < 64; o <<= 1)
+#pragma unroll
+        for (int u = 0; u < G; ++u) top[u] = fmaxf(top[u], __shfl_xor(top[u], o, 64));
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        const float offset = offset_of(top[u]);
+        float s = 0.0f;
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(logit(u, ni, e), kLog2E, -offset));
+        sum[u] = put_right(s, top[u], offset);
+        if (__ballot(at[g + u] >= 0)) {  // few tiles hold a label of theirs
+          float picked = 0.0f;
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) picked = at[g + u] == 16 * ni + e ? acc[g + u][ni][e] : picked;
+          if (at[g + u] >= 0) l.picked[row + 16 * (g + u)] = picked;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o < 64; o <<= 1)
+#pragma unroll
+        for (int u = 0; u < G; ++u) sum[u] += __shfl_xor(sum[u], o, 64);
+      // each quarter of the lanes writes a quarter of the rows
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        const int32_t m = row + 16 * (g + u);
+        if ((uint32_t)((g + u) & 3) == quarter && m < M) out[m] = make_float2(top[u], sum[u]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  // The gradient: what a lane needs of its rows, and the logits of a block of rows to dz on
+  // their way into the staging.
+  template <class CF> struct Rows { RowGrad r[CF::MI]; };
+  template <class CF>
+  static __device__ __forceinline__ Rows<CF> rows(uint32_t lane, int32_t m_base, int32_t n_base, int32_t M) {
+    const LossTerms l = loss_terms();
+    asm volatile("" : "+v"(lane));
+    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * (lane >> 4));
+    Rows<CF> f;
+#pragma unroll
+    for (int mi = 0; mi < CF::MI; ++mi) {
+      const int32_t m = row + 16 * mi;
+      f.r[mi] = {0.0f, 0.0f, -1};
+      if (m < M) f.r[mi] = row_grad(l, m);
+      f.r[mi].at -= first;
+    }
+    return f;
+  }
+  template <class CF, class Hold, class Get, class Put>
+  static __device__ __forceinline__ void values(const Rows<CF> &f, int mi, Hold hold, Get get, Put put) {
+    const RowGrad &r = f.r[mi];
+    const bool none = r.factor == 0.0f;
+    auto block = [&](int ni, bool labelled) {
+      hold(ni);  // in the accumulators until here
+      const f32x4 z = get(ni);
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float p = probability(z[e], r);
+        if (labelled) p -= r.at == 16 * ni + e ? 1.0f : 0.0f;
+        v[e] = none ? 0.0f : p * r.factor;
+      }
+      put(ni, v);
+    };
+    // few tiles hold a label of theirs
+    if (__ballot(r.at >= 0 && r.at < CF::WN)) {
+#pragma unroll
+      for (int ni = 0; ni < CF::NI; ++ni) block(ni, true);
+    } else {
+#pragma unroll
+      for (int ni = 0; ni < CF::NI; ++ni) block(ni, false);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Staged rows (see ProductOp) to memory: a K-chunk's sums as they are, or dz in bf16.
+  template <int RP, int ROW_B, int STRIDE>
+  static __device__ __forceinline__ void flush(const Args &, const unsigned char *wl, uint32_t lane, int32_t m_base, int32_t n_base,
+                                               int32_t M, int32_t N, float *slot) {
+    constexpr int LPR = ROW_B / 32, RPI = 64 / LPR;
+    asm volatile("" : "+v"(lane));
+    const uint32_t q = lane % LPR, r0 = lane / LPR;
+    const int32_t n = n_base + (int32_t)(8u * q);
+    const int32_t left = M - m_base - (int32_t)r0;
+    if (n >= N || left <= 0) return;
+    const int rows = left >= RP ? RP / RPI : (left + RPI - 1) / RPI;
+    const LossTerms l = loss_terms();
+    __bf16 *dz = (__bf16 *)l.dz + (int64_t)(m_base + (int32_t)r0) * l.lddz + n;
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+      const uint32_t row = (uint32_t)(i * RPI) + r0;
+      const f32x4 lo = *(const f32x4 *)(wl + row * ROW_B + (((2u * q) ^ (row & 15u)) << 4));
+      const f32x4 hi = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + 1u) ^ (row & 15u)) << 4));
+      const f32x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      if (slot) store8(slot + row * STRIDE + 8u * q, v);
+      else if (FORM == kFormLogitGrad) store8(dz + (int64_t)(i * RPI) * l.lddz, v);
+    }
+  }
+};
+
+template <int EDGE, int FORM, int MODE>
+__global__ __launch_bounds__(256, 1) void ptg_loss_kernel(const LossKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, LossOp<FORM>>(a.gemm, a.op);
+}
+
+// The tiles that were split along k: their chunks' sums, added in chunk order, then what
+// a whole tile's wave does with them. A row's lanes follow each other, so a block's
+// EDGE / 2 columns lie in EDGE / 16 of them.
+struct LossChunksArgs {
+  LossTerms loss;
+  const float *ws;
+  int32_t m, n, tiles_m, tiles_n, raster_group, first, chunks;
+};
+template <int EDGE, int FORM>
+__global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksArgs a) {
+  constexpr int LPR = EDGE / 8, kRows = 256 / LPR, kParts = EDGE / kRows, kLanes = LPR / 2;
+  const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
+  int32_t m_t, n_t;
+  decode_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
+  const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
+  const bool in = m < a.m && n < a.n;  // (n is a multiple of 8 everywhere)
+  f32x8 z = {};
+  if (in) z = chunk_sum<EDGE, false>(a.ws, tile, r, q, a.chunks);
+  if constexpr (FORM == kFormLogitGrad) {
+    if (!in) return;
+    const RowGrad g = row_grad(a.loss, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = times_factor(g.factor, probability(z[e], g) - (g.at == n + e ? 1.0f : 0.0f));
+    store8((__bf16 *)a.loss.dz + (int64_t)m * a.loss.lddz + n, z);
+  } else {
+    float top = -INFINITY, sum = 0.0f;
+    if (in) {
+      const int64_t at = a.loss.label[m] - a.loss.first - n;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        top = fmaxf(top, z[e]);
+        if (at == e && a.loss.label[m] >= 0) a.loss.picked[m] = z[e];
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    const float offset = offset_of(top);
+    if (in) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(fmaf(z[e], kLog2E, -offset));
+    }
+    sum = put_right(sum, top, offset);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor(sum, o, 64);
+    if (in && q % kLanes == 0) a.loss.partial[(size_t)(n / loss_block(EDGE)) * (size_t)a.m + m] = make_float2(top, sum);
+  }
+}
+
+// The blocks of a row joined: R rows a workgroup (a power of two), 256 / R slices of the
+// blocks a row, added in a fixed order.
+struct LossJoinArgs {
+  const float2 *partial;
+  const int64_t *label;
+  float *lse, *loss;
+  int64_t entries;
+  int32_t blocks, m;
+};
+template <int R>
+__global__ __launch_bounds__(256) void ptg_loss_join_kernel(const LossJoinArgs a) {
+  constexpr int S = 256 / R;
+  __shared__ float2 lds[S][R];
+  const int32_t r = (int32_t)threadIdx.x % R, slice = (int32_t)threadIdx.x / R;
+  const int32_t m = (int32_t)blockIdx.x * R + r;
+  float top = -INFINITY, sum = 0.0f;
+  auto add = [&](float2 p) {
+    const float t = fmaxf(top, p.x);
+    // (equal maxima are not subtracted: both may be -infinity)
+    sum = (top == t ? sum : sum * __builtin_amdgcn_exp2f((top - t) * kLog2E)) + (p.x == t ? p.y : p.y * __builtin_amdgcn_exp2f((p.x - t) * kLog2E));
+    top = t;
+  };
+  if (m < a.m)
+    for (int32_t b = slice; b < a.blocks; b += S) add(a.partial[(size_t)b * (size_t)a.m + m]);
+  lds[slice][r] = make_float2(top, sum);
+  __syncthreads();
+  if (slice != 0 || m >= a.m) return;
+  for (int i = 1; i < S; ++i) add(lds[i][r]);
+  const float lse = top + logf(sum);
+  const int64_t label = a.label[m];
+  const float picked = a.lse[m];
+  a.lse[m] = lse;
+  if (a.loss) a.loss[m] = label < 0 ? 0.0f : label >= a.entries ? __uint_as_float(0x7fc00000u) : lse - picked;
+}
+
+hipError_t launch_loss_join(const float2 *partial, int32_t blocks, const int64_t *label, int64_t entries, float *lse, float *loss, int32_t m,
+                            hipStream_t s) {
+  const LossJoinArgs a = {partial, label, lse, loss, entries, blocks, m};
+  if (m > 512) hipLaunchKernelGGL(ptg_loss_join_kernel<32>, dim3((uint32_t)(m + 31) / 32u), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(ptg_loss_join_kernel<4>, dim3((uint32_t)(m + 3) / 4u), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int EDGE>
+static hipError_t reduce_edge(int form, const LossChunksArgs &a, int tiles, hipStream_t s) {
+  const dim3 grid(reduce_grid<EDGE>(tiles));
+  if (form == kFormLoss) hipLaunchKernelGGL((ptg_loss_chunks_kernel<EDGE, kFormLoss>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((ptg_loss_chunks_kernel<EDGE, kFormLogitGrad>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+                              int32_t first, int32_t tiles, int32_t chunks, hipStream_t s) {
+  const LossChunksArgs a = {loss, ws, m, n, (m + tile_edge - 1) / tile_edge, (n + tile_edge - 1) / tile_edge, raster_group, first, chunks};
+  return tile_edge == 256 ? reduce_edge<256>(form, a, tiles, s) : reduce_edge<128>(form, a, tiles, s);
+}
+
+template <int EDGE, int FORM>
+static hipError_t launch_form(int mode, const LossKernelArgs &a, int grid, hipStream_t s) {
+  const dim3 g((uint32_t)grid), b(256);
+  if (mode == kDynamic) hipLaunchKernelGGL((ptg_loss_kernel<EDGE, FORM, kDynamic>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((ptg_loss_kernel<EDGE, FORM, kNonPersistent>), g, b, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
+                               int grid, hipStream_t s) {
+  const LossKernelArgs a = {args, op, loss};
+  if (tile_edge == 256)
+    return form == kFormLoss ? launch_form<256, kFormLoss>(mode, a, grid, s) : launch_form<256, kFormLogitGrad>(mode, a, grid, s);
+  return form == kFormLoss ? launch_form<128, kFormLoss>(mode, a, grid, s) : launch_form<128, kFormLogitGrad>(mode, a, grid, s);
+}
+
+}  // namespace ptg

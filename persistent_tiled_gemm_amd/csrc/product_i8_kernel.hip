@@ -1,0 +1,40 @@
+// The int8 product as tiles: the bf16 one's main loop, byte for byte, with the
+// 16 x 16 x 64 int8 MFMA, which multiplies twice as many values in the same time and
+// adds them in 32-bit integers: sums are exact (k is limited so that they fit) and are
+// rounded once, on their way into the epilogue.
+#include "product_op.hpp"
+
+namespace ptg {
+
+template <int EDGE, int MODE>
+__global__ __launch_bounds__(256, product_workgroups(EDGE, kFormNTI8)) void ptg_product_i8_kernel(const ProductKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, ProductOp<kFormNTI8>>(a.gemm, a.op);
+}
+
+template <int EDGE>
+__global__ __launch_bounds__(256) void ptg_product_i8_reduce_kernel(const ReduceArgs a) {
+  reduce_tiles<EDGE, kScalesRowCol, true>(a);
+}
+
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
+                            int32_t chunks, hipStream_t s) {
+  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks};
+  if (tile_edge == 256) hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<256>, dim3(reduce_grid<256>(tiles)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<128>, dim3(reduce_grid<128>(tiles)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int EDGE>
+static hipError_t launch_edge(int mode, const ProductKernelArgs &a, int grid, hipStream_t s) {
+  const dim3 g((uint32_t)grid), b(256);
+  if (mode == kDynamic) hipLaunchKernelGGL((ptg_product_i8_kernel<EDGE, kDynamic>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((ptg_product_i8_kernel<EDGE, kNonPersistent>), g, b, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_product_i8(int tile_edge, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+  const ProductKernelArgs a = {args, op};
+  return tile_edge == 256 ? launch_edge<256>(mode, a, grid, s) : launch_edge<128>(mode, a, grid, s);
+}
+
+}  // namespace ptg

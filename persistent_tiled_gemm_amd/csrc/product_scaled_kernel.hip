@@ -1,0 +1,41 @@
+// The products of a linear layer's gradient (NN, TN) with one factor for all sums,
+// read from the device when a tile is finished: the incoming gradient of a loss, which
+// then stays out of the operands' rounding.
+#include "product_op.hpp"
+
+namespace ptg {
+
+template <int EDGE, int FORM, int MODE>
+__global__ __launch_bounds__(256, product_workgroups(EDGE, FORM)) void ptg_product_scaled_kernel(const ProductKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, ProductOp<FORM>>(a.gemm, a.op);
+}
+
+template <int EDGE>
+__global__ __launch_bounds__(256) void ptg_product_scaled_reduce_kernel(const ReduceArgs a) {
+  reduce_tiles<EDGE, kScalesOne, false>(a);
+}
+
+hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
+                                int32_t chunks, hipStream_t s) {
+  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks};
+  if (tile_edge == 256) hipLaunchKernelGGL(ptg_product_scaled_reduce_kernel<256>, dim3(reduce_grid<256>(tiles)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(ptg_product_scaled_reduce_kernel<128>, dim3(reduce_grid<128>(tiles)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int EDGE, int FORM>
+static hipError_t launch_form(int mode, const ProductKernelArgs &a, int grid, hipStream_t s) {
+  const dim3 g((uint32_t)grid), b(256);
+  if (mode == kDynamic) hipLaunchKernelGGL((ptg_product_scaled_kernel<EDGE, FORM, kDynamic>), g, b, 0, s, a);
+  else hipLaunchKernelGGL((ptg_product_scaled_kernel<EDGE, FORM, kNonPersistent>), g, b, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_product_scaled(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+  const ProductKernelArgs a = {args, op};
+  if (tile_edge == 256)
+    return form == kFormNNScaled ? launch_form<256, kFormNNScaled>(mode, a, grid, s) : launch_form<256, kFormTNScaled>(mode, a, grid, s);
+  return form == kFormNNScaled ? launch_form<128, kFormNNScaled>(mode, a, grid, s) : launch_form<128, kFormTNScaled>(mode, a, grid, s);
+}
+
+}  // namespace ptg

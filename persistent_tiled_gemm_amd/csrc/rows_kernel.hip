@@ -1,6 +1,10 @@
 // The product of the layer operators for few rows (a decode step): out = act(x .
 // w^T scales + bias) + residual with m up to 64.
 //
+// And the same with int8 operands (v_mfma_i32_16x16x64_i8, sums in 32-bit integers,
+// exact), and with a cross entropy's end: each row's maximum and sum of exponentials
+// over the workgroup's rows of w in place of the logits (see loss_kernel.hip).
+//
 // Every weight is used for at most 64 rows, so the kernel is bound by reading w
 // once; everything is laid out for bytes in flight. A workgroup owns 16 NBLK rows
 // of w and, of k, the share S-th of the grid gives it; its waves split that share
@@ -16,6 +20,7 @@
 #include <algorithm>
 
 #include "layer_device.hpp"
+#include "loss_device.hpp"
 
 namespace ptg {
 
@@ -33,11 +38,19 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
 
 static constexpr int kPolicyStream = 2;  // nt: w is read once
 
-template <bool E8, int MT, int NBLK, int WAVES, int U>
-__global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) {
+// Sums as they meet in LDS and memory: fp32, or the bits of integers.
+template <bool I8>
+__device__ __forceinline__ f32x4 add4(const f32x4 &a, const f32x4 &b) {
+  if constexpr (I8) return __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, a) + __builtin_bit_cast(i32x4, b));
+  else return a + b;
+}
+
+template <int TYPE, bool LOSS, int MT, int NBLK, int WAVES, int U>
+__device__ __forceinline__ void rows_body(const RowsArgs &a, const LossTerms &loss) {
+  constexpr bool E8 = TYPE == kTypeE4m3, I8 = TYPE == kTypeI8;
   constexpr int kItems = MT * NBLK;  // 16 x 16 blocks of the workgroup's tile
-  constexpr int kStep = E8 ? 64 : 32;
-  constexpr uint32_t kSize = E8 ? 1u : 2u;
+  constexpr int kStep = E8 || I8 ? 64 : 32;
+  constexpr uint32_t kSize = E8 || I8 ? 1u : 2u;
   __shared__ f32x4 sums[WAVES][kItems][64];
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_uniform(tid >> 6);
@@ -71,7 +84,8 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 #pragma unroll
   for (int t = 0; t < MT; ++t) x_row[t] = 16 * t + row < a.m ? (uint32_t)(16 * t + row) * (uint32_t)a.ldx * kSize : kBufOob;
 
-  f32x4 acc[MT][NBLK] = {};
+  typedef typename std::conditional<I8, i32x4, f32x4>::type acc4;
+  acc4 acc[MT][NBLK] = {};
   struct Batch { i32x4 w[U][NBLK], x[U][MT]; };
   auto load = [&](Batch &f, int32_t s) {
 #pragma unroll
@@ -91,6 +105,13 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
   auto multiply = [&](const Batch &f) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if constexpr (I8) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int b = 0; b < NBLK; ++b) acc[t][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[u][b], f.x[u][t], acc[t][b], 0, 0, 0);
+        continue;
+      }
 #pragma unroll
       for (int h = 0; h < (E8 ? 2 : 1); ++h) {
         bf16x8 wf[NBLK], xf[MT];
@@ -103,7 +124,8 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int b = 0; b < NBLK; ++b) acc[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b], xf[t], acc[t][b], 0, 0, 0);
+          for (int b = 0; b < NBLK; ++b)
+            if constexpr (!I8) acc[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[b], xf[t], acc[t][b], 0, 0, 0);
       }
     }
   };
@@ -123,14 +145,14 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int b = 0; b < NBLK; ++b) sums[wave][t * NBLK + b][lane] = acc[t][b];
+    for (int b = 0; b < NBLK; ++b) sums[wave][t * NBLK + b][lane] = __builtin_bit_cast(f32x4, acc[t][b]);
   __syncthreads();
   const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.partial);
   const uint32_t slots = (uint32_t)(kItems * 64);
   for (uint32_t i = tid; i < slots; i += 64 * WAVES) {
     f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) z += sums[w][i >> 6][i & 63u];
+    for (int w = 0; w < WAVES; ++w) z = add4<I8>(z, sums[w][i >> 6][i & 63u]);
     if (gridDim.y > 1) store16_agent(pr, ((tile * gridDim.y + part) * slots + i) * 16u, z);
     else sums[0][i >> 6][i & 63u] = z;
   }
@@ -147,6 +169,50 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
     __syncthreads();
     if (wave_uniform(last) == 0) return;
   }
+  // slot i of the tile, all its parts added
+  auto whole = [&](uint32_t i) -> f32x4 {
+    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (gridDim.y > 1) {
+      for (uint32_t p = 0; p < gridDim.y; ++p) z = add4<I8>(z, load16_agent(pr, ((tile * gridDim.y + p) * slots + i) * 16u));
+    } else {
+      z = sums[0][i >> 6][i & 63u];
+    }
+    return z;
+  };
+  if constexpr (LOSS) {
+    if (gridDim.y == 1) __syncthreads();  // a wave reads what others have added
+    // sixteen rows a wave: a lane holds a quarter of a row's columns in each block
+    for (uint32_t t = wave; t < (uint32_t)MT; t += WAVES) {
+      const int32_t m = (int32_t)(16u * t + (lane & 15u)), first = n0 + (int32_t)(4u * (lane >> 4));
+      f32x4 z[NBLK];
+      float top = -INFINITY;
+      const int64_t label = m < a.m ? loss.label[m] : -1;
+#pragma unroll
+      for (int b = 0; b < NBLK; ++b) {
+        z[b] = whole((t * NBLK + (uint32_t)b) * 64u + lane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int32_t n = first + 16 * b + q;
+          if (m < a.m && n < a.n && label == n) loss.picked[m] = z[b][q];
+          z[b][q] = n < a.n ? z[b][q] : -INFINITY;
+          top = fmaxf(top, z[b][q]);
+        }
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float offset = offset_of(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NBLK; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += __builtin_amdgcn_exp2f(fmaf(z[b][q], kLog2E, -offset));
+      sum = put_right(sum, top, offset);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (lane < 16u && m < a.m) loss.partial[(size_t)tile * (size_t)a.m + m] = make_float2(top, sum);
+    }
+    return;
+  }
   // ---- epilogue: four columns of one row at a time
   const EpilogueArgs &e = a.ep;
   for (uint32_t i = tid; i < slots; i += 64 * WAVES) {
@@ -154,13 +220,9 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
     const int64_t m = (int64_t)(16u * (item / NBLK) + (l & 15u));
     const int32_t n = n0 + (int32_t)(16u * (item % NBLK) + 4u * (l >> 4));
     if (m >= a.m || n >= a.n) continue;
-    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (gridDim.y > 1) {
-      for (uint32_t p = 0; p < gridDim.y; ++p) z += load16_agent(pr, ((tile * gridDim.y + p) * slots + i) * 16u);
-    } else {
-      z = sums[0][item][l];
-    }
-    if constexpr (E8) {
+    f32x4 z = whole(i);
+    if constexpr (I8) z = __builtin_convertvector(__builtin_bit_cast(i32x4, z), f32x4);
+    if constexpr (E8 || I8) {
       if (e.row_scale) z *= e.row_scale[m];
       if (e.col_scale) z *= *(const f32x4 *)(e.col_scale + n);
     }
@@ -172,6 +234,19 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
     if (e.out_type == kTypeF32) *(f32x4 *)((float *)e.out + m * e.ldo + n) = z;
     else store4((__bf16 *)e.out + m * e.ldo + n, z);
   }
+}
+
+template <bool E8, int MT, int NBLK, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) {
+  rows_body<E8 ? kTypeE4m3 : kTypeBf16, false, MT, NBLK, WAVES, U>(a, LossTerms{});
+}
+template <int MT, int NBLK, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_i8_kernel(const RowsArgs a) {
+  rows_body<kTypeI8, false, MT, NBLK, WAVES, U>(a, LossTerms{});
+}
+template <int MT, int NBLK, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_loss_kernel(const RowsArgs a, const LossTerms loss) {
+  rows_body<kTypeBf16, true, MT, NBLK, WAVES, U>(a, loss);
 }
 
 // The shape of a call: 16-row blocks of x and w a workgroup takes, its waves, and
@@ -191,7 +266,8 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_kernel(const RowsArgs a) 
 //   - k is shared until there are as many workgroups as CUs, while a wave keeps
 //     four steps (1024 x 8192, one row: 12.6 us unshared, 9.1 with four).
 struct RowsShape { int mt, nblk, waves, split; };
-static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, bool e8, int cu_count) {
+static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, int type, int cu_count) {
+  const bool e8 = type != kTypeBf16;
   RowsShape f;
   const bool large = (int64_t)n * k >= (int64_t)32 << 20;
   f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
@@ -209,7 +285,8 @@ static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, bool e8, int cu_cou
 // 38; 64 rows 51 and 40; 4096^2: 64 rows 20 and 22), from 33 in e4m3 (8192^2: 32
 // rows 24 and 29, 64 rows 31 and 31), and from 5 where bf16 rows do not start on
 // 64-byte lines (5000^2: one row 21.8 and 23.0, 8 rows 25.5 and 23.8, 64 44 and 29).
-bool rows_preferred(const ProductArgs &p, bool e8) {
+bool rows_preferred(const ProductArgs &p, int type) {
+  const bool e8 = type != kTypeBf16;
   if (p.m > kRowsMost) return false;
   const int64_t size = (int64_t)p.n * p.k;
   if (e8) return p.m <= 32 || size < (int64_t)32 << 20;
@@ -217,8 +294,8 @@ bool rows_preferred(const ProductArgs &p, bool e8) {
   return p.m <= 16 || size < (int64_t)32 << 20;
 }
 
-int64_t rows_partial_floats(const ProductArgs &p, bool e8, int cu_count, int64_t *tiles) {
-  const RowsShape f = rows_shape(p.m, p.n, p.k, e8, cu_count);
+int64_t rows_partial_floats(const ProductArgs &p, int type, int cu_count, int64_t *tiles) {
+  const RowsShape f = rows_shape(p.m, p.n, p.k, type, cu_count);
   *tiles = f.split > 1 ? (p.n + 16 * f.nblk - 1) / (16 * f.nblk) : 0;
   return *tiles * f.split * f.mt * f.nblk * 256;
 }
@@ -241,8 +318,19 @@ static hipError_t rows_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, 
   return hipGetLastError();
 }
 
-hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
-  const RowsShape f = rows_shape(p.m, p.n, p.k, e8, cu_count);
+static hipError_t rows_i8_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * f.waves);
+  if (f.mt == 2 && f.nblk == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 4, 4, 2>), grid, block, 0, s, a);
+  else if (f.mt == 1 && f.nblk == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1 && f.nblk == 1) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 8, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 2, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 2 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 2, 4, 2>), grid, block, 0, s, a);
+  else if (f.mt == 4 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<4, 2, 4, 2>), grid, block, 0, s, a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+static RowsArgs rows_args(const ProductArgs &p, float *partial, uint32_t *arrivals) {
   RowsArgs a;
   a.x = p.a;
   a.w = p.b;
@@ -254,8 +342,30 @@ hipError_t launch_rows(const ProductArgs &p, bool e8, float *partial, uint32_t *
   a.partial = partial;
   a.arrivals = arrivals;
   a.ep = p.ep;
-  const dim3 grid((uint32_t)((p.n + 16 * f.nblk - 1) / (16 * f.nblk)), (uint32_t)f.split);
-  return e8 ? rows_blocks<true>(f, a, grid, s) : rows_blocks<false>(f, a, grid, s);
+  return a;
+}
+static dim3 rows_grid(const RowsShape &f, int32_t n) { return dim3((uint32_t)((n + 16 * f.nblk - 1) / (16 * f.nblk)), (uint32_t)f.split); }
+
+hipError_t launch_rows(const ProductArgs &p, int type, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
+  const RowsShape f = rows_shape(p.m, p.n, p.k, type, cu_count);
+  const RowsArgs a = rows_args(p, partial, arrivals);
+  if (type == kTypeI8) return rows_i8_blocks(f, a, rows_grid(f, p.n), s);
+  return type == kTypeE4m3 ? rows_blocks<true>(f, a, rows_grid(f, p.n), s) : rows_blocks<false>(f, a, rows_grid(f, p.n), s);
+}
+
+int32_t rows_loss_block(const ProductArgs &p, int cu_count) { return 16 * rows_shape(p.m, p.n, p.k, kTypeBf16, cu_count).nblk; }
+
+hipError_t launch_rows_loss(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
+  const RowsShape f = rows_shape(p.m, p.n, p.k, kTypeBf16, cu_count);
+  const RowsArgs a = rows_args(p, partial, arrivals);
+  const dim3 grid = rows_grid(f, p.n), block(64 * f.waves);
+  if (f.mt == 1 && f.nblk == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_loss_kernel<1, 1, 4, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 1 && f.nblk == 1) hipLaunchKernelGGL((ptg_rows_loss_kernel<1, 1, 8, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_loss_kernel<1, 2, 4, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 2 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_loss_kernel<2, 2, 4, 2>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 4 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_loss_kernel<4, 2, 4, 2>), grid, block, 0, s, a, p.loss);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
 }
 
 }  // namespace ptg

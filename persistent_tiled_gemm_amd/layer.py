@@ -1,9 +1,11 @@
 """Python binding of the layer operators' C ABI (include/ptg_layer.h): the RMS norm with the residual's
-addition, the product with bias, activation and residual in its epilogue, and their gradients.
+addition, the product with bias, activation and residual in its epilogue, and their gradients; rows quantised to
+8 bits; the cross entropy of an output head and its gradient, without the logits.
 
 Argument marshalling only, like the GEMM's binding. The function names are the C ABI's: layer_create,
 layer_destroy, layer_sync, layer_last_hip_error, layer_rmsnorm, layer_rmsnorm_backward, layer_linear,
-layer_activation_backward, layer_linear_backward. Matrices are 2-D device tensors whose rows are dense; the row
+layer_activation_backward, layer_linear_backward, layer_quantize, layer_cross_entropy,
+layer_cross_entropy_scratch, layer_cross_entropy_backward. Matrices are 2-D device tensors whose rows are dense; the row
 stride is free (a column slice of a wider buffer works). Streams are torch.cuda streams (default: the current
 stream). Outputs are given by the caller.
 """
@@ -15,12 +17,13 @@ import struct
 
 from . import GEMM_OK, PtgError, _stream_ptr, load_library
 
-LAYER_F32, LAYER_BF16, LAYER_E4M3 = 0, 1, 2
+LAYER_F32, LAYER_BF16, LAYER_E4M3, LAYER_I8 = 0, 1, 2, 3
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # exported names, in the order of the header
 LAYER_ABI_FUNCTIONS = ("layer_create", "layer_destroy", "layer_sync", "layer_last_hip_error", "layer_rmsnorm",
-                       "layer_rmsnorm_backward", "layer_linear", "layer_activation_backward", "layer_linear_backward")
+                       "layer_rmsnorm_backward", "layer_linear", "layer_activation_backward", "layer_linear_backward",
+                       "layer_quantize", "layer_cross_entropy", "layer_cross_entropy_scratch", "layer_cross_entropy_backward")
 
 
 def _struct(pointers, sizes, ints, floats=()):
@@ -53,6 +56,19 @@ class LinearGradArgs(ctypes.Structure):
                        ("dx_type", "dw_type", "accumulate", "pad"))
 
 
+class QuantizeArgs(ctypes.Structure):
+    _fields_ = _struct(("x", "out", "scale"), ("m", "n", "ldx", "ldo"), ("type", "out_type"))
+
+
+class CrossEntropyArgs(ctypes.Structure):
+    _fields_ = _struct(("x", "w", "label", "lse", "loss"), ("m", "n", "k", "ldx", "ldw"), ())
+
+
+class CrossEntropyGradArgs(ctypes.Structure):
+    _fields_ = _struct(("x", "w", "label", "lse", "weight", "dloss", "dx", "dw", "scratch"),
+                       ("scratch_bytes", "m", "n", "k", "ldx", "ldw", "lddx", "lddw"), ("dx_type", "dw_type", "accumulate", "pad"))
+
+
 def _packer(cls):
     """The structure's values as bytes in one call (setting ctypes fields one by one costs microseconds a call, which is
     what a decode step's small operators take on the device)."""
@@ -62,8 +78,9 @@ def _packer(cls):
     return p.pack
 
 
-_RMSNORM, _RMSNORM_GRAD, _LINEAR, _ACTIVATION_GRAD, _LINEAR_GRAD = (
-    _packer(c) for c in (RmsnormArgs, RmsnormGradArgs, LinearArgs, ActivationGradArgs, LinearGradArgs))
+_RMSNORM, _RMSNORM_GRAD, _LINEAR, _ACTIVATION_GRAD, _LINEAR_GRAD, _QUANTIZE, _CROSS_ENTROPY, _CROSS_ENTROPY_GRAD = (
+    _packer(c) for c in (RmsnormArgs, RmsnormGradArgs, LinearArgs, ActivationGradArgs, LinearGradArgs, QuantizeArgs, CrossEntropyArgs,
+                         CrossEntropyGradArgs))
 
 _lib = None
 
@@ -83,6 +100,11 @@ def _library():
         lib.layer_linear.argtypes = [vp, vp, vp]
         lib.layer_activation_backward.argtypes = [vp, vp, vp]
         lib.layer_linear_backward.argtypes = [vp, vp, vp]
+        lib.layer_quantize.argtypes = [vp, vp]
+        lib.layer_cross_entropy.argtypes = [vp, vp, vp]
+        lib.layer_cross_entropy_scratch.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int32]
+        lib.layer_cross_entropy_scratch.restype = ctypes.c_int64
+        lib.layer_cross_entropy_backward.argtypes = [vp, vp, vp]
         _lib = lib
     return _lib
 
@@ -150,7 +172,8 @@ _current_device = None
 def _prepare():
     global _raw_stream, _current_device
     import torch
-    _codes.update({torch.float32: LAYER_F32, torch.bfloat16: LAYER_BF16, torch.float8_e4m3fn: LAYER_E4M3})
+    _codes.update({torch.float32: LAYER_F32, torch.bfloat16: LAYER_BF16, torch.float8_e4m3fn: LAYER_E4M3,
+                   torch.int8: LAYER_I8})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -220,7 +243,7 @@ def _activation(name) -> int:
 
 _STREAM = (LAYER_F32, LAYER_BF16)
 _ANY = (LAYER_F32, LAYER_BF16, LAYER_E4M3)
-_ONLY = {c: (c,) for c in _ANY}  # the types allowed beside one that is given
+_ONLY = {c: (c,) for c in (*_ANY, LAYER_I8)}  # the types allowed beside one that is given
 
 
 def layer_rmsnorm(x, weight, out, *, residual=None, sum_out=None, scale=None, eps: float = 1e-6, stream=None) -> None:
@@ -261,8 +284,8 @@ def layer_rmsnorm_backward(dy, s, weight, dx, dweight, plan: LayerPlan, *, dsum=
 
 def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "none", residual=None, pre=None, x_scale=None,
                  w_scale=None, stream=None) -> None:
-    """layer_linear: out = act(x . w^T + bias) + residual, x: m x k, w: n x k, both bf16 or both float8_e4m3fn (then
-    with row scales x_scale and w_scale, fp32). out and residual: bf16 or fp32; residual may be out. pre (bf16)
+    """layer_linear: out = act(x . w^T + bias) + residual, x: m x k, w: n x k, both bf16, both float8_e4m3fn or both int8 (the
+    8-bit types with row scales x_scale and w_scale, fp32). out and residual: bf16 or fp32; residual may be out. pre (bf16)
     keeps the activation's argument for layer_activation_backward."""
     act = _activation(activation)
     x_shape, at = _first("x", x, plan.device)
@@ -272,7 +295,7 @@ def layer_linear(x, w, out, plan: LayerPlan, *, bias=None, activation: str = "no
     if k2 != k:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
     shape = (m, n)
-    px, ldx, ty = _matrix("x", x, x_shape, at, (LAYER_BF16, LAYER_E4M3))
+    px, ldx, ty = _matrix("x", x, x_shape, at, (LAYER_BF16, LAYER_E4M3, LAYER_I8))
     pw, ldw, _ = _matrix("w", w, w_shape, at, _ONLY[ty])
     pxs, _ = _vector("x_scale", x_scale, m, at, _ONLY[LAYER_F32])
     pws, _ = _vector("w_scale", w_scale, n, at, _ONLY[LAYER_F32])
@@ -321,3 +344,82 @@ def layer_linear_backward(dpre, x, w, plan: LayerPlan, *, dx=None, dw=None, accu
     st = (_lib or _library()).layer_linear_backward(a, plan.handle, _stream_of(stream, at))
     if st:
         _check(st, "layer_linear_backward", plan)
+
+
+def layer_quantize(x, out, scale, *, stream=None) -> None:
+    """layer_quantize: out = x / scale by rows, scale = max |x| / 127 (out int8) or / 448 (out float8_e4m3fn); x: bf16 or fp32.
+    x is then about out * scale[:, None]: an operand of layer_linear with its row scales."""
+    shape, at = _first("x", x)
+    m, n = shape
+    px, ldx, ty = _matrix("x", x, shape, at, _STREAM)
+    po, ldo, ot = _matrix("out", out, shape, at, (LAYER_I8, LAYER_E4M3))
+    pc, _ = _vector("scale", scale, m, at, _ONLY[LAYER_F32])
+    st = (_lib or _library()).layer_quantize(_QUANTIZE(px, po, pc, m, n, ldx, ldo, ty, ot), _stream_of(stream, at))
+    if st:
+        _check(st, "layer_quantize")
+
+
+def _labels(label, m, at):
+    """The pointer of a dense int64 vector of m labels."""
+    import torch
+    if label.dtype is not torch.int64 or label.shape != (m,) or label.get_device() != at or not label.is_contiguous():
+        raise ValueError(f"label must be {m} contiguous int64 values on device {at}, got {label.dtype} {tuple(label.shape)} on {label.device}")
+    return label.data_ptr()
+
+
+def _head(x, w, plan):
+    """(m, n, k, device, pointers and row strides of x and w) of an output head."""
+    x_shape, at = _first("x", x, plan.device)
+    w_shape, _ = _first("w", w, plan.device)
+    m, k = x_shape
+    n, k2 = w_shape
+    if k2 != k:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w {tuple(w.shape)}")
+    px, ldx, _ = _matrix("x", x, x_shape, at, _ONLY[LAYER_BF16])
+    pw, ldw, _ = _matrix("w", w, w_shape, at, _ONLY[LAYER_BF16])
+    return m, n, k, at, px, ldx, pw, ldw
+
+
+def layer_cross_entropy(x, w, label, lse, plan: LayerPlan, *, loss=None, stream=None) -> None:
+    """layer_cross_entropy: with the logits z = x . w^T, which are not kept, lse = logsumexp(z) by rows and loss = lse -
+    z[label] (fp32, one value a row; 0 where the label is negative). x: m x k, w: n x k, bf16; label: int64."""
+    m, n, k, at, px, ldx, pw, ldw = _head(x, w, plan)
+    pn = _labels(label, m, at)
+    pl, _ = _vector("lse", lse, m, at, _ONLY[LAYER_F32])
+    po, _ = _vector("loss", loss, m, at, _ONLY[LAYER_F32])
+    st = (_lib or _library()).layer_cross_entropy(_CROSS_ENTROPY(px, pw, pn, pl, po, m, n, k, ldx, ldw), plan.handle, _stream_of(stream, at))
+    if st:
+        _check(st, "layer_cross_entropy", plan)
+
+
+def layer_cross_entropy_scratch(m: int, n: int, k: int, pieces: int = 1) -> int:
+    """layer_cross_entropy_scratch: the bytes of scratch with which layer_cross_entropy_backward takes the vocabulary in at
+    most `pieces` pieces."""
+    size = int(_library().layer_cross_entropy_scratch(m, n, k, pieces))
+    if size < 0:
+        raise ValueError(f"layer_cross_entropy_scratch: sizes {m}, {n}, {k} in {pieces} pieces")
+    return size
+
+
+def layer_cross_entropy_backward(x, w, label, lse, scratch, plan: LayerPlan, *, dx=None, dw=None, weight=None, dloss=None,
+                                 accumulate: bool = False, stream=None) -> None:
+    """layer_cross_entropy_backward: the gradient of dloss * sum(weight * loss) at the forward pass's lse: dx (m x k) and dw
+    (n x k; added to dw with accumulate), each bf16 or fp32 and optional. weight: fp32, one value a row, or None (ones);
+    dloss: one fp32 value on the device, or None (1). scratch: a contiguous device tensor of any dtype; the vocabulary is
+    taken in pieces that fit its bytes (layer_cross_entropy_scratch)."""
+    if dx is None and dw is None:
+        raise ValueError("layer_cross_entropy_backward needs dx or dw")
+    m, n, k, at, px, ldx, pw, ldw = _head(x, w, plan)
+    pn = _labels(label, m, at)
+    pl, _ = _vector("lse", lse, m, at, _ONLY[LAYER_F32])
+    if lse is None or scratch is None or scratch.get_device() != at or not scratch.is_contiguous():
+        raise ValueError(f"lse and a contiguous scratch on device {at} are needed")
+    pq, _ = _vector("weight", weight, m, at, _ONLY[LAYER_F32])
+    pd, _ = _vector("dloss", dloss if dloss is None else dloss.reshape(-1), 1, at, _ONLY[LAYER_F32])
+    pdx, lddx, xt = _matrix("dx", dx, (m, k), at, _STREAM)
+    pdw, lddw, wt = _matrix("dw", dw, (n, k), at, _STREAM)
+    a = _CROSS_ENTROPY_GRAD(px, pw, pn, pl, pq, pd, pdx, pdw, scratch.data_ptr(), scratch.numel() * scratch.element_size(), m, n, k, ldx, ldw,
+                            lddx, lddw, xt, wt, 1 if accumulate else 0, 0)
+    st = (_lib or _library()).layer_cross_entropy_backward(a, plan.handle, _stream_of(stream, at))
+    if st:
+        _check(st, "layer_cross_entropy_backward", plan)
