@@ -261,8 +261,10 @@ __global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksAr
   }
 }
 
-// The blocks of a row joined: R rows a workgroup (a power of two), 256 / R slices of the
-// blocks a row, added in a fixed order.
+// The blocks of a row joined: R rows a workgroup, whose threads take a slice of the blocks
+// each, eight at a time with all their loads under way, and meet in a tree; the order is
+// fixed. Sixteen rows fill a 128-byte line. One block after the other, each waiting for
+// the one before, took 57 us for 4096 rows of 1024 blocks and 12.6 for 4 rows of 2048.
 struct LossJoinArgs {
   const float2 *partial;
   const int64_t *label;
@@ -270,25 +272,47 @@ struct LossJoinArgs {
   int64_t entries;
   int32_t blocks, m;
 };
+__device__ __forceinline__ float rescaled(float sum, float from, float to) {
+  // (equal maxima are not subtracted: both may be infinite)
+  return from == to ? sum : sum * __builtin_amdgcn_exp2f((from - to) * kLog2E);
+}
 template <int R>
-__global__ __launch_bounds__(256) void ptg_loss_join_kernel(const LossJoinArgs a) {
-  constexpr int S = 256 / R;
+__global__ __launch_bounds__(512) void ptg_loss_join_kernel(const LossJoinArgs a) {
+  constexpr int S = 512 / R, U = 8;
   __shared__ float2 lds[S][R];
   const int32_t r = (int32_t)threadIdx.x % R, slice = (int32_t)threadIdx.x / R;
   const int32_t m = (int32_t)blockIdx.x * R + r;
   float top = -INFINITY, sum = 0.0f;
-  auto add = [&](float2 p) {
-    const float t = fmaxf(top, p.x);
-    // (equal maxima are not subtracted: both may be -infinity)
-    sum = (top == t ? sum : sum * __builtin_amdgcn_exp2f((top - t) * kLog2E)) + (p.x == t ? p.y : p.y * __builtin_amdgcn_exp2f((p.x - t) * kLog2E));
-    top = t;
-  };
-  if (m < a.m)
-    for (int32_t b = slice; b < a.blocks; b += S) add(a.partial[(size_t)b * (size_t)a.m + m]);
+  if (m < a.m) {
+    for (int32_t b0 = slice; b0 < a.blocks; b0 += U * S) {
+      float2 p[U];
+      float t = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int32_t b = b0 + u * S;
+        p[u] = b < a.blocks ? a.partial[(size_t)b * (size_t)a.m + m] : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) t = fmaxf(t, p[u].x);
+      sum = rescaled(sum, top, t);
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum += rescaled(p[u].y, p[u].x, t);
+      top = t;
+    }
+  }
   lds[slice][r] = make_float2(top, sum);
-  __syncthreads();
+#pragma unroll
+  for (int half = S / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (slice < half) {
+      const float2 q = lds[slice + half][r];
+      const float t = fmaxf(top, q.x);
+      sum = rescaled(sum, top, t) + rescaled(q.y, q.x, t);
+      top = t;
+      lds[slice][r] = make_float2(top, sum);
+    }
+  }
   if (slice != 0 || m >= a.m) return;
-  for (int i = 1; i < S; ++i) add(lds[i][r]);
   const float lse = top + logf(sum);
   const int64_t label = a.label[m];
   const float picked = a.lse[m];
@@ -299,8 +323,9 @@ __global__ __launch_bounds__(256) void ptg_loss_join_kernel(const LossJoinArgs a
 hipError_t launch_loss_join(const float2 *partial, int32_t blocks, const int64_t *label, int64_t entries, float *lse, float *loss, int32_t m,
                             hipStream_t s) {
   const LossJoinArgs a = {partial, label, lse, loss, entries, blocks, m};
-  if (m > 512) hipLaunchKernelGGL(ptg_loss_join_kernel<32>, dim3((uint32_t)(m + 31) / 32u), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(ptg_loss_join_kernel<4>, dim3((uint32_t)(m + 3) / 4u), dim3(256), 0, s, a);
+  if (m > 64) hipLaunchKernelGGL(ptg_loss_join_kernel<16>, dim3((uint32_t)(m + 15) / 16u), dim3(512), 0, s, a);
+  else if (m > 1) hipLaunchKernelGGL(ptg_loss_join_kernel<2>, dim3((uint32_t)(m + 1) / 2u), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL(ptg_loss_join_kernel<1>, dim3(1), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
