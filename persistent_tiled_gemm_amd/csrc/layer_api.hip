@@ -141,12 +141,18 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // 62, in 8 chunks: 20; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
 // last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55 (chosen: the last eight in 13
 // chunks, whose fit is 40 and whose time 49).
+// int8 and the loss forms take the bf16 figures (a k-step of theirs is 128 int8: 0.26 to
+// 0.33, and 0.45 to 0.85 as more CUs work) with the fill, drain and writes of a CU's
+// further units, 5 and 12, counted: with half the k-steps of bf16 they decide (int8 4096 x
+// 4096 x 1024: 128 without them, 48.9 us; 256, 30.7). Over 36 products of them the choice was
+// within 3% of the best of all edges and splits in 30.
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN || form == ptg::kFormTNScaled;
   const bool nn = form == ptg::kFormNN || form == ptg::kFormNNScaled;
   const int64_t units = ptg::form_units(form), nk = ceil_div(a.k / units, 32), line = 32 * units;
   const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (!nn && a.ldb % line != 0));
   const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : nn ? 1.05 : 1.13) : 1.0;
+  const bool refill = form >= ptg::kFormNTI8;
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
     const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
@@ -161,7 +167,10 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
       return (double)steps * step;
     };
     const int64_t resident = cus * ptg::product_workgroups(edge, form);
-    auto fixed = [&](int64_t units) { return (edge == 256 ? 18.0 : 8.0) - (units <= resident ? 2.0 : 0.0); };
+    auto fixed = [&](int64_t units) {
+      const double again = refill ? (edge == 256 ? 12.0 : 5.0) * (double)(ceil_div(units, resident) - 1) : 0.0;
+      return (edge == 256 ? 18.0 : 8.0) - (units <= resident ? 2.0 : 0.0) + again;
+    };
     const double join = edge == 256 ? 0.06 : 0.02;
     const double whole = fixed(T) + run(T, nk);
     if (whole < best.us) best = {edge, 1, 0, whole};
