@@ -436,8 +436,13 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.residual_type = a->residual_type;
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
+  int64_t tiles = 0;
+  if (a->in_type == LAYER_I8 && ptg::rows_shared_preferred(k, p->cu_count) &&
+      ptg::rows_shared_floats(k, p->cu_count, &tiles) <= p->ws_floats && tiles <= kArrivals) {
+    hipError_t e = ptg::launch_rows_shared(k, p->ws, p->d_arrivals, p->cu_count, s);
+    return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
+  }
   if (ptg::rows_preferred(k, a->in_type)) {
-    int64_t tiles = 0;
     if (ptg::rows_partial_floats(k, a->in_type, p->cu_count, &tiles) > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
     hipError_t e = ptg::launch_rows(k, a->in_type, p->ws, p->d_arrivals, p->cu_count, s);
     return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");

@@ -263,6 +263,9 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_loss_kernel(const RowsArg
 //     here in e4m3 alone, and 32 at most (rows_preferred). Smaller w: one block up
 //     to 16 rows, two for more (4096^2, 32 rows: two 14.9, four 14.8; 2048^2: two
 //     9.0, one 8.7);
+//   - int8 has nothing to widen, and takes one block of w where w is small, however many
+//     rows (2048^2, 64 rows: two 9.7 us, one with eight waves 7.5; 1024 x 8192: 13.7, 10.9;
+//     larger w runs in rows_shared_kernel.hip from 8 or 32 rows on);
 //   - k is shared until there are as many workgroups as CUs, while a wave keeps
 //     four steps (1024 x 8192, one row: 12.6 us unshared, 9.1 with four).
 struct RowsShape { int mt, nblk, waves, split; };
@@ -271,9 +274,9 @@ static RowsShape rows_shape(int32_t m, int32_t n, int32_t k, int type, int cu_co
   RowsShape f;
   const bool large = (int64_t)n * k >= (int64_t)32 << 20;
   f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
-  f.nblk = m <= 16 ? (large && (e8 || m > 8) ? 2 : 1) : (large && e8 ? 4 : 2);
+  f.nblk = m <= 16 ? (large && (e8 || m > 8) ? 2 : 1) : type == kTypeI8 ? 1 : (large && e8 ? 4 : 2);
   const int64_t tiles = (n + 16 * f.nblk - 1) / (16 * f.nblk);
-  f.waves = f.nblk == 1 && tiles < 4 * cu_count ? 8 : 4;
+  f.waves = f.nblk == 1 && tiles < (type == kTypeI8 && m > 16 ? 1 : 4) * cu_count ? 8 : 4;
   const int64_t steps = (k + (e8 ? 63 : 31)) / (e8 ? 64 : 32);
   f.split = (int)std::max<int64_t>(1, std::min<int64_t>({cu_count / tiles, steps / (4 * f.waves), 16}));
   return f;
@@ -320,13 +323,13 @@ static hipError_t rows_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, 
 
 static hipError_t rows_i8_blocks(const RowsShape &f, const RowsArgs &a, dim3 grid, hipStream_t s) {
   const dim3 block(64 * f.waves);
-  if (f.mt == 2 && f.nblk == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 4, 4, 2>), grid, block, 0, s, a);
-  else if (f.mt == 1 && f.nblk == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 4, 4>), grid, block, 0, s, a);
-  else if (f.mt == 1 && f.nblk == 1) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 8, 4>), grid, block, 0, s, a);
-  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 2, 4, 4>), grid, block, 0, s, a);
-  else if (f.mt == 2 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 2, 4, 2>), grid, block, 0, s, a);
-  else if (f.mt == 4 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<4, 2, 4, 2>), grid, block, 0, s, a);
-  else return hipErrorInvalidValue;
+  if (f.mt == 1 && f.nblk == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 2, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_i8_kernel<1, 1, 8, 4>), grid, block, 0, s, a);
+  else if (f.mt == 2 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 1, 4, 2>), grid, block, 0, s, a);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_i8_kernel<2, 1, 8, 2>), grid, block, 0, s, a);
+  else if (f.waves == 4) hipLaunchKernelGGL((ptg_rows_i8_kernel<4, 1, 4, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((ptg_rows_i8_kernel<4, 1, 8, 2>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -1,0 +1,194 @@
+// The product for some rows (up to 64) with x in LDS, for int8 operands.
+//
+// rows_kernel.hip reads w and x alike from memory into MFMA operands. x comes from the
+// caches, but returns in turn with w, and so takes its share of the loads that a CU can
+// have under way: 8192^2 in int8 took 15.4 us for one row of x and 21 for 24, what w and
+// all the copies of x take at 5.8 TB/s. Here a workgroup owns 16 rows of w a wave and
+// one share of k (of S): it brings x's share to LDS once for all its waves, and each
+// wave then streams its own rows of w over the whole share, with nothing else in its
+// queue. (8192^2: 24 rows 22.0 -> 17.9 us, 64 rows 27.2 -> 20.9; 16384 x 4096: 31.7 -> 20.2.) No wave's sums meet another's; the shares of k meet in the plan's workspace, as
+// in rows_kernel.hip.
+//
+// LDS: 256-byte segments, segment by segment, x's rows one after the other in each; 16-byte
+// chunk c of row r sits in slot c ^ (r mod 16), so that 16 rows' reads of one chunk are
+// free of bank conflicts.
+#include <algorithm>
+
+#include "layer_device.hpp"
+
+namespace ptg {
+
+static constexpr int kSharedBytes = 128 * 1024;
+static constexpr int kPolicyStream = 2;  // nt: w is read once
+
+template <int MT, int WAVES, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const RowsArgs a) {
+  constexpr int kRows = 16 * MT;
+  __shared__ __attribute__((aligned(1024))) unsigned char xs[kSharedBytes];
+  __shared__ uint32_t last;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_uniform(tid >> 6);
+  const uint32_t tile = blockIdx.x, part = blockIdx.y;
+  const int32_t n0 = (int32_t)(tile * WAVES + wave) * 16;
+  const uint32_t row = lane & 15u, group = lane >> 4;
+
+  // the workgroup's share of k, in segments of 256 bytes (four steps of 64)
+  const uint32_t segs = ((uint32_t)a.k + 255u) / 256u;
+  const uint32_t g0 = segs * part / gridDim.y, count = segs * (part + 1u) / gridDim.y - g0;
+  // each wave starts part-way into the share and wraps around, so that the waves spread
+  // over the memory channels
+  const uint32_t rot = count > 1u ? (((tile * (uint32_t)WAVES + wave) * 2654435761u) >> 16) % count : 0u;
+
+  // ---- x to LDS: a load moves four rows' segment
+  {
+    const i32x4 xr = make_rsrc_words(a.x);
+    const uint32_t base = lds_addr(xs);
+    const uint32_t loads = count * (uint32_t)(kRows / 4);
+    for (uint32_t i = wave; i < loads; i += WAVES) {
+      const uint32_t seg = i / (uint32_t)(kRows / 4), r = (i % (uint32_t)(kRows / 4)) * 4u + group;
+      const uint32_t at = (g0 + seg) * 256u + (row ^ (r & 15u)) * 16u;
+      load16_to_lds(xr, base + i * 1024u, (int32_t)r < a.m && at < (uint32_t)a.k ? r * (uint32_t)a.ldx + at : kBufOob);
+    }
+  }
+
+  // ---- w: DEPTH segments of the wave's rows under way. Segments past the share are asked
+  // for out of range (zeros, no traffic), so that every turn of the loop is alike and waits for
+  // the oldest segment alone.
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)a.ldw);
+  const bool w_in = n0 + (int32_t)row < a.n;
+  const uint32_t w_row = row * (uint32_t)a.ldw;  // byte offset of the lane's row
+  i32x4 acc[MT] = {};
+  i32x4 w[DEPTH][4];
+  auto seg_of = [&](uint32_t g) -> uint32_t { return g + rot < count ? g + rot : g + rot - count; };
+  auto load = [&](int d, uint32_t g) {
+    const uint32_t first = (g0 + seg_of(g)) * 256u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t at = first + 64u * (uint32_t)u + 16u * group;
+      const bool in = w_in && g < count && at < (uint32_t)a.k;
+      w[d][u] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? (int)(w_row + at) : (int)kBufOob, 0, kPolicyStream);
+    }
+  };
+  const uint32_t off = row * 256u + ((group ^ row) << 4);  // of the lane's chunk in a segment, first step
+  auto multiply = [&](int d, uint32_t g) {
+    const unsigned char *seg = xs + seg_of(min(g, count - 1u)) * (uint32_t)(kRows * 256);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const i32x4 x = *(const i32x4 *)(seg + (off ^ (uint32_t)(64 * u)) + t * 16 * 256);
+        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d][u], x, acc[t], 0, 0, 0);
+      }
+  };
+  if (count > 0) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(d, (uint32_t)d);
+    // x has landed once no more loads are under way than those
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DEPTH * 4) : "memory");
+    wg_barrier();
+    for (uint32_t g = 0; g < count; g += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        multiply(d, g + (uint32_t)d);
+        load(d, g + (uint32_t)(d + DEPTH));
+      }
+    }
+  }
+
+  // ---- the shares of k meet: each part through to memory, a relaxed count, and the last
+  // workgroup of the tile adds the parts in order (integers: in any order the same)
+  const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.partial);
+  constexpr uint32_t kSlots = (uint32_t)(WAVES * MT * 64);
+  const uint32_t mine = wave * (uint32_t)(MT * 64) + lane;
+  if (gridDim.y > 1) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      store16_agent(pr, ((tile * gridDim.y + part) * kSlots + mine + (uint32_t)t * 64u) * 16u, __builtin_bit_cast(f32x4, acc[t]));
+    wait_vmem_all();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t before = __hip_atomic_fetch_add(&a.arrivals[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = before + 1u == gridDim.y ? 1u : 0u;
+      if (last) __hip_atomic_store(&a.arrivals[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (wave_uniform(last) == 0) return;
+    for (uint32_t p = 0; p < gridDim.y; ++p) {
+      if (p == part) continue;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] += __builtin_bit_cast(i32x4, load16_agent(pr, ((tile * gridDim.y + p) * kSlots + mine + (uint32_t)t * 64u) * 16u));
+    }
+  }
+  // ---- epilogue: four columns of one row at a time
+  const EpilogueArgs &e = a.ep;
+  const int32_t n = n0 + 4 * (int32_t)group;
+  if (n >= a.n) return;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t m = 16 * t + (int32_t)row;
+    if (m >= a.m) continue;
+    f32x4 z = __builtin_convertvector(acc[t], f32x4);
+    if (e.row_scale) z *= e.row_scale[m];
+    if (e.col_scale) z *= *(const f32x4 *)(e.col_scale + n);
+    if (e.bias) z += load4_as(e.bias, e.bias_type, n);
+    if (e.pre) store4((__bf16 *)e.pre + m * e.ldp + n, z);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[q] = act_f32(e.act, z[q]);
+    if (e.residual) z += load4_as(e.residual, e.residual_type, m * e.ldr + n);
+    if (e.out_type == kTypeF32) *(f32x4 *)((float *)e.out + m * e.ldo + n) = z;
+    else store4((__bf16 *)e.out + m * e.ldo + n, z);
+  }
+}
+
+// The shape of a call: 16-row blocks of x, the waves of a workgroup (16 rows of w each) and
+// the shares of k: as many as bring the workgroups to the CUs' number, and as x needs to
+// fit. Up to 32 rows four waves with four segments under way; more take eight with two,
+// so that fewer workgroups hold copies of x (8192^2, 64 rows: four 24.2 us, eight 20.9).
+struct SharedShape { int mt, waves; int64_t tiles, split; };
+static SharedShape shared_shape(int32_t m, int32_t n, int32_t k, int cu_count) {
+  SharedShape f;
+  f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+  f.waves = f.mt < 4 ? 4 : 8;
+  f.tiles = (n + 16 * f.waves - 1) / (16 * f.waves);
+  const int64_t segs = (k + 255) / 256, fits = kSharedBytes / (f.mt * 16 * 256);
+  f.split = std::max<int64_t>({1, std::min<int64_t>({cu_count / f.tiles, segs, 16}), (segs + fits - 1) / fits});
+  return f;
+}
+
+int64_t rows_shared_floats(const ProductArgs &p, int cu_count, int64_t *tiles) {
+  const SharedShape f = shared_shape(p.m, p.n, p.k, cu_count);
+  *tiles = f.split > 1 ? f.tiles : 0;
+  return *tiles * f.split * f.waves * f.mt * 256;
+}
+
+// Where w is large enough to be worth x's way through LDS: from 8 rows on with 32 Mi
+// elements of w (8192^2: 4 rows 16.5 us here and 16.1 there, 8 rows 16.4 and 16.6, 24 rows
+// 17.9 and 22.0), from 32 rows on with 16 Mi (4096^2: 24 rows 9.4 and 8.8, 48 rows 10.9 and
+// 11.4). Smaller w runs in the few-row kernel at every m (2048^2, 64 rows: 9.6 and 7.5).
+bool rows_shared_preferred(const ProductArgs &p, int cu_count) {
+  const int64_t size = (int64_t)p.n * p.k;
+  if (p.m > kRowsMost || size < (int64_t)16 << 20 || p.m < (size < (int64_t)32 << 20 ? 32 : 8)) return false;
+  return shared_shape(p.m, p.n, p.k, cu_count).split <= 16;
+}
+
+hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
+  const SharedShape f = shared_shape(p.m, p.n, p.k, cu_count);
+  RowsArgs a;
+  a.x = p.a;
+  a.w = p.b;
+  a.ldx = (int32_t)p.lda;
+  a.ldw = (int32_t)p.ldb;
+  a.m = p.m;
+  a.n = p.n;
+  a.k = p.k;
+  a.partial = partial;
+  a.arrivals = arrivals;
+  a.ep = p.ep;
+  const dim3 grid((uint32_t)f.tiles, (uint32_t)f.split), block(64 * f.waves);
+  if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<1, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<2, 4, 4>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<4, 8, 2>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace ptg

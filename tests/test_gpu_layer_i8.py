@@ -102,6 +102,20 @@ def test_large_tiles(plan, m, n, k):
     assert torch.equal(a, b), "the same call twice gave different bits"
 
 
+# w large enough that x goes through LDS: one share of k and several, shares that end inside a segment, a ragged last block of w
+@pytest.mark.parametrize("m,n,k", [(8, 8200, 4112), (16, 4104, 8208), (17, 16408, 2064), (24, 2056, 16400), (32, 65544, 528), (32, 4104, 4112),
+                                   (33, 8200, 2064), (48, 1032, 32784), (64, 2056, 16400), (64, 33032, 1040), (40, 16392, 1296)])
+def test_some_rows_of_a_large_weight(plan, m, n, k):
+    say("int8 some rows", m, n, k)
+    check(plan, m, n, k, act="silu", pad=48)
+    x, w = codes(1, m, k), codes(2, n, k)
+    a, b = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+    ptg.layer_linear(x, w, a, plan)
+    ptg.layer_linear(x, w, b, plan)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(a.cpu(), (x.cpu().float().double() @ w.cpu().float().double().t()).float())
+
+
 @pytest.mark.parametrize("m", [1, 40, 70, 300])
 def test_sums_are_exact_to_the_last_bit(plan, m):
     """The largest sums that 32 bits hold, and sums whose low bits fp32 additions would lose on the way."""
