@@ -307,7 +307,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
   args.ring_depth = p->desc.ring_depth;
   args.claim_lead = p->desc.claim_lead;
   args.claim_policy = p->desc.claim_policy;
-  args.raster_group = operands && operands->raster_group > 1 ? operands->raster_group : p->desc.raster == 1 ? p->desc.raster_group : 1;
+  args.raster_group = operands && operands->raster_group != 0 ? operands->raster_group : p->desc.raster == 1 ? p->desc.raster_group : 1;
   args.k_rotation = resolve_k_rotation(p->desc.k_rotation, grouped, args.single.N, p->desc.bn);
   args.counter_base = 0;
   if (mode == GEMM_SCHED_DYNAMIC && p->preset_pending) {
@@ -464,8 +464,8 @@ gemm_status plan_run_product(gemm_tile_cfg p, const ProductArgs &a, int form, in
   if (st != GEMM_OK || split <= 1) return st;
   const int32_t first = (int32_t)split_base, tiles = (int32_t)(tm * tn - split_base);
   const hipError_t e = form_is_loss(form) ? launch_reduce_loss(p->desc.bm, form, a.loss, p->d_ws, a.m, a.n, args.raster_group, first, tiles, split, s)
-                       : form == kFormNTI8 ? launch_reduce_i8(p->desc.bm, op, p->d_ws, a.m, a.n, first, tiles, split, s)
-                       : product_scales(form) == kScalesOne ? launch_reduce_scaled(p->desc.bm, op, p->d_ws, a.m, a.n, first, tiles, split, s)
+                       : form == kFormNTI8 ? launch_reduce_i8(p->desc.bm, op, p->d_ws, a.m, a.n, args.raster_group, first, tiles, split, s)
+                       : product_scales(form) == kScalesOne ? launch_reduce_scaled(p->desc.bm, op, p->d_ws, a.m, a.n, args.raster_group, first, tiles, split, s)
                                                             : launch_product_reduce(p->desc.bm, form, op, p->d_ws, a.m, a.n, first, tiles, split, s);
   return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "split product");
 }

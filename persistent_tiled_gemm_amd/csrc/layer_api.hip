@@ -190,7 +190,17 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   return best;
 }
 
-gemm_status run_choice(layer_plan *p, const ptg::ProductArgs &a, int form, const TileChoice &c, hipStream_t s) {
+// Rows of a super-tile (see decode_tile): 16 x 16 tiles, or as near as the product is wide.
+int32_t super_rows(int64_t tiles_m, int64_t tiles_n) {
+  int32_t r = 16;
+  while (r > 1 && r > tiles_m) r /= 2;
+  if (r == 16)
+    while (r < 256 && 256 / r > tiles_n) r *= 2;
+  return r;
+}
+
+gemm_status run_choice(layer_plan *p, ptg::ProductArgs a, int form, const TileChoice &c, hipStream_t s) {
+  if (form >= ptg::kFormNTI8) a.raster_group = -super_rows(ceil_div(a.m, c.edge), ceil_div(a.n, c.edge));
   gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
   gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
   if (st == GEMM_E_HIP) std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));
@@ -215,9 +225,6 @@ ptg::ProductArgs loss_product(const void *x, const void *w, int64_t ldx, int64_t
   k.m = (int32_t)m;
   k.n = (int32_t)n;
   k.k = (int32_t)kk;
-  // w is many times the caches: all of x's rows of tiles, up to 32, meet a column of w's
-  // together, so that w comes from memory once
-  k.raster_group = 32;
   return k;
 }
 

@@ -83,7 +83,7 @@ struct ProductArgs {
   int32_t m, n, k;
   EpilogueArgs ep;
   LossTerms loss;        // the loss forms', in the epilogue's place
-  int32_t raster_group;  // tile rows that are walked together, column by column (0: rows of tiles one by one)
+  int32_t raster_group;  // as KernelArgs' (0: the plan's)
 };
 
 // Forms of a product, by operand layout and type.
@@ -158,10 +158,10 @@ hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelAr
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s);
-hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
-                            int32_t chunks, hipStream_t s);
-hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first, int32_t tiles,
-                                int32_t chunks, hipStream_t s);
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group, int32_t first,
+                            int32_t tiles, int32_t chunks, hipStream_t s);
+hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+                                int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
 hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t raster_group,
                               int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
 // Columns of a block that leaves one partial maximum and sum: the tiles' and the few-row kernel's.

@@ -30,18 +30,19 @@ struct LossKernelArgs {
 
 __device__ __forceinline__ LossTerms loss_terms() { return late_args<LossTerms, offsetof(LossKernelArgs, loss)>(); }
 
+// A row's label as a column of the product, -1 where it has none there.
+__device__ __forceinline__ int32_t label_column(int64_t label, int64_t first) {
+  const int64_t at = label - first;
+  return label < 0 || at < 0 || at >= (int64_t)1 << 30 ? -1 : (int32_t)at;
+}
+
 // What the gradient takes of a row: exp(z - lse) = 2^(z log2 e - offset), dz = factor (that
 // - [column == at]). A row that is not counted has factor 0, and its dz are zeros whatever
 // its logits are, NaN included. A label past the vocabulary is a mistake, shown as NaN.
-struct RowGrad { float offset, factor; int32_t at; };
-__device__ __forceinline__ RowGrad row_grad(const LossTerms &l, int64_t m) {
-  const int64_t label = l.label[m];
-  RowGrad r;
-  r.offset = l.lse[m] * kLog2E;
-  r.factor = label < 0 ? 0.0f : label >= l.entries ? __uint_as_float(0x7fc00000u) : l.weight ? l.weight[m] : 1.0f;
-  const int64_t at = label - l.first;
-  r.at = at < 0 || at >= (int64_t)1 << 30 ? -1 : (int32_t)at;
-  return r;
+struct RowGrad { float offset, factor; int32_t at, pad; };
+__device__ __forceinline__ RowGrad row_grad(int64_t label, float lse, float weight, int64_t first, int64_t entries) {
+  const float factor = label < 0 ? 0.0f : label >= entries ? __uint_as_float(0x7fc00000u) : weight;
+  return {lse * kLog2E, factor, label_column(label, first), 0};
 }
 __device__ __forceinline__ float probability(float z, const RowGrad &r) { return __builtin_amdgcn_exp2f(fmaf(z, kLog2E, -r.offset)); }
 __device__ __forceinline__ float times_factor(float factor, float v) { return factor == 0.0f ? 0.0f : factor * v; }
@@ -49,58 +50,75 @@ __device__ __forceinline__ float times_factor(float factor, float v) { return fa
 template <int FORM>
 struct LossOp {
   using Args = ProductOpArgs;
-  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true;
-  static constexpr int kDirect = FORM == kFormLoss ? kDirectStats : kDirectValues;
+  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kLate = true;
+  static constexpr bool kGrad = FORM == kFormLogitGrad;
   template <int EDGE> using Tile = ProductOp<kFormNT>::Tile<EDGE>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
 
-  // The wave's WM x WN accumulators: lane l holds, of row l mod 16 of its MI blocks of
-  // rows, the columns 16 ni + 4 (l / 16) + 0..3. Two blocks at a time (their exchanges
-  // between lanes overlap; more do not fit the registers).
-  template <class CF, class Acc>
-  static __device__ __forceinline__ void stats(Acc &acc, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
-    static_assert(CF::MB == 16 && CF::WN == loss_block(CF::BN_), "blocks");
-    if (n_base >= N) return;  // a block past the vocabulary
-    if (n_base + CF::WN > N) stats_of<CF, true>(acc, lane, m_base, n_base, M, N);
-    else stats_of<CF, false>(acc, lane, m_base, n_base, M, N);
+  // A row's terms as asked for, and as finish reads them.
+  struct Ask { int64_t label; float lse, weight; };
+  using Row = typename std::conditional<kGrad, RowGrad, int32_t>::type;
+  static __device__ __forceinline__ Ask ask(int32_t m, int32_t M) {
+    const LossTerms l = loss_terms();
+    Ask a = {-1, 0.0f, 1.0f};
+    if (m >= M) return a;
+    a.label = l.label[m];
+    if constexpr (kGrad) {
+      a.lse = l.lse[m];
+      if (l.weight) a.weight = l.weight[m];
+    }
+    return a;
   }
-  template <class CF, bool EDGE, class Acc>
-  static __device__ __forceinline__ void stats_of(Acc &acc, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+  static __device__ __forceinline__ Row row(const Ask &a) {
+    const LossTerms l = loss_terms();
+    if constexpr (kGrad) return row_grad(a.label, a.lse, a.weight, l.first, l.entries);
+    else return label_column(a.label, l.first);
+  }
+
+  // The wave's WM x WN accumulators: lane l holds, of row l mod 16 of its MI blocks of
+  // rows, the columns 16 ni + 4 (l / 16) + 0..3. They leave the accumulator registers a few
+  // blocks at a time (the statements that name them: otherwise all 256 would at once, for
+  // memory).
+  template <class CF, class Acc>
+  static __device__ __forceinline__ void finish(Acc &acc, const Row *rows, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+    static_assert(CF::MB == 16 && CF::WN == loss_block(CF::BN_) && CF::NI % 2 == 0, "blocks");
+    if (n_base >= N) return;  // a block past the vocabulary
+    asm volatile("" : "+v"(lane));
+    if constexpr (kGrad) grad<CF>(acc, rows, lane, m_base, n_base, M, N);
+    else stats<CF>(acc, rows, lane, m_base, n_base, M, N);
+  }
+
+  // Two blocks of rows at a time (their exchanges between lanes overlap). Columns past the
+  // vocabulary, four at a time since it is a multiple of 8, are kept out by a limit of
+  // -infinity on their maximum and by an infinite offset: one operation a quad for each.
+  template <class CF, class Acc>
+  static __device__ __forceinline__ void stats(Acc &acc, const Row *rows, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
     constexpr int MI = CF::MI, NI = CF::NI, G = 2;
     const LossTerms l = loss_terms();
-    asm volatile("" : "+v"(lane));
     const uint32_t quarter = lane >> 4;
-    const int32_t row = m_base + (int32_t)(lane & 15u), left = N - n_base - (int32_t)(4u * quarter);
-    int32_t at[MI];  // the row's label, from the lane's first column on, where it is one of the lane's
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const int32_t m = row + 16 * mi;
-      const int64_t label = m < M ? l.label[m] : -1;
-      const int64_t off = label - l.first - n_base;
-      at[mi] = label >= 0 && off >= 0 && off < CF::WN && (((uint32_t)off >> 2) & 3u) == quarter ? (int32_t)off - (int32_t)(4u * quarter) : -1;
-    }
+    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * quarter), left = N - first;
     float2 *out = l.partial + (size_t)(n_base / CF::WN) * (size_t)M;
+    float limit[NI];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) limit[ni] = 16 * ni < left ? INFINITY : -INFINITY;
 #pragma unroll
     for (int g = 0; g < MI; g += G) {
-      // the sums leave their accumulator registers here, a group at a time
 #pragma unroll
       for (int u = 0; u < G; ++u)
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) asm volatile("" : "+a"(acc[g + u][ni]));
-      // columns past the vocabulary add nothing
-      auto logit = [&](int u, int ni, int e) -> float {
-        const float z = acc[g + u][ni][e];
-        return !EDGE || 16 * ni + e < left ? z : -INFINITY;
-      };
+      int32_t at[G];  // the label, from the lane's first column on
       float top[G], sum[G];
 #pragma unroll
       for (int u = 0; u < G; ++u) {
+        at[u] = rows[16 * (g + u) + (int)(lane & 15u)] - first;
         top[u] = -INFINITY;
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top[u] = fmaxf(top[u], logit(u, ni, e));
+        for (int ni = 0; ni < NI; ++ni) {
+          const auto &z = acc[g + u][ni];
+          top[u] = fmaxf(top[u], fminf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), limit[ni]));
+        }
       }
 #pragma unroll
       for (int o = 16; o < 64; o <<= 1)
@@ -111,17 +129,24 @@ struct LossOp {
         const float offset = offset_of(top[u]);
         float s = 0.0f;
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni)
+        for (int ni = 0; ni < NI; ++ni) {
+          const float o = fmaxf(offset, -limit[ni]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(logit(u, ni, e), kLog2E, -offset));
+          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[g + u][ni][e], kLog2E, -o));
+        }
         sum[u] = put_right(s, top[u], offset);
-        if (__ballot(at[g + u] >= 0)) {  // few tiles hold a label of theirs
+        if (__ballot(at[u] >= 0 && at[u] < CF::WN)) {  // few tiles hold a label of theirs
           float picked = 0.0f;
+          bool mine = false;
 #pragma unroll
           for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) picked = at[g + u] == 16 * ni + e ? acc[g + u][ni][e] : picked;
-          if (at[g + u] >= 0) l.picked[row + 16 * (g + u)] = picked;
+            for (int e = 0; e < 4; ++e) {
+              const bool here = at[u] == 16 * ni + e;
+              picked = here ? acc[g + u][ni][e] : picked;
+              mine = mine || here;
+            }
+          if (mine) l.picked[row + 16 * (g + u)] = picked;
         }
       }
 #pragma unroll
@@ -138,72 +163,78 @@ struct LossOp {
     }
   }
 
-  // The gradient: what a lane needs of its rows, and the logits of a block of rows to dz on
-  // their way into the staging.
-  template <class CF> struct Rows { RowGrad r[CF::MI]; };
-  template <class CF>
-  static __device__ __forceinline__ Rows<CF> rows(uint32_t lane, int32_t m_base, int32_t n_base, int32_t M) {
+  // dz of two blocks of columns at a time: four bf16 a lane and block, which two exchanges of
+  // lane quarters turn into eight consecutive ones, so that a store writes 64 bytes of
+  // sixteen rows. (Through LDS, in whole rows, a tile's took some 12 us longer than the loss's
+  // statistics.)
+  template <class CF, class Acc>
+  static __device__ __forceinline__ void grad(Acc &acc, const Row *rows, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+    constexpr int MI = CF::MI, NI = CF::NI;
     const LossTerms l = loss_terms();
-    asm volatile("" : "+v"(lane));
-    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * (lane >> 4));
-    Rows<CF> f;
+    const uint32_t quarter = lane >> 4;
+    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * quarter);
+    const int32_t n = n_base + (int32_t)(16u * (quarter >> 1) + 8u * (quarter & 1u));  // the lane's columns of a store
+    __bf16 *out = (__bf16 *)l.dz + (int64_t)row * l.lddz + n;
 #pragma unroll
-    for (int mi = 0; mi < CF::MI; ++mi) {
-      const int32_t m = row + 16 * mi;
-      f.r[mi] = {0.0f, 0.0f, -1};
-      if (m < M) f.r[mi] = row_grad(l, m);
-      f.r[mi].at -= first;
-    }
-    return f;
-  }
-  template <class CF, class Hold, class Get, class Put>
-  static __device__ __forceinline__ void values(const Rows<CF> &f, int mi, Hold hold, Get get, Put put) {
-    const RowGrad &r = f.r[mi];
-    const bool none = r.factor == 0.0f;
-    auto block = [&](int ni, bool labelled) {
-      hold(ni);  // in the accumulators until here
-      const f32x4 z = get(ni);
-      f32x4 v;
+    for (int mi = 0; mi < MI; ++mi) {
+      RowGrad r = rows[16 * mi + (int)(lane & 15u)];
+      r.at -= first;
+      const bool none = r.factor == 0.0f, in = row + 16 * mi < M;
+      auto pair = [&](int ni, bool labelled) {
+        typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+        u32x2 v[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float p = probability(z[e], r);
-        if (labelled) p -= r.at == 16 * ni + e ? 1.0f : 0.0f;
-        v[e] = none ? 0.0f : p * r.factor;
+        for (int h = 0; h < 2; ++h) {
+          asm volatile("" : "+a"(acc[mi][ni + h]));
+          f32x4 d;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = probability(acc[mi][ni + h][e], r);
+            if (labelled) p -= r.at == 16 * (ni + h) + e ? 1.0f : 0.0f;
+            d[e] = p * r.factor;
+          }
+          v[h] = __builtin_bit_cast(u32x2, __builtin_convertvector(d, bf16x4));
+          if (none) v[h] = u32x2{0u, 0u};
+        }
+        // quarters (a0 a1 a2 a3), (b0 b1 b2 b3) -> (a0 a2 b0 b2), (a1 a3 b1 b3)
+        i32x4 w;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const auto x = __builtin_amdgcn_permlane32_swap(v[0][j], v[1][j], false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+          w[j] = (int)y[0];
+          w[2 + j] = (int)y[1];
+        }
+        if (in && n + 16 * ni < N) *(i32x4 *)(out + 16 * ni) = w;
+      };
+      if (__ballot(r.at >= 0 && r.at < CF::WN)) {  // few tiles hold a label of theirs
+#pragma unroll
+        for (int ni = 0; ni < NI; ni += 2) pair(ni, true);
+      } else {
+#pragma unroll
+        for (int ni = 0; ni < NI; ni += 2) pair(ni, false);
       }
-      put(ni, v);
-    };
-    // few tiles hold a label of theirs
-    if (__ballot(r.at >= 0 && r.at < CF::WN)) {
-#pragma unroll
-      for (int ni = 0; ni < CF::NI; ++ni) block(ni, true);
-    } else {
-#pragma unroll
-      for (int ni = 0; ni < CF::NI; ++ni) block(ni, false);
+      out += 16 * l.lddz;
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Staged rows (see ProductOp) to memory: a K-chunk's sums as they are, or dz in bf16.
+  // Staged rows (see ProductOp) of a K-chunk's sums, to their slot.
   template <int RP, int ROW_B, int STRIDE>
   static __device__ __forceinline__ void flush(const Args &, const unsigned char *wl, uint32_t lane, int32_t m_base, int32_t n_base,
                                                int32_t M, int32_t N, float *slot) {
     constexpr int LPR = ROW_B / 32, RPI = 64 / LPR;
     asm volatile("" : "+v"(lane));
     const uint32_t q = lane % LPR, r0 = lane / LPR;
-    const int32_t n = n_base + (int32_t)(8u * q);
     const int32_t left = M - m_base - (int32_t)r0;
-    if (n >= N || left <= 0) return;
+    if (n_base + (int32_t)(8u * q) >= N || left <= 0) return;
     const int rows = left >= RP ? RP / RPI : (left + RPI - 1) / RPI;
-    const LossTerms l = loss_terms();
-    __bf16 *dz = (__bf16 *)l.dz + (int64_t)(m_base + (int32_t)r0) * l.lddz + n;
 #pragma unroll 4
     for (int i = 0; i < rows; ++i) {
       const uint32_t row = (uint32_t)(i * RPI) + r0;
       const f32x4 lo = *(const f32x4 *)(wl + row * ROW_B + (((2u * q) ^ (row & 15u)) << 4));
       const f32x4 hi = *(const f32x4 *)(wl + row * ROW_B + (((2u * q + 1u) ^ (row & 15u)) << 4));
-      const f32x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      if (slot) store8(slot + row * STRIDE + 8u * q, v);
-      else if (FORM == kFormLogitGrad) store8(dz + (int64_t)(i * RPI) * l.lddz, v);
+      store8(slot + row * STRIDE + 8u * q, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
@@ -233,7 +264,7 @@ __global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksAr
   if (in) z = chunk_sum<EDGE, false>(a.ws, tile, r, q, a.chunks);
   if constexpr (FORM == kFormLogitGrad) {
     if (!in) return;
-    const RowGrad g = row_grad(a.loss, m);
+    const RowGrad g = row_grad(a.loss.label[m], a.loss.lse[m], a.loss.weight ? a.loss.weight[m] : 1.0f, a.loss.first, a.loss.entries);
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = times_factor(g.factor, probability(z[e], g) - (g.at == n + e ? 1.0f : 0.0f));
     store8((__bf16 *)a.loss.dz + (int64_t)m * a.loss.lddz + n, z);

@@ -32,7 +32,7 @@ static hipError_t launch_reduce_edge(const ReduceArgs &a, int tiles, bool e8, hi
 
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s) {
-  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks};
+  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks, (m + tile_edge - 1) / tile_edge, 0};
   return tile_edge == 256 ? launch_reduce_edge<256>(a, tiles, form == kFormNTE4m3, s) : launch_reduce_edge<128>(a, tiles, form == kFormNTE4m3, s);
 }
 

@@ -124,7 +124,8 @@ struct ProductOp {
   using Args = ProductOpArgs;
   static constexpr bool AT = FORM == kFormTN || FORM == kFormTNScaled, E8 = FORM == kFormNTE4m3, I8 = FORM == kFormNTI8;
   static constexpr bool BT = FORM == kFormNT || E8 || I8, kPlain = false, kWide = !AT;
-  static constexpr int kScales = product_scales(FORM), kDirect = kDirectNone;
+  static constexpr int kScales = product_scales(FORM);
+  static constexpr bool kLate = false;
   // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step
   // ahead of their MFMAs (the 128 x 128 tile's other form, 32 x 32 blocks read half
   // a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192). k-contiguous
@@ -215,6 +216,7 @@ struct ReduceArgs {
   EpilogueArgs ep;
   const float *ws;
   int32_t m, n, tiles_n, first, chunks;  // first: the first split tile
+  int32_t tiles_m, raster_group;
 };
 // Its grid: EDGE rows a tile, 256 / (EDGE / 8) a workgroup.
 template <int EDGE>
@@ -237,8 +239,9 @@ template <int EDGE, int SCALES, bool I8>
 __device__ __forceinline__ void reduce_tiles(const ReduceArgs &a) {
   constexpr int LPR = EDGE / 8, kRows = 256 / LPR, kParts = EDGE / kRows;  // a workgroup: kRows rows of a tile
   const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
-  const int32_t t = a.first + (int32_t)tile;
-  const int32_t m = t / a.tiles_n * EDGE + (int32_t)r, n = t % a.tiles_n * EDGE + (int32_t)(8u * q);
+  int32_t m_t, n_t;
+  decode_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
+  const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
   if (m >= a.m || n >= a.n) return;
   const RowTerms row = row_terms<SCALES>(a.ep, m, n);
   const ColumnTerms col = column_terms<SCALES>(a.ep, n);
