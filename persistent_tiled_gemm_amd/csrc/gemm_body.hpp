@@ -323,11 +323,10 @@ __device__ __forceinline__ uint32_t claim_next(const KernelArgs &a, uint32_t xcc
 }
 
 // What an operation does with a whole tile's accumulators: stage them for flush, or
-// (kLate) its own work on them in registers, finish. That needs no LDS, so a worker does it
-// after the next tile's first loads have gone out, which land meanwhile (k = 2048, 256 x
-// 256: stats 4 us beside a fill of 5). What finish needs of the tile's rows is asked for at
-// the tile's own set-up and kept in LDS, two tiles' worth.
-
+// (kDirect) its own work on them in registers, finish. What finish needs of the tile's
+// rows is asked for at the tile's set-up and waits in LDS, two tiles' worth. (finish needs no
+// LDS else, so the next tile's first loads could go out before it: measured, the loss's
+// tiles then took 1 to 4% longer.)
 // The plain product: fp32 C, row strides as long as the rows. BT: B is given as
 // N x K row-major (C = A . B^T); its stage then holds BN rows x 32 k like A's, and
 // its fragments are read like A's.
@@ -335,15 +334,16 @@ template <bool BT_>
 struct PlainOp {
   struct Args {};
   static constexpr bool AT = false, BT = BT_, E8 = false, I8 = false, kPlain = true, kWide = false;
-  static constexpr bool kLate = false;
+  static constexpr bool kDirect = false;
   template <int EDGE> using Tile = typename TileCfg<EDGE>::type;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &pb, const Args &) { return pb.K; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &pb, const Args &) { return BT_ ? pb.K : pb.N; }
 };
 
-// LDS for the rows' terms of a late operation's tiles, two tiles' worth.
+// LDS for the rows' terms of a worker's tiles, two tiles' worth: a tile's are written before
+// barriers of its main loop, which all waves pass after they have read the tile's before last.
 template <class OP, int BM>
-__device__ __forceinline__ typename OP::Row *late_rows(uint32_t tile) {
+__device__ __forceinline__ typename OP::Row *row_terms_of(uint32_t tile) {
   __shared__ typename OP::Row rows[2][BM];
   return rows[tile & 1u];
 }
@@ -356,9 +356,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
   constexpr bool WA = OP::kWide && !AT, WB = OP::kWide && BT, WIDE = WA || WB;
   static_assert(!WIDE || CF::MB == 16, "wide stages are read in 16 x 16 blocks");
   static_assert(!E8 || (!AT && BT && CF::MB == 16), "e4m3 operands are both K-contiguous, in 16 x 16 blocks");
-  constexpr bool LATE = OP::kLate;
-  static_assert(!LATE || (CF::MB == 16 && WA && WB && CF::THREADS >= BM && !GROUPED), "late operations");
-  constexpr bool DEFER = LATE && MODE != kNonPersistent;  // (a workgroup of one tile finishes it at once)
+  constexpr bool DIRECT = OP::kDirect;
+  static_assert(!DIRECT || (CF::MB == 16 && CF::THREADS >= BM && !GROUPED), "direct operations");
   static_assert(!I8 || (!AT && BT && CF::MB == 16), "int8 operands are both K-contiguous, in 16 x 16 blocks");
   static_assert(CF::BM_ == BM && CF::BN_ == BN, "config");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[CF::LDS];  // the stage ring
@@ -465,19 +464,9 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
     valid = unit < (uint32_t)T;
   }
 
-  typedef typename std::conditional<I8, int, float>::type acc_t;
-  typedef acc_t accv __attribute__((ext_vector_type(CF::ACC_N)));
-  accv acc[CF::MI][CF::NI];
-  bool pending = false;          // acc holds a tile's sums that are not finished,
-  int32_t late_m = 0, late_n = 0;  // the wave's part of it: first row and column,
-  uint32_t late_tile = 0;        // and which of the worker's tiles it is
-  uint32_t late_count = 0;
-
+  uint32_t tiles_done = 0;  // of the worker
   uint32_t sub = 0;  // the current item's place in its unit (claim groups)
-  while (valid || (DEFER && pending)) {
-    // with nothing left but a tile to finish, the set-up below is of no tile, and loads nothing
-    const bool have = !DEFER || wave_uniform(valid ? 1u : 0u) != 0;
-    if constexpr (DEFER) unit = wave_uniform(have ? unit : 0u);
+  while (valid) {
     // ---- the work item: unit u covers items [u g, u g + g) (g = claim_group, 1
     // unless claim groups are on); items below split_base are whole tiles (id =
     // tile id), item split_base + q*S + c is K-chunk c of tile split_base + q
@@ -823,24 +812,9 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       }
     };
 
-    if constexpr (LATE) {
-      typename OP::Ask ask;
-      if (have) ask = OP::ask(m0 + (int32_t)tid, M);
-      if (have && ke > kb) {
-#pragma unroll
-        for (int q = 0; q < CF::NSTAGE; q += 2) issue_pair(q, kb + q);
-      }
-      if constexpr (DEFER) {
-        if (wave_uniform(pending ? 1u : 0u) != 0) {
-          OP::template finish<CF>(acc, late_rows<OP, BM>(late_tile) + wm * CF::WM, lane, late_m, late_n, M, N);
-          pending = false;
-        }
-        if (!have) break;
-      }
-      if (tid < (uint32_t)BM) late_rows<OP, BM>(late_count)[tid] = OP::row(ask);
-      wait_lds_all();
-      if (ke == kb) wg_barrier();  // (otherwise the main loop's)
-    }
+    typedef typename std::conditional<I8, int, float>::type acc_t;
+    typedef acc_t accv __attribute__((ext_vector_type(CF::ACC_N)));
+    accv acc[CF::MI][CF::NI];
 #pragma unroll
     for (int mi = 0; mi < CF::MI; ++mi)
 #pragma unroll
@@ -932,7 +906,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         // three k-steps in flight.
         // loads of a k-step that are not wide, and of a pair of k-steps
         constexpr int kNarrow = (WA ? 0 : CF::A_LOADS) + (WB ? 0 : CF::B_LOADS), kPair = kWide + 2 * kNarrow;
-        if constexpr (!LATE) {
+        auto first_loads = [&]() {
 #pragma unroll
           for (int q = 0; q < NST; ++q) {
             if constexpr (WIDE) {
@@ -940,6 +914,14 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
             }
             issue_all(q, kb + q);
           }
+        };
+        if constexpr (DIRECT) {
+          const auto ask = OP::ask(m0 + (int32_t)tid, M);
+          first_loads();
+          if (tid < (uint32_t)BM) row_terms_of<OP, BM>(tiles_done)[tid] = OP::row(ask);
+          wait_lds_all();
+        } else {
+          first_loads();
         }
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NST / 2 - 1) * kPair) : "memory");  // stages 0 and 1 landed
         wg_barrier();
@@ -1330,9 +1312,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       typedef acc_t acc4 __attribute__((ext_vector_type(4)));
       return __builtin_bit_cast(f32x4, acc4{acc[mi][ni][4 * qd + 0], acc[mi][ni][4 * qd + 1], acc[mi][ni][4 * qd + 2], acc[mi][ni][4 * qd + 3]});
     };
-    // (loads past the unit still write the stages that a late operation's next tile fills)
-    if constexpr (LATE) wait_vmem_all();
-    if (LATE ? split : !OP::kPlain || !split) {
+    if (DIRECT ? split : !OP::kPlain || !split) {
       epi_begin();
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
@@ -1340,27 +1320,21 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
         for (int mi = p * MI_PASS; mi < (p + 1) * MI_PASS; ++mi)
 #pragma unroll
           for (int ni = 0; ni < CF::NI; ++ni) {
-            if constexpr (LATE) asm volatile("" : "+a"(acc[mi][ni]));  // (see finish)
+            if constexpr (DIRECT) asm volatile("" : "+a"(acc[mi][ni]));  // (see finish)
 #pragma unroll
             for (int qd = 0; qd < CF::QUADS; ++qd) stage(p, mi, ni, qd, sums(mi, ni, qd));
           }
         flush(p);
       }
       epi_end();
-      if constexpr (DEFER) {
-        // nothing of these sums goes on to the next tile (said so, they need not meet the sums that do)
-#pragma unroll
-        for (int mi = 0; mi < CF::MI; ++mi)
-#pragma unroll
-          for (int ni = 0; ni < CF::NI; ++ni) acc[mi][ni] = __builtin_nondeterministic_value(acc[mi][ni]);
+    } else if constexpr (DIRECT) {
+      if (ke == kb) {  // no main loop, whose barriers the rows' terms pass
+        if (tid < (uint32_t)BM) row_terms_of<OP, BM>(tiles_done)[tid] = OP::row(OP::ask(m0 + (int32_t)tid, M));
+        wait_lds_all();
+        wg_barrier();
       }
-    } else if constexpr (DEFER) {
-      pending = true;
-      late_m = m0 + (int32_t)(wm * CF::WM);
-      late_n = n0 + (int32_t)(wn * CF::WN);
-      late_tile = late_count;
-    } else if constexpr (LATE) {
-      OP::template finish<CF>(acc, late_rows<OP, BM>(late_count) + wm * CF::WM, lane, m0 + (int32_t)(wm * CF::WM),
+      epi_begin();  // (loads past the unit still write the stages that the next one fills)
+      OP::template finish<CF>(acc, row_terms_of<OP, BM>(tiles_done) + wm * CF::WM, lane, m0 + (int32_t)(wm * CF::WM),
                               n0 + (int32_t)(wn * CF::WN), M, N);
     } else if constexpr (OP::kPlain) {
       // K-chunk of a split tile: publish the partial sum; the workgroup that
@@ -1436,7 +1410,7 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       }
     }
 
-    if constexpr (LATE) ++late_count;
+    if constexpr (DIRECT) ++tiles_done;
 
     // ---- claims after the work (claims_ahead = 0): issue and publish
     if (wave == 0) {

@@ -50,7 +50,7 @@ __device__ __forceinline__ float times_factor(float factor, float v) { return fa
 template <int FORM>
 struct LossOp {
   using Args = ProductOpArgs;
-  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kLate = true;
+  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kDirect = true;
   static constexpr bool kGrad = FORM == kFormLogitGrad;
   template <int EDGE> using Tile = ProductOp<kFormNT>::Tile<EDGE>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }

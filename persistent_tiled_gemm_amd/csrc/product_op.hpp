@@ -125,7 +125,7 @@ struct ProductOp {
   static constexpr bool AT = FORM == kFormTN || FORM == kFormTNScaled, E8 = FORM == kFormNTE4m3, I8 = FORM == kFormNTI8;
   static constexpr bool BT = FORM == kFormNT || E8 || I8, kPlain = false, kWide = !AT;
   static constexpr int kScales = product_scales(FORM);
-  static constexpr bool kLate = false;
+  static constexpr bool kDirect = false;
   // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step
   // ahead of their MFMAs (the 128 x 128 tile's other form, 32 x 32 blocks read half
   // a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192). k-contiguous
