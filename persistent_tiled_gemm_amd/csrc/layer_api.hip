@@ -444,8 +444,8 @@ gemm_status layer_linear(const layer_linear_args *a, layer_cfg p, void *stream) 
   k.ep.out_type = a->out_type;
   k.ep.act = a->activation;
   int64_t tiles = 0;
-  if (a->in_type == LAYER_I8 && ptg::rows_shared_preferred(k, p->cu_count) &&
-      ptg::rows_shared_floats(k, p->cu_count, &tiles) <= p->ws_floats && tiles <= kArrivals) {
+  if (a->in_type == LAYER_I8 && ptg::rows_shared_preferred(k, LAYER_I8, p->cu_count) &&
+      ptg::rows_shared_floats(k, LAYER_I8, p->cu_count, &tiles) <= p->ws_floats && tiles <= kArrivals) {
     hipError_t e = ptg::launch_rows_shared(k, p->ws, p->d_arrivals, p->cu_count, s);
     return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "linear");
   }
@@ -602,16 +602,20 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, 
   k.loss.picked = a->lse;
   k.loss.entries = a->n;
   hipError_t e;
-  if (ptg::rows_preferred(k, LAYER_BF16)) {
-    int64_t tiles = 0;
-    const int64_t parts = ceil_div(ptg::rows_partial_floats(k, LAYER_BF16, p->cu_count, &tiles), 2) * 2;
-    const int64_t blocks = ceil_div(a->n, ptg::rows_loss_block(k, p->cu_count));
-    if (parts + 2 * blocks * a->m > p->ws_floats || tiles > kArrivals) return GEMM_E_SHAPE;
-    k.loss.partial = reinterpret_cast<float2 *>(p->ws + parts);
-    e = ptg::launch_rows_loss(k, p->ws, p->d_arrivals, p->cu_count, s);
-    if (e != hipSuccess) return hip_fail(p, e, "cross entropy");
-    e = ptg::launch_loss_join(k.loss.partial, (int32_t)blocks, a->label, a->n, a->lse, a->loss, k.m, s);
-    return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "cross entropy");
+  int64_t tiles = 0;
+  const bool shared = ptg::rows_shared_preferred(k, LAYER_BF16, p->cu_count);
+  if (shared || ptg::rows_preferred(k, LAYER_BF16)) {
+    const int64_t sums = shared ? ptg::rows_shared_floats(k, LAYER_BF16, p->cu_count, &tiles) : ptg::rows_partial_floats(k, LAYER_BF16, p->cu_count, &tiles);
+    const int64_t parts = ceil_div(sums, 2) * 2;
+    const int64_t blocks = ceil_div(a->n, shared ? ptg::rows_shared_loss_block(k, p->cu_count) : ptg::rows_loss_block(k, p->cu_count));
+    if (parts + 2 * blocks * a->m <= p->ws_floats && tiles <= kArrivals) {
+      k.loss.partial = reinterpret_cast<float2 *>(p->ws + parts);
+      e = shared ? ptg::launch_rows_shared_loss(k, p->ws, p->d_arrivals, p->cu_count, s)
+                 : ptg::launch_rows_loss(k, p->ws, p->d_arrivals, p->cu_count, s);
+      if (e != hipSuccess) return hip_fail(p, e, "cross entropy");
+      e = ptg::launch_loss_join(k.loss.partial, (int32_t)blocks, a->label, a->n, a->lse, a->loss, k.m, s);
+      return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "cross entropy");
+    }
   }
   // Tiles, in as many runs over the rows as the blocks' partial sums need. Those lie in the
   // workspace that the run's own split tiles leave free.

@@ -130,10 +130,12 @@ bool rows_preferred(const ProductArgs &p, int type);
 // Workspace of a call, floats; *tiles: the arrival counts it uses.
 int64_t rows_partial_floats(const ProductArgs &p, int type, int cu_count, int64_t *tiles);
 hipError_t launch_rows(const ProductArgs &p, int type, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
-// The same for int8 operands with x in LDS.
-bool rows_shared_preferred(const ProductArgs &p, int cu_count);
-int64_t rows_shared_floats(const ProductArgs &p, int cu_count, int64_t *tiles);
+// The same with x in LDS: int8 operands, and bf16 with a cross entropy's end.
+bool rows_shared_preferred(const ProductArgs &p, int type, int cu_count);
+int64_t rows_shared_floats(const ProductArgs &p, int type, int cu_count, int64_t *tiles);
 hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
+int32_t rows_shared_loss_block(const ProductArgs &p, int cu_count);
+hipError_t launch_rows_shared_loss(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);
 // A cross entropy's end of the same product (bf16): p.loss, in column blocks of rows_loss_block.
 int32_t rows_loss_block(const ProductArgs &p, int cu_count);
 hipError_t launch_rows_loss(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s);

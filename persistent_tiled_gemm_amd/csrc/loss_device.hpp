@@ -14,5 +14,10 @@ __device__ __forceinline__ float offset_of(float top) { return fabsf(top) < INFI
 __device__ __forceinline__ float put_right(float sum, float top, float offset) {
   return fabsf(top) < INFINITY ? fmaf(sum, -fmaf(top, kLog2E, -offset) * kLn2, sum) : sum;
 }
+// A sum of exponentials below one maximum, below another.
+__device__ __forceinline__ float rescaled(float sum, float from, float to) {
+  // (equal maxima are not subtracted: both may be infinite)
+  return from == to ? sum : sum * __builtin_amdgcn_exp2f((from - to) * kLog2E);
+}
 
 }  // namespace ptg

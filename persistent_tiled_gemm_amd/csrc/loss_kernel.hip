@@ -303,10 +303,6 @@ struct LossJoinArgs {
   int64_t entries;
   int32_t blocks, m;
 };
-__device__ __forceinline__ float rescaled(float sum, float from, float to) {
-  // (equal maxima are not subtracted: both may be infinite)
-  return from == to ? sum : sum * __builtin_amdgcn_exp2f((from - to) * kLog2E);
-}
 template <int R>
 __global__ __launch_bounds__(512) void ptg_loss_join_kernel(const LossJoinArgs a) {
   constexpr int S = 512 / R, U = 8;
@@ -354,7 +350,7 @@ __global__ __launch_bounds__(512) void ptg_loss_join_kernel(const LossJoinArgs a
 hipError_t launch_loss_join(const float2 *partial, int32_t blocks, const int64_t *label, int64_t entries, float *lse, float *loss, int32_t m,
                             hipStream_t s) {
   const LossJoinArgs a = {partial, label, lse, loss, entries, blocks, m};
-  if (m > 64) hipLaunchKernelGGL(ptg_loss_join_kernel<16>, dim3((uint32_t)(m + 15) / 16u), dim3(512), 0, s, a);
+  if (m >= 16) hipLaunchKernelGGL(ptg_loss_join_kernel<16>, dim3((uint32_t)(m + 15) / 16u), dim3(512), 0, s, a);
   else if (m > 1) hipLaunchKernelGGL(ptg_loss_join_kernel<2>, dim3((uint32_t)(m + 1) / 2u), dim3(512), 0, s, a);
   else hipLaunchKernelGGL(ptg_loss_join_kernel<1>, dim3(1), dim3(512), 0, s, a);
   return hipGetLastError();

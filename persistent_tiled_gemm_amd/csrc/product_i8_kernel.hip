@@ -13,7 +13,7 @@ __global__ __launch_bounds__(256, product_workgroups(EDGE, kFormNTI8)) void ptg_
 
 template <int EDGE>
 __global__ __launch_bounds__(256) void ptg_product_i8_reduce_kernel(const ReduceArgs a) {
-  reduce_tiles<EDGE, kScalesRowCol, true>(a);
+  reduce_tiles<EDGE, kScalesRowCol, true, true>(a);
 }
 
 hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group, int32_t first, int32_t tiles, int32_t chunks,

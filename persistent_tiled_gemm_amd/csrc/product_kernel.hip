@@ -19,7 +19,7 @@ __global__ __launch_bounds__(256, product_workgroups(EDGE, FORM)) void ptg_produ
 
 template <int EDGE, bool E8>
 __global__ __launch_bounds__(256) void ptg_product_reduce_kernel(const ReduceArgs a) {
-  reduce_tiles<EDGE, E8 ? kScalesRowCol : kScalesNone, false>(a);
+  reduce_tiles<EDGE, E8 ? kScalesRowCol : kScalesNone, false, false>(a);
 }
 
 template <int EDGE>

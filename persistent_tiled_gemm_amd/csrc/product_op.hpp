@@ -235,12 +235,13 @@ __device__ __forceinline__ f32x8 chunk_sum(const float *ws, uint32_t tile, uint3
   return sums_of<I8>(z);
 }
 
-template <int EDGE, int SCALES, bool I8>
+template <int EDGE, int SCALES, bool I8, bool SUPER>
 __device__ __forceinline__ void reduce_tiles(const ReduceArgs &a) {
   constexpr int LPR = EDGE / 8, kRows = 256 / LPR, kParts = EDGE / kRows;  // a workgroup: kRows rows of a tile
   const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
-  int32_t m_t, n_t;
-  decode_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
+  const int32_t t = a.first + (int32_t)tile;
+  int32_t m_t = t / a.tiles_n, n_t = t % a.tiles_n;
+  if constexpr (SUPER) decode_tile(t, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
   const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
   if (m >= a.m || n >= a.n) return;
   const RowTerms row = row_terms<SCALES>(a.ep, m, n);

@@ -12,7 +12,7 @@ __global__ __launch_bounds__(256, product_workgroups(EDGE, FORM)) void ptg_produ
 
 template <int EDGE>
 __global__ __launch_bounds__(256) void ptg_product_scaled_reduce_kernel(const ReduceArgs a) {
-  reduce_tiles<EDGE, kScalesOne, false>(a);
+  reduce_tiles<EDGE, kScalesOne, false, true>(a);
 }
 
 hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group, int32_t first, int32_t tiles, int32_t chunks,

@@ -1,4 +1,5 @@
-// The product for some rows (up to 64) with x in LDS, for int8 operands.
+// The product for some rows (up to 64) with x in LDS: int8 operands with the layer
+// operators' epilogue, and bf16 operands with a cross entropy's end (see loss_kernel.hip).
 //
 // rows_kernel.hip reads w and x alike from memory into MFMA operands. x comes from the
 // caches, but returns in turn with w, and so takes its share of the loads that a CU can
@@ -15,15 +16,31 @@
 #include <algorithm>
 
 #include "layer_device.hpp"
+#include "loss_device.hpp"
 
 namespace ptg {
 
 static constexpr int kSharedBytes = 128 * 1024;
 static constexpr int kPolicyStream = 2;  // nt: w is read once
 
-template <int MT, int WAVES, int DEPTH>
-__global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const RowsArgs a) {
+template <bool I8>
+__device__ __forceinline__ f32x4 mfma_step(const i32x4 &w, const i32x4 &x, const f32x4 &acc) {
+  if constexpr (I8) return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, __builtin_bit_cast(i32x4, acc), 0, 0, 0));
+  else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+}
+template <bool I8>
+__device__ __forceinline__ f32x4 add_parts(const f32x4 &a, const f32x4 &b) {
+  if constexpr (I8) return __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, a) + __builtin_bit_cast(i32x4, b));
+  else return a + b;
+}
+
+// I8: int8 operands and the layer operators' epilogue; otherwise bf16 and a cross entropy's.
+// Lengths and strides in bytes from here on.
+template <bool I8, int MT, int WAVES, int DEPTH>
+__device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &loss) {
   constexpr int kRows = 16 * MT;
+  constexpr uint32_t kSize = I8 ? 1u : 2u;
+  const uint32_t bytes = (uint32_t)a.k * kSize, ldx = (uint32_t)a.ldx * kSize, ldw = (uint32_t)a.ldw * kSize;
   __shared__ __attribute__((aligned(1024))) unsigned char xs[kSharedBytes];
   __shared__ uint32_t last;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = wave_uniform(tid >> 6);
@@ -32,7 +49,7 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
   const uint32_t row = lane & 15u, group = lane >> 4;
 
   // the workgroup's share of k, in segments of 256 bytes (four steps of 64)
-  const uint32_t segs = ((uint32_t)a.k + 255u) / 256u;
+  const uint32_t segs = (bytes + 255u) / 256u;
   const uint32_t g0 = segs * part / gridDim.y, count = segs * (part + 1u) / gridDim.y - g0;
   // each wave starts part-way into the share and wraps around, so that the waves spread
   // over the memory channels
@@ -46,17 +63,17 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
     for (uint32_t i = wave; i < loads; i += WAVES) {
       const uint32_t seg = i / (uint32_t)(kRows / 4), r = (i % (uint32_t)(kRows / 4)) * 4u + group;
       const uint32_t at = (g0 + seg) * 256u + (row ^ (r & 15u)) * 16u;
-      load16_to_lds(xr, base + i * 1024u, (int32_t)r < a.m && at < (uint32_t)a.k ? r * (uint32_t)a.ldx + at : kBufOob);
+      load16_to_lds(xr, base + i * 1024u, (int32_t)r < a.m && at < bytes ? r * ldx + at : kBufOob);
     }
   }
 
   // ---- w: DEPTH segments of the wave's rows under way. Segments past the share are asked
   // for out of range (zeros, no traffic), so that every turn of the loop is alike and waits for
   // the oldest segment alone.
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)a.ldw);
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)ldw);
   const bool w_in = n0 + (int32_t)row < a.n;
-  const uint32_t w_row = row * (uint32_t)a.ldw;  // byte offset of the lane's row
-  i32x4 acc[MT] = {};
+  const uint32_t w_row = row * ldw;  // byte offset of the lane's row
+  f32x4 acc[MT] = {};  // (int8: the bits of integers)
   i32x4 w[DEPTH][4];
   auto seg_of = [&](uint32_t g) -> uint32_t { return g + rot < count ? g + rot : g + rot - count; };
   auto load = [&](int d, uint32_t g) {
@@ -64,7 +81,7 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t at = first + 64u * (uint32_t)u + 16u * group;
-      const bool in = w_in && g < count && at < (uint32_t)a.k;
+      const bool in = w_in && g < count && at < bytes;
       w[d][u] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? (int)(w_row + at) : (int)kBufOob, 0, kPolicyStream);
     }
   };
@@ -76,7 +93,7 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const i32x4 x = *(const i32x4 *)(seg + (off ^ (uint32_t)(64 * u)) + t * 16 * 256);
-        acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[d][u], x, acc[t], 0, 0, 0);
+        acc[t] = mfma_step<I8>(w[d][u], x, acc[t]);
       }
   };
   if (count > 0) {
@@ -95,14 +112,14 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
   }
 
   // ---- the shares of k meet: each part through to memory, a relaxed count, and the last
-  // workgroup of the tile adds the parts in order (integers: in any order the same)
+  // workgroup of the tile adds the parts, in order (integers give the same in any)
   const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.partial);
   constexpr uint32_t kSlots = (uint32_t)(WAVES * MT * 64);
   const uint32_t mine = wave * (uint32_t)(MT * 64) + lane;
   if (gridDim.y > 1) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-      store16_agent(pr, ((tile * gridDim.y + part) * kSlots + mine + (uint32_t)t * 64u) * 16u, __builtin_bit_cast(f32x4, acc[t]));
+      store16_agent(pr, ((tile * gridDim.y + part) * kSlots + mine + (uint32_t)t * 64u) * 16u, acc[t]);
     wait_vmem_all();
     __syncthreads();
     if (tid == 0) {
@@ -112,12 +129,50 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
     }
     __syncthreads();
     if (wave_uniform(last) == 0) return;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (uint32_t p = 0; p < gridDim.y; ++p) {
-      if (p == part) continue;
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        acc[t] += __builtin_bit_cast(i32x4, load16_agent(pr, ((tile * gridDim.y + p) * kSlots + mine + (uint32_t)t * 64u) * 16u));
+        acc[t] = add_parts<I8>(acc[t], load16_agent(pr, ((tile * gridDim.y + p) * kSlots + mine + (uint32_t)t * 64u) * 16u));
     }
+  }
+  if constexpr (!I8) {
+    // a lane holds four columns of row 16 t + row: the wave's 16 of a row are in four lanes.
+    // The waves' maxima and sums meet in LDS (x is done with), one block a workgroup.
+    float2 *meet = (float2 *)xs;  // [row][wave]
+    __syncthreads();
+    const int32_t first = n0 + 4 * (int32_t)group;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int32_t m = 16 * t + (int32_t)row;
+      const int64_t label = m < a.m ? loss.label[m] : -1;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (first < a.n && label == first + q) loss.picked[m] = acc[t][q];
+        top = first < a.n ? fmaxf(top, acc[t][q]) : top;
+      }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float offset = offset_of(top);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += first < a.n ? __builtin_amdgcn_exp2f(fmaf(acc[t][q], kLog2E, -offset)) : 0.0f;
+      sum = put_right(sum, top, offset);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (group == 0) meet[(uint32_t)m * WAVES + wave] = make_float2(top, sum);
+    }
+    __syncthreads();
+    const int32_t m = (int32_t)tid;
+    if (m >= a.m || m >= kRows) return;
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, meet[m * WAVES + v].x);
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) sum += rescaled(meet[m * WAVES + v].y, meet[m * WAVES + v].x, top);
+    loss.partial[(size_t)tile * (size_t)a.m + m] = make_float2(top, sum);
+    return;
   }
   // ---- epilogue: four columns of one row at a time
   const EpilogueArgs &e = a.ep;
@@ -127,7 +182,7 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
   for (int t = 0; t < MT; ++t) {
     const int64_t m = 16 * t + (int32_t)row;
     if (m >= a.m) continue;
-    f32x4 z = __builtin_convertvector(acc[t], f32x4);
+    f32x4 z = __builtin_convertvector(__builtin_bit_cast(i32x4, acc[t]), f32x4);
     if (e.row_scale) z *= e.row_scale[m];
     if (e.col_scale) z *= *(const f32x4 *)(e.col_scale + n);
     if (e.bias) z += load4_as(e.bias, e.bias_type, n);
@@ -140,39 +195,55 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const Ro
   }
 }
 
+template <int MT, int WAVES, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_i8_kernel(const RowsArgs a) {
+  rows_shared<true, MT, WAVES, DEPTH>(a, LossTerms{});
+}
+template <int MT, int WAVES, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_loss_kernel(const RowsArgs a, const LossTerms loss) {
+  rows_shared<false, MT, WAVES, DEPTH>(a, loss);
+}
+
 // The shape of a call: 16-row blocks of x, the waves of a workgroup (16 rows of w each) and
 // the shares of k: as many as bring the workgroups to the CUs' number, and as x needs to
 // fit. Up to 32 rows four waves with four segments under way; more take eight with two,
-// so that fewer workgroups hold copies of x (8192^2, 64 rows: four 24.2 us, eight 20.9).
+// so that fewer workgroups hold copies of x (int8 8192^2, 64 rows: four 24.2 us, eight 20.9).
 struct SharedShape { int mt, waves; int64_t tiles, split; };
-static SharedShape shared_shape(int32_t m, int32_t n, int32_t k, int cu_count) {
+static SharedShape shared_shape(const ProductArgs &p, int type, int cu_count) {
   SharedShape f;
-  f.mt = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+  f.mt = p.m <= 16 ? 1 : p.m <= 32 ? 2 : 4;
   f.waves = f.mt < 4 ? 4 : 8;
-  f.tiles = (n + 16 * f.waves - 1) / (16 * f.waves);
-  const int64_t segs = (k + 255) / 256, fits = kSharedBytes / (f.mt * 16 * 256);
+  f.tiles = (p.n + 16 * f.waves - 1) / (16 * f.waves);
+  const int64_t segs = ((int64_t)p.k * (type == kTypeI8 ? 1 : 2) + 255) / 256, fits = kSharedBytes / (f.mt * 16 * 256);
   f.split = std::max<int64_t>({1, std::min<int64_t>({cu_count / f.tiles, segs, 16}), (segs + fits - 1) / fits});
   return f;
 }
 
-int64_t rows_shared_floats(const ProductArgs &p, int cu_count, int64_t *tiles) {
-  const SharedShape f = shared_shape(p.m, p.n, p.k, cu_count);
+int64_t rows_shared_floats(const ProductArgs &p, int type, int cu_count, int64_t *tiles) {
+  const SharedShape f = shared_shape(p, type, cu_count);
   *tiles = f.split > 1 ? f.tiles : 0;
   return *tiles * f.split * f.waves * f.mt * 256;
 }
 
-// Where w is large enough to be worth x's way through LDS: from 8 rows on with 32 Mi
+// Where w is large enough to be worth x's way through LDS. int8: from 8 rows on with 32 Mi
 // elements of w (8192^2: 4 rows 16.5 us here and 16.1 there, 8 rows 16.4 and 16.6, 24 rows
 // 17.9 and 22.0), from 32 rows on with 16 Mi (4096^2: 24 rows 9.4 and 8.8, 48 rows 10.9 and
 // 11.4). Smaller w runs in the few-row kernel at every m (2048^2, 64 rows: 9.6 and 7.5).
-bool rows_shared_preferred(const ProductArgs &p, int cu_count) {
-  const int64_t size = (int64_t)p.n * p.k;
-  if (p.m > kRowsMost || size < (int64_t)16 << 20 || p.m < (size < (int64_t)32 << 20 ? 32 : 8)) return false;
-  return shared_shape(p.m, p.n, p.k, cu_count).split <= 16;
+// The cross entropy's bf16: from 8 rows on with 32 Mi elements (131072 x 2048: 4 rows 111 and
+// 109, 8 rows 112 and 119) and rows of 1024 (100000 x 512, 8 rows: 37 and 30); from 17 on with
+// 16 Mi (4096^2, 24 rows: 16.0 and 18.1) up to where the tiles are as fast, whose x is read
+// less often (24 rows: 8192 x 4096 21.7 here and 28.8 as tiles, 16384 x 8192 67 and 73, 32768 x
+// 4096 68 and 62, 50264 x 2056 83 and 75).
+bool rows_shared_preferred(const ProductArgs &p, int type, int cu_count) {
+  const int64_t size = (int64_t)p.n * p.k, mi = (int64_t)1 << 20;
+  if (p.m > kRowsMost || size < 16 * mi || shared_shape(p, type, cu_count).split > 16) return false;
+  if (type == kTypeI8) return p.m >= (size < 32 * mi ? 32 : 8);
+  if (p.k < 1024) return false;
+  if (p.m <= 16) return p.m >= 8 && size >= 32 * mi;
+  return p.n <= 32768 && (size < 128 * mi || p.n <= 16384);
 }
 
-hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
-  const SharedShape f = shared_shape(p.m, p.n, p.k, cu_count);
+static RowsArgs rows_args(const ProductArgs &p, float *partial, uint32_t *arrivals) {
   RowsArgs a;
   a.x = p.a;
   a.w = p.b;
@@ -184,10 +255,28 @@ hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *ar
   a.partial = partial;
   a.arrivals = arrivals;
   a.ep = p.ep;
+  return a;
+}
+
+hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
+  const SharedShape f = shared_shape(p, kTypeI8, cu_count);
+  const RowsArgs a = rows_args(p, partial, arrivals);
   const dim3 grid((uint32_t)f.tiles, (uint32_t)f.split), block(64 * f.waves);
   if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<1, 4, 4>), grid, block, 0, s, a);
   else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<2, 4, 4>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<4, 8, 2>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+int32_t rows_shared_loss_block(const ProductArgs &p, int cu_count) { return 16 * shared_shape(p, kTypeBf16, cu_count).waves; }
+
+hipError_t launch_rows_shared_loss(const ProductArgs &p, float *partial, uint32_t *arrivals, int cu_count, hipStream_t s) {
+  const SharedShape f = shared_shape(p, kTypeBf16, cu_count);
+  const RowsArgs a = rows_args(p, partial, arrivals);
+  const dim3 grid((uint32_t)f.tiles, (uint32_t)f.split), block(64 * f.waves);
+  if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<1, 4, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<2, 4, 4>), grid, block, 0, s, a, p.loss);
+  else hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<4, 8, 2>), grid, block, 0, s, a, p.loss);
   return hipGetLastError();
 }
 

@@ -88,6 +88,19 @@ def test_loss_sizes(plan, m, n, k):
     check_forward(plan, m, n, k, pad=8)
 
 
+# w large enough that few rows' x goes through LDS: one share of k and several, a share that ends inside a segment, a ragged
+# last block of w
+@pytest.mark.parametrize("m,n,k", [(8, 33032, 1032), (11, 8200, 4104), (16, 2056, 16400), (17, 16392, 1040), (24, 4104, 4112), (32, 2056, 8208),
+                                   (33, 8200, 2064), (48, 1032, 32784), (64, 16392, 1296), (63, 4104, 8200)])
+def test_loss_of_some_rows_of_a_large_weight(plan, m, n, k):
+    say("cross entropy, some rows", m, n, k)
+    check_forward(plan, m, n, k, pad=24)
+    x, w, label, a = check_forward(plan, m, n, k)
+    b = forward(plan, x, w, label)[0][1: m + 1]
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("m,n,k", SHAPES)
 def test_gradient_sizes(plan, m, n, k):
     say("cross entropy backward", m, n, k)
