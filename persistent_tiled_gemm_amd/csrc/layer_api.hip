@@ -617,20 +617,25 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, 
       return e == hipSuccess ? GEMM_OK : hip_fail(p, e, "cross entropy");
     }
   }
-  // Tiles, in as many runs over the rows as the blocks' partial sums need. Those lie in the
-  // workspace that the run's own split tiles leave free.
-  const int64_t blocks128 = ceil_div(a->n, ptg::loss_block(128));
-  const int64_t most = std::max<int64_t>(256, std::min(p->ws_floats, p->ws128_floats * 2) / (2 * blocks128) / 256 * 256);
-  const int64_t runs = ceil_div(a->m, most), rows = ceil_div(ceil_div(a->m, runs), 256) * 256;
+  // Tiles. The blocks' partial sums lie in the workspace that the run's own split tiles leave
+  // free; where that holds no more than a part of the rows, they run in parts of 256 x 256
+  // tiles, unsplit.
+  TileChoice c = choose_tiles(k, ptg::kFormLoss, p->cu_count);
+  float *at = c.edge == 256 && c.split > 1 ? p->ws128 : p->ws;
+  int64_t blocks = ceil_div(a->n, ptg::loss_block(c.edge)), rows = a->m;
+  if (2 * blocks * a->m > (at == p->ws ? p->ws_floats : p->ws128_floats)) {
+    c = {256, 1, 0, 0.0};
+    at = p->ws;
+    blocks = ceil_div(a->n, ptg::loss_block(256));
+    const int64_t most = p->ws_floats / (2 * blocks) / 256 * 256;
+    if (most < 256) return GEMM_E_SHAPE;  // (not so for any n within the limit)
+    rows = ceil_div(ceil_div(a->m, ceil_div(a->m, most)), 256) * 256;
+  }
   for (int64_t first = 0; first < a->m; first += rows) {
     k.m = (int32_t)std::min(rows, a->m - first);
     k.a = static_cast<const uint16_t *>(a->x) + first * k.lda;
     k.loss.label = a->label + first;
     k.loss.picked = a->lse + first;
-    const TileChoice c = choose_tiles(k, ptg::kFormLoss, p->cu_count);
-    const int64_t blocks = ceil_div(a->n, ptg::loss_block(c.edge));
-    float *at = c.edge == 256 && c.split > 1 ? p->ws128 : p->ws;
-    if (2 * blocks * k.m > (at == p->ws ? p->ws_floats : p->ws128_floats)) return GEMM_E_SHAPE;
     k.loss.partial = reinterpret_cast<float2 *>(at);
     st = run_choice(p, k, ptg::kFormLoss, c, s);
     if (st != GEMM_OK) return st;

@@ -6,6 +6,7 @@ import torch
 
 import persistent_tiled_gemm_amd as ptg
 from oracle import layer_ref as ref
+from tests import head_cases
 from tests.layer_util import Out, normal, say, within
 from tests.test_gpu_layer_linear import LARGE, SHAPES, sampled
 
@@ -114,6 +115,12 @@ def test_some_rows_of_a_large_weight(plan, m, n, k):
     ptg.layer_linear(x, w, b, plan)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(a.cpu(), (x.cpu().float().double() @ w.cpu().float().double().t()).float())
+
+
+@pytest.mark.parametrize("what,kind,m,n,k", [c for c in head_cases.CASES if c[1] == "i8"])
+def test_every_kernel(plan, what, kind, m, n, k):
+    say(what, m, n, k)
+    check(plan, m, n, k, BF16, "silu", rows=sampled(m, 256)[:200])
 
 
 @pytest.mark.parametrize("m", [1, 40, 70, 300])

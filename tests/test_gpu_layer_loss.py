@@ -5,6 +5,7 @@ import torch
 
 import persistent_tiled_gemm_amd as ptg
 from oracle import layer_ref as ref
+from tests import head_cases
 from tests.layer_util import Out, normal, say, within
 
 pytestmark = pytest.mark.gpu
@@ -317,6 +318,47 @@ def test_a_step_replays_from_a_graph(plan, streams, m):
     torch.cuda.synchronize()
 
 
+def check_sampled(plan, m, n, k, pieces=1, backward=True):
+    """Some rows of every output against the oracle, the whole of it finite and the same bits twice."""
+    x, w, label = head(m, n, k)
+    lse, loss = forward(plan, x, w, label)
+    at = torch.randperm(m, generator=torch.Generator().manual_seed(m))[:40]
+    at = torch.cat([at, torch.tensor([0, 255, 256, m - 1]).clamp(max=m - 1)]).cuda()
+    torch.cuda.synchronize()
+    exact, bound = ref.cross_entropy(x[at], w, label[at]), ref.cross_entropy_bounds(x[at], w, label[at])
+    within(lse[1:-1][at], exact[0], bound[0], f"lse {m} {n} {k}")
+    within(loss[1:-1][at], exact[1], bound[1], f"loss {m} {n} {k}")
+    again = forward(plan, x, w, label)
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], lse) and torch.equal(again[1], loss) and torch.isfinite(lse).all() and torch.isfinite(loss).all()
+    if not backward:
+        return
+    dx, dw = Out(m, k, BF16), Out(n, k, F32)
+    scratch = torch.empty(ptg.layer_cross_entropy_scratch(m, n, k, pieces), dtype=torch.uint8, device="cuda")
+    ptg.layer_cross_entropy_backward(x, w, label, lse[1: m + 1], scratch, plan, dx=dx.t, dw=dw.t)
+    torch.cuda.synchronize()
+    dx.check()
+    dw.check()
+    (want, off), _ = ref.cross_entropy_backward_bounds(x[at], w, label[at], lse[1:-1][at], BF16, F32)
+    within(dx.t[at], want, off, f"dx {m} {n} {k}")
+    # dw's rows: dz's columns of some of the vocabulary's entries
+    to = torch.randperm(n, generator=torch.Generator().manual_seed(n))[:40]
+    to = torch.cat([to, torch.tensor([0, 255, 256, n - 1]).clamp(max=n - 1)]).cuda()
+    z, v = ref.d(x) @ ref.d(w[to]).t(), ref.d(lse[1:-1])[:, None]
+    dz = torch.exp(z - v) - (label.cpu()[:, None] == to.cpu()[None, :]).double()
+    dz[label.cpu() < 0] = 0.0
+    t = ref._logits_error(x, w[to]) + 3 * ref.U32 * (z.abs() + v.abs())
+    err = torch.exp(z - v) * (torch.expm1(t) + 4 * ref.U32) + 2 * ref.U32
+    err = err + 2.0 ** -8 * (dz.abs() + err) + 2.0 ** -126
+    exact_dw = dz.t() @ ref.d(x)
+    off = ref.rounded(exact_dw, F32, err.t() @ ref.d(x).abs() + (dz.abs().t() @ ref.d(x).abs()) * (m + 64) * ref.U32)
+    within(dw.t[to], exact_dw, off, f"dw {m} {n} {k}")
+    dx2, dw2 = torch.empty_like(dx.t), torch.empty_like(dw.t)
+    ptg.layer_cross_entropy_backward(x, w, label, lse[1: m + 1], scratch, plan, dx=dx2, dw=dw2)
+    torch.cuda.synchronize()
+    assert torch.equal(dx2, dx.t) and torch.equal(dw2, dw.t) and torch.isfinite(dx2).all() and torch.isfinite(dw2).all()
+
+
 # whole waves of 256 x 256 tiles and a split partial one; ragged edges; long k; several pieces
 LARGE = [(1000, 8200, 2056, 1), (520, 33032, 1032, 3), (2049, 4104, 520, 1), (260, 16392, 4104, 2)]
 
@@ -324,36 +366,13 @@ LARGE = [(1000, 8200, 2056, 1), (520, 33032, 1032, 3), (2049, 4104, 520, 1), (26
 @pytest.mark.parametrize("m,n,k,pieces", LARGE)
 def test_large(plan, m, n, k, pieces):
     say("cross entropy large", m, n, k)
-    x, w, label = head(m, n, k)
-    lse, loss = forward(plan, x, w, label)
-    dx, dw = Out(m, k, BF16), Out(n, k, F32)
-    scratch = torch.empty(ptg.layer_cross_entropy_scratch(m, n, k, pieces), dtype=torch.uint8, device="cuda")
-    ptg.layer_cross_entropy_backward(x, w, label, lse[1: m + 1], scratch, plan, dx=dx.t, dw=dw.t)
-    torch.cuda.synchronize()
-    dx.check()
-    dw.check()
-    at = torch.randperm(m, generator=torch.Generator().manual_seed(m))[:40].cuda()
-    at = torch.cat([at, torch.tensor([0, 255, 256, m - 1]).cuda()])
-    exact, bound = ref.cross_entropy(x[at], w, label[at]), ref.cross_entropy_bounds(x[at], w, label[at])
-    within(lse[1:-1][at], exact[0], bound[0], "lse")
-    within(loss[1:-1][at], exact[1], bound[1], "loss")
-    (want, off), _ = ref.cross_entropy_backward_bounds(x[at], w, label[at], lse[1:-1][at], BF16, F32)
-    within(dx.t[at], want, off, "dx")
-    to = torch.cat([torch.randperm(n, generator=torch.Generator().manual_seed(n))[:40], torch.tensor([0, 255, 256, n - 1])]).cuda()
-    # dw's rows: the same logits with the vocabulary cut to them (labels moved, or past: no entry of this row's)
-    z = ref.d(x) @ ref.d(w[to]).t()
-    p = torch.exp(z - ref.d(lse[1:-1])[:, None]) - (label.cpu()[:, None] == to.cpu()[None, :]).double()
-    p[label.cpu() < 0] = 0.0
-    t = ref._logits_error(x, w[to]) + 3 * ref.U32 * (z.abs() + ref.d(lse[1:-1]).abs()[:, None])
-    err = torch.exp(z - ref.d(lse[1:-1])[:, None]) * (torch.expm1(t) + 4 * ref.U32) + 2 * ref.U32
-    err = err + 2.0 ** -8 * (p.abs() + err) + 2.0 ** -126
-    exact_dw = p.t() @ ref.d(x)
-    within(dw.t[to], exact_dw, ref.rounded(exact_dw, F32, err.t() @ ref.d(x).abs() + (p.abs().t() @ ref.d(x).abs()) * (m + 64) * ref.U32), "dw")
-    again = forward(plan, x, w, label)
-    dx2, dw2 = torch.empty_like(dx.t), torch.empty_like(dw.t)
-    ptg.layer_cross_entropy_backward(x, w, label, lse[1: m + 1], scratch, plan, dx=dx2, dw=dw2)
-    torch.cuda.synchronize()
-    assert torch.equal(again[0], lse) and torch.equal(again[1], loss) and torch.equal(dx2, dx.t) and torch.equal(dw2, dw.t)
+    check_sampled(plan, m, n, k, pieces)
+
+
+@pytest.mark.parametrize("what,kind,m,n,k", [c for c in head_cases.CASES if c[1] != "i8"])
+def test_every_kernel(plan, what, kind, m, n, k):
+    say(what, kind, m, n, k)
+    check_sampled(plan, m, n, k, backward=kind != "loss")
 
 
 def test_refusals(plan):
