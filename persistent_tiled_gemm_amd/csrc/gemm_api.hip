@@ -307,7 +307,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
   args.ring_depth = p->desc.ring_depth;
   args.claim_lead = p->desc.claim_lead;
   args.claim_policy = p->desc.claim_policy;
-  args.raster_group = operands && operands->raster_group != 0 ? operands->raster_group : p->desc.raster == 1 ? p->desc.raster_group : 1;
+  args.raster_group = operands && ptg::form_is_super(form) ? operands->super_rows : p->desc.raster == 1 ? p->desc.raster_group : 1;
   args.k_rotation = resolve_k_rotation(p->desc.k_rotation, grouped, args.single.N, p->desc.bn);
   args.counter_base = 0;
   if (mode == GEMM_SCHED_DYNAMIC && p->preset_pending) {

@@ -334,7 +334,7 @@ template <bool BT_>
 struct PlainOp {
   struct Args {};
   static constexpr bool AT = false, BT = BT_, E8 = false, I8 = false, kPlain = true, kWide = false;
-  static constexpr bool kDirect = false;
+  static constexpr bool kDirect = false, kSuper = false;  // kSuper: tiles in the order of decode_super_tile
   template <int EDGE> using Tile = typename TileCfg<EDGE>::type;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &pb, const Args &) { return pb.K; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &pb, const Args &) { return BT_ ? pb.K : pb.N; }
@@ -508,7 +508,8 @@ __device__ __forceinline__ void gemm_body(const KernelArgs &args, const typename
       pb = args.single;
     }
     int32_t m_t, n_t;
-    decode_tile(local, pb.tiles_m, pb.tiles_n, args.raster_group, m_t, n_t);
+    if constexpr (OP::kSuper) decode_super_tile(local, pb.tiles_m, pb.tiles_n, args.raster_group, m_t, n_t);
+    else decode_tile(local, pb.tiles_m, pb.tiles_n, args.raster_group, m_t, n_t);
     const int32_t m0 = m_t * BM, n0 = n_t * BN;
     const int32_t M = pb.M, N = pb.N, K = pb.K;
 

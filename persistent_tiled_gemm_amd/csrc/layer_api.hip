@@ -152,7 +152,7 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const int64_t units = ptg::form_units(form), nk = ceil_div(a.k / units, 32), line = 32 * units;
   const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (!nn && a.ldb % line != 0));
   const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : nn ? 1.05 : 1.13) : 1.0;
-  const bool refill = form >= ptg::kFormNTI8;
+  const bool refill = ptg::form_is_super(form);
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
     const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
@@ -190,7 +190,7 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   return best;
 }
 
-// Rows of a super-tile (see decode_tile): 16 x 16 tiles, or as near as the product is wide.
+// Rows of a super-tile (see decode_super_tile): 16 x 16 tiles, or as near as the product is wide.
 int32_t super_rows(int64_t tiles_m, int64_t tiles_n) {
   int32_t r = 16;
   while (r > 1 && r > tiles_m) r /= 2;
@@ -200,7 +200,7 @@ int32_t super_rows(int64_t tiles_m, int64_t tiles_n) {
 }
 
 gemm_status run_choice(layer_plan *p, ptg::ProductArgs a, int form, const TileChoice &c, hipStream_t s) {
-  if (form >= ptg::kFormNTI8) a.raster_group = -super_rows(ceil_div(a.m, c.edge), ceil_div(a.n, c.edge));
+  if (ptg::form_is_super(form)) a.super_rows = super_rows(ceil_div(a.m, c.edge), ceil_div(a.n, c.edge));
   gemm_tile_cfg t = c.edge == 256 ? p->tiles256 : p->tiles128;
   gemm_status st = ptg::plan_run_product(t, a, form, c.split, c.base, s);
   if (st == GEMM_E_HIP) std::snprintf(p->last_error, sizeof(p->last_error), "%s", gemm_last_hip_error(t));

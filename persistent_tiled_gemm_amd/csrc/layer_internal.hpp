@@ -83,7 +83,7 @@ struct ProductArgs {
   int32_t m, n, k;
   EpilogueArgs ep;
   LossTerms loss;        // the loss forms', in the epilogue's place
-  int32_t raster_group;  // as KernelArgs' (0: the plan's)
+  int32_t super_rows;    // of forms in super-tiles
 };
 
 // Forms of a product, by operand layout and type.
@@ -98,6 +98,7 @@ enum ProductForm {
   kFormLoss = 7,      // kFormNT's sums as logits: each row's maximum and sum of exponentials by column blocks
   kFormLogitGrad = 8  // kFormNT's sums as logits: their gradient
 };
+constexpr bool form_is_super(int form) { return form >= kFormNTI8; }  // tiles in the order of decode_super_tile
 constexpr bool form_is_loss(int form) { return form == kFormLoss || form == kFormLogitGrad; }
 constexpr int64_t form_units(int form) { return form == kFormNTE4m3 || form == kFormNTI8 ? 2 : 1; }  // values per 16 bits along k
 // The factors that a form's epilogue takes: of each row and column, or one (at row_scale).
@@ -160,11 +161,11 @@ hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelAr
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,
                                  int32_t tiles, int32_t chunks, hipStream_t s);
-hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group, int32_t first,
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first,
                             int32_t tiles, int32_t chunks, hipStream_t s);
-hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows,
                                 int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
-hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t super_rows,
                               int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
 // Columns of a block that leaves one partial maximum and sum: the tiles' and the few-row kernel's.
 constexpr int32_t loss_block(int tile_edge) { return tile_edge / 2; }

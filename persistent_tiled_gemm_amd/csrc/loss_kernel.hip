@@ -50,7 +50,7 @@ __device__ __forceinline__ float times_factor(float factor, float v) { return fa
 template <int FORM>
 struct LossOp {
   using Args = ProductOpArgs;
-  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kDirect = true;
+  static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kDirect = true, kSuper = true;
   static constexpr bool kGrad = FORM == kFormLogitGrad;
   template <int EDGE> using Tile = ProductOp<kFormNT>::Tile<EDGE>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
@@ -250,14 +250,14 @@ __global__ __launch_bounds__(256, 1) void ptg_loss_kernel(const LossKernelArgs a
 struct LossChunksArgs {
   LossTerms loss;
   const float *ws;
-  int32_t m, n, tiles_m, tiles_n, raster_group, first, chunks;
+  int32_t m, n, tiles_m, tiles_n, super_rows, first, chunks;
 };
 template <int EDGE, int FORM>
 __global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksArgs a) {
   constexpr int LPR = EDGE / 8, kRows = 256 / LPR, kParts = EDGE / kRows, kLanes = LPR / 2;
   const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
   int32_t m_t, n_t;
-  decode_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
+  decode_super_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.super_rows, m_t, n_t);
   const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
   const bool in = m < a.m && n < a.n;  // (n is a multiple of 8 everywhere)
   f32x8 z = {};
@@ -364,9 +364,9 @@ static hipError_t reduce_edge(int form, const LossChunksArgs &a, int tiles, hipS
   return hipGetLastError();
 }
 
-hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t raster_group,
+hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t super_rows,
                               int32_t first, int32_t tiles, int32_t chunks, hipStream_t s) {
-  const LossChunksArgs a = {loss, ws, m, n, (m + tile_edge - 1) / tile_edge, (n + tile_edge - 1) / tile_edge, raster_group, first, chunks};
+  const LossChunksArgs a = {loss, ws, m, n, (m + tile_edge - 1) / tile_edge, (n + tile_edge - 1) / tile_edge, super_rows, first, chunks};
   return tile_edge == 256 ? reduce_edge<256>(form, a, tiles, s) : reduce_edge<128>(form, a, tiles, s);
 }
 

@@ -16,9 +16,9 @@ __global__ __launch_bounds__(256) void ptg_product_i8_reduce_kernel(const Reduce
   reduce_tiles<EDGE, kScalesRowCol, true, true>(a);
 }
 
-hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t raster_group, int32_t first, int32_t tiles, int32_t chunks,
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first, int32_t tiles, int32_t chunks,
                             hipStream_t s) {
-  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks, (m + tile_edge - 1) / tile_edge, raster_group};
+  const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks, (m + tile_edge - 1) / tile_edge, super_rows};
   if (tile_edge == 256) hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<256>, dim3(reduce_grid<256>(tiles)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<128>, dim3(reduce_grid<128>(tiles)), dim3(256), 0, s, a);
   return hipGetLastError();

@@ -125,7 +125,7 @@ struct ProductOp {
   static constexpr bool AT = FORM == kFormTN || FORM == kFormTNScaled, E8 = FORM == kFormNTE4m3, I8 = FORM == kFormNTI8;
   static constexpr bool BT = FORM == kFormNT || E8 || I8, kPlain = false, kWide = !AT;
   static constexpr int kScales = product_scales(FORM);
-  static constexpr bool kDirect = false;
+  static constexpr bool kDirect = false, kSuper = form_is_super(FORM);
   // 16 x 16 blocks for both tile edges: a k-step's fragments are read a whole step
   // ahead of their MFMAs (the 128 x 128 tile's other form, 32 x 32 blocks read half
   // a step ahead, measured 160 us against 152 on 1024 x 8192 x 8192). k-contiguous
@@ -216,7 +216,7 @@ struct ReduceArgs {
   EpilogueArgs ep;
   const float *ws;
   int32_t m, n, tiles_n, first, chunks;  // first: the first split tile
-  int32_t tiles_m, raster_group;
+  int32_t tiles_m, super_rows;
 };
 // Its grid: EDGE rows a tile, 256 / (EDGE / 8) a workgroup.
 template <int EDGE>
@@ -241,7 +241,7 @@ __device__ __forceinline__ void reduce_tiles(const ReduceArgs &a) {
   const uint32_t q = threadIdx.x % LPR, r = blockIdx.x % kParts * kRows + threadIdx.x / LPR, tile = blockIdx.x / kParts;
   const int32_t t = a.first + (int32_t)tile;
   int32_t m_t = t / a.tiles_n, n_t = t % a.tiles_n;
-  if constexpr (SUPER) decode_tile(t, a.tiles_m, a.tiles_n, a.raster_group, m_t, n_t);
+  if constexpr (SUPER) decode_super_tile(t, a.tiles_m, a.tiles_n, a.super_rows, m_t, n_t);
   const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
   if (m >= a.m || n >= a.n) return;
   const RowTerms row = row_terms<SCALES>(a.ep, m, n);

@@ -123,32 +123,12 @@ __device__ __forceinline__ uint32_t wave_uniform(uint32_t v) { return __builtin_
 
 // Tile id -> (m_t, n_t) inside one problem. Row-major, or grouped-M: groups of
 // `group` tile rows, column-major inside a group (so consecutive ids share B
-// column panels and a few A row panels). Or (group < 0) super-tiles of 256: -group =
-// R rows (a power of two) by 256 / R columns, column by column of them, each dealt to the
-// XCDs (which take ids in turn) as 8 blocks of about 8 x 4, so that the tiles an XCD runs at
-// one time share 12 operand panels through its L2. Super-tiles that the edges cut are
-// walked down their columns.
+// column panels and a few A row panels).
 __device__ __forceinline__ void decode_tile(int32_t t, int32_t tiles_m, int32_t tiles_n, int32_t group,
                                             int32_t &m_t, int32_t &n_t) {
-  if (group == 0 || group == 1) {
+  if (group <= 1) {
     m_t = t / tiles_n;
     n_t = t - m_t * tiles_n;
-    return;
-  }
-  if (group < 0) {
-    const int32_t R = -group, C = 256 / R;
-    const int32_t cb = t / (tiles_m * C);  // super-tile column
-    const int32_t u = t - cb * tiles_m * C, c0 = cb * C, cols = min(C, tiles_n - c0);
-    const int32_t rb = u / (R * cols), s = u - rb * R * cols, r0 = rb * R, rows = min(R, tiles_m - r0);
-    if (rows < R || cols < C) {
-      m_t = r0 + s % rows;
-      n_t = c0 + s / rows;
-      return;
-    }
-    const int32_t xr = R <= 8 ? 1 : R <= 64 ? R / 8 : 8, xc = kXcdRegions / xr, br = R / xr;  // blocks of XCDs, rows of one's
-    const int32_t x = s % kXcdRegions, j = s / kXcdRegions;
-    m_t = r0 + (x / xc) * br + j % br;
-    n_t = c0 + (x % xc) * (C / xc) + j / br;
     return;
   }
   const int32_t per_group = group * tiles_n;
@@ -159,6 +139,28 @@ __device__ __forceinline__ void decode_tile(int32_t t, int32_t tiles_m, int32_t 
   const int32_t r = t - g * per_group;
   m_t = first_m + r % gm;
   n_t = r / gm;
+}
+
+// Tile id -> (m_t, n_t) in super-tiles of 256: R rows (a power of two) by 256 / R columns,
+// column by column of them, each dealt to the XCDs (which take ids in turn) as 8 blocks of
+// about 8 x 4, so that the tiles an XCD runs at one time share 12 operand panels through its
+// L2 (column by column, four rows of tiles are 33 panels: the loss of 1000 x 50264 x 2056
+// took 238 us, and 203 in this order). Super-tiles that the edges cut are walked down their
+// columns.
+__device__ __forceinline__ void decode_super_tile(int32_t t, int32_t tiles_m, int32_t tiles_n, int32_t R, int32_t &m_t, int32_t &n_t) {
+  const int32_t C = 256 / R;
+  const int32_t cb = t / (tiles_m * C);  // super-tile column
+  const int32_t u = t - cb * tiles_m * C, c0 = cb * C, cols = min(C, tiles_n - c0);
+  const int32_t rb = u / (R * cols), s = u - rb * R * cols, r0 = rb * R, rows = min(R, tiles_m - r0);
+  if (rows < R || cols < C) {
+    m_t = r0 + s % rows;
+    n_t = c0 + s / rows;
+    return;
+  }
+  const int32_t xr = R <= 8 ? 1 : R <= 64 ? R / 8 : 8, xc = kXcdRegions / xr, br = R / xr;  // blocks of XCDs, rows of one's
+  const int32_t x = s % kXcdRegions, j = s / kXcdRegions;
+  m_t = r0 + (x / xc) * br + j % br;
+  n_t = c0 + (x % xc) * (C / xc) + j / br;
 }
 
 // Which entry of a grouped launch's table owns work unit u: the last entry

@@ -67,15 +67,15 @@ def test_super_tiles_visit_every_tile_once(tmp_path):
 
     csrc = os.path.join(hip_stand_in.ROOT, "persistent_tiled_gemm_amd", "csrc")
     text = open(os.path.join(csrc, "ptg_device.hpp")).read()
-    body = re.search(r"__device__ __forceinline__ void decode_tile\(.*?\n}\n", text, re.S).group(0)
+    body = re.search(r"__device__ __forceinline__ void decode_super_tile\(.*?\n}\n", text, re.S).group(0)
     src = tmp_path / "decode.cpp"
     src.write_text("#include <stdint.h>\n#include <algorithm>\nusing std::min;\nstatic constexpr int kXcdRegions = 8;\n"
                    + body.replace("__device__ __forceinline__", "static")
-                   + '\nextern "C" int at(int t, int tm, int tn, int g) { int m, n; decode_tile(t, tm, tn, g, m, n); return m * 100000 + n; }\n')
+                   + '\nextern "C" int at(int t, int tm, int tn, int g) { int m, n; decode_super_tile(t, tm, tn, g, m, n); return m * 100000 + n; }\n')
     subprocess.run(["g++", "-O2", "-shared", "-fPIC", str(src), "-o", str(tmp_path / "decode.so")], check=True)
     at = ctypes.CDLL(str(tmp_path / "decode.so")).at
     for tm in (1, 2, 3, 7, 8, 9, 16, 17, 33, 64):
         for tn in (1, 2, 5, 8, 16, 17, 40, 130, 257):
-            for g in (0, 1, 8, 32, -1, -2, -4, -8, -16, -32, -64, -128, -256):
+            for g in (1, 2, 4, 8, 16, 32, 64, 128, 256):
                 seen = {at(t, tm, tn, g) for t in range(tm * tn)}
                 assert seen == {m * 100000 + n for m in range(tm) for n in range(tn)}, (tm, tn, g)
