@@ -4,8 +4,8 @@
  * product with bias, activation and residual in its epilogue, and the
  * gradients of both. Together they are a pre-norm feed-forward layer:
  *
- *   layer_rmsnorm              s = x + residual, y = s / rms(s) * weight, bf16, fp32 or
- *                              e4m3 with one scale a row (the next product's operand)
+ *   layer_rmsnorm              s = x + residual, y = s / rms(s) * weight, bf16, fp32, or e4m3
+ *                              or int8 with one scale a row (the next product's operand)
  *   layer_linear               out = act(x . w^T + bias) + residual
  *   layer_activation_backward  dpre = dout * act'(pre), dbias
  *   layer_linear_backward      dx = dpre . w, dw = dpre^T . x
@@ -122,10 +122,11 @@ const char *layer_last_hip_error(layer_cfg cfg);
  * kept) receives it rounded to `type`, and may be x or residual itself (same
  * pointer and stride: the residual stream updated in place).
  *
- * out_type LAYER_E4M3: `scale` receives one fp32 value a row, max_j |y_j| / 448
- * (at least 2^-126; 1 where the row's y is all zeros), and out the codes
- * y_j / scale (the fp32 quotient, rounded to nearest). The scale's reader multiplies: y is about code * scale. A row
- * whose y holds a NaN or an infinity gets a NaN scale and NaN codes. scale must
+ * out_type LAYER_E4M3 or LAYER_I8: `scale` receives one fp32 value a row,
+ * max_j |y_j| / 448 or / 127 (at least 2^-126; 1 where the row's y is all
+ * zeros), and out the codes y_j / scale (the fp32 quotient, rounded to nearest).
+ * The scale's reader multiplies: y is about code * scale. A row whose y holds a
+ * NaN or an infinity gets a NaN scale and NaN codes (int8: zeros). scale must
  * be NULL for the other types.
  *
  * Squares are summed in fp32: a row whose sum of squares passes 3.4e38
@@ -143,12 +144,12 @@ typedef struct layer_rmsnorm_args {
   const void *weight;   /* n, weight_type, or NULL */
   void *sum_out;        /* m x n, type, or NULL */
   void *out;            /* m x n, out_type */
-  float *scale;         /* m, e4m3 outputs only */
+  float *scale;         /* m, e4m3 and int8 outputs only */
   int64_t m, n;
   int64_t ldx, ldr, lds, ldo;
   int32_t type;         /* LAYER_F32 or LAYER_BF16: x, residual, sum_out */
   int32_t weight_type;
-  int32_t out_type;     /* LAYER_F32, LAYER_BF16 or LAYER_E4M3 */
+  int32_t out_type;     /* LAYER_F32, LAYER_BF16, LAYER_E4M3 or LAYER_I8 */
   float eps;
 } layer_rmsnorm_args;
 

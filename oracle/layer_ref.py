@@ -94,6 +94,12 @@ def rounded(exact, dtype, err):
     return err + HALF_STEP[dtype] * (exact.abs() + err) + TINY[dtype]
 
 
+def rmsnorm_codes_bound(v):
+    """Of int8 codes against the unrounded quotients v: half a code, and the quotient's own error. The root is in
+    both of its parts and cancels; left are the sum s (in both), two products in each, two divisions: 8 roundings."""
+    return 0.5 + 10 * U32 * v.abs()
+
+
 def rmsnorm_bound(y, dtype, n):
     # the sum of squares: terms and a chain of at most 64 additions a thread, then the tree; its root halves
     # that; then a handful of products

@@ -309,14 +309,15 @@ const char *layer_last_hip_error(layer_cfg p) { return p ? p->last_error : ""; }
 
 gemm_status layer_rmsnorm(const layer_rmsnorm_args *a, void *stream) {
   if (!a) return GEMM_E_INVALID_ARG;
-  if (!stream_type(a->type) || (a->out_type != LAYER_E4M3 && !stream_type(a->out_type)) ||
-      (a->weight && !stream_type(a->weight_type)) || !(a->eps >= 0.0f))
+  const bool codes = a->out_type == LAYER_E4M3 || a->out_type == LAYER_I8;
+  if (!stream_type(a->type) || (!codes && !stream_type(a->out_type)) || (a->weight && !stream_type(a->weight_type)) ||
+      !(a->eps >= 0.0f))
     return GEMM_E_INVALID_ARG;
   if (bad_size(a->m, a->n, 8) || a->n > LAYER_MAX_NORM_COLS || bad_stride(a->ldx, a->m, a->n, 8) ||
       (a->residual && bad_stride(a->ldr, a->m, a->n, 8)) || (a->sum_out && bad_stride(a->lds, a->m, a->n, 8)) ||
       bad_stride(a->ldo, a->m, a->n, 8))
     return GEMM_E_SHAPE;
-  if ((a->out_type == LAYER_E4M3) != (a->scale != nullptr) && (a->m > 0 || a->scale)) return GEMM_E_INVALID_ARG;
+  if (codes != (a->scale != nullptr) && (a->m > 0 || a->scale)) return GEMM_E_INVALID_ARG;
   if (a->m == 0 || a->n == 0) return GEMM_OK;
   if (!a->x || !a->out || !aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->sum_out) ||
       !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->scale) & 3u))

@@ -100,6 +100,28 @@ template <> __device__ __forceinline__ void store8_nt<e4m3_t>(e4m3_t *p, const f
   __builtin_nontemporal_store(w, (i32x2 *)p);
 }
 
+// Eight quotients as 8-bit codes, rounded to nearest, ties to even; int8 codes of a row whose
+// scale is NaN (`bad`) are zeros.
+struct i8_t { int8_t v; };
+template <typename TO> inline constexpr float kTop = 127.0f;  // what a row's largest value becomes
+template <> inline constexpr float kTop<e4m3_t> = kE4m3Max;
+__device__ __forceinline__ void store_codes(e4m3_t *p, const f32x8 &v, bool) { store8_nt(p, v); }
+__device__ __forceinline__ void store_codes(i8_t *p, const f32x8 &v, bool bad) {
+  // added to 1.5 2^23, a quotient is rounded to an integer in the sum's low bits
+  typedef __attribute__((ext_vector_type(2))) int i32x2;
+  uint32_t b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = bad ? 0u : __float_as_uint(v[e] + 12582912.0f);
+  i32x2 w;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000c0cu);
+    w[h] = (int)(lo | hi);
+  }
+  __builtin_nontemporal_store(w, (i32x2 *)p);
+}
+
 // e^(-z^2 / 2), with the square's rounding in the second part.
 __device__ __forceinline__ float exp_half_square(float z) {
   const float s = z * z, h = s * (-0.5f * kLog2e);

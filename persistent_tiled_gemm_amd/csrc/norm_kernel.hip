@@ -22,14 +22,14 @@ static NormShape norm_shape(int32_t n) {
   return {t, per <= 1 ? 1 : per <= 2 ? 2 : 4};
 }
 
-// Forward. The largest |y| of an e4m3 row is r max |s weight|, so the sum of
+// Forward. The largest |y| of an e4m3 or int8 row is r max |s weight|, so the sum of
 // squares and that maximum come from one reduction. |s weight| is compared as
 // bit patterns: they order like the values, and a NaN's are the largest, so a
 // NaN reaches the scale instead of being skipped.
 template <int T, int NCH, typename TS, typename TO>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const NormArgs a, int32_t groups) {
+__device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, int32_t groups) {
   constexpr int kGroups = T < 256 ? 256 / T : 1;
-  constexpr bool E8 = std::is_same<TO, e4m3_t>::value;
+  constexpr bool E8 = std::is_same<TO, e4m3_t>::value || std::is_same<TO, i8_t>::value;  // codes with a scale a row
   __shared__ float lds_sum[2][16];
   __shared__ uint32_t lds_top[2][16];
   const int32_t t = (int32_t)threadIdx.x % T;
@@ -106,11 +106,13 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const No
     }
     const float r = 1.0f / sqrtf(sum / (float)a.n + a.eps);
     float lift = 1.0f, lifted = 1.0f, inv_lifted = 1.0f;
+    bool bad = false;
     if constexpr (E8) {
       // the floor keeps 1 / scale finite (r / scale need not be: y is formed first)
       const float amax = __uint_as_float(top) * r;
-      float scale = amax == 0.0f ? 1.0f : fmaxf(amax / kE4m3Max, 0x1p-126f);
-      if (!(amax < INFINITY)) scale = __uint_as_float(0x7fc00000u);  // NaN or infinity in y
+      float scale = amax == 0.0f ? 1.0f : fmaxf(amax / kTop<TO>, 0x1p-126f);
+      bad = !(amax < INFINITY);
+      if (bad) scale = __uint_as_float(0x7fc00000u);  // NaN or infinity in y
       if (t == 0) a.scale[row] = scale;
       if (scale < 0x1p-60f) lift = 0x1p64f;  // the quotient's remainder stays above the subnormal numbers
       lifted = scale * lift;
@@ -133,10 +135,19 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const No
             y[e] = fmaf(fmaf(-q, lifted, y[e]), inv_lifted, q);
           }
         }
-        store8_nt(out + j, y);
+        if constexpr (E8) store_codes(out + j, y, bad);
+        else store8_nt(out + j, y);
       }
     }
   }
+}
+template <int T, int NCH, typename TS, typename TO>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_rmsnorm_kernel(const NormArgs a, int32_t groups) {
+  rmsnorm_rows<T, NCH, TS, TO>(a, groups);
+}
+template <int T, int NCH, typename TS>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_norm_i8_kernel(const NormArgs a, int32_t groups) {
+  rmsnorm_rows<T, NCH, TS, i8_t>(a, groups);
 }
 
 // Gradient. Row groups stride over the rows; a thread's columns are the same
@@ -319,6 +330,7 @@ static void rmsnorm_out(const NormArgs &a, int groups, hipStream_t s) {
   const dim3 grid((uint32_t)((groups + per - 1) / per)), block(T < 256 ? 256 : T);
   if (a.out_type == kTypeF32) hipLaunchKernelGGL((ptg_rmsnorm_kernel<T, NCH, TS, float>), grid, block, 0, s, a, groups);
   else if (a.out_type == kTypeBf16) hipLaunchKernelGGL((ptg_rmsnorm_kernel<T, NCH, TS, __bf16>), grid, block, 0, s, a, groups);
+  else if (a.out_type == kTypeI8) hipLaunchKernelGGL((ptg_norm_i8_kernel<T, NCH, TS>), grid, block, 0, s, a, groups);
   else hipLaunchKernelGGL((ptg_rmsnorm_kernel<T, NCH, TS, e4m3_t>), grid, block, 0, s, a, groups);
 }
 

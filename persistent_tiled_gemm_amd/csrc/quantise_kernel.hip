@@ -10,11 +10,6 @@
 
 namespace ptg {
 
-struct i8_t { int8_t v; };
-
-template <typename TO> static constexpr float kTop = 127.0f;
-template <> constexpr float kTop<e4m3_t> = kE4m3Max;
-
 // A row's scale and what its quotients are formed with. |x| is compared as bit patterns,
 // which order like the values, a NaN's above all: a NaN or infinity gives the scale NaN.
 // The quotient x / scale is the product with the reciprocal, put right by its remainder:
@@ -36,31 +31,14 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   r.inv = 1.0f / r.lifted;
   return r;
 }
-template <typename TO>
-__device__ __forceinline__ void store_codes(TO *out, f32x8 v, const RowScale &r) {
+__device__ __forceinline__ f32x8 quotients(f32x8 v, const RowScale &r) {
   v *= r.lift;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float q = v[e] * r.inv;
     v[e] = fmaf(-fmaf(q, r.lifted, -v[e]), r.inv, q);  // (this way round, -0 keeps its sign)
   }
-  if constexpr (std::is_same<TO, e4m3_t>::value) {
-    store8_nt(out, v);
-  } else {
-    // added to 1.5 2^23, a quotient is rounded to an integer in the sum's low bits
-    typedef __attribute__((ext_vector_type(2))) int i32x2;
-    uint32_t b[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = r.bad ? 0u : __float_as_uint(v[e] + 12582912.0f);
-    i32x2 w;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
-      const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000c0cu);
-      w[h] = (int)(lo | hi);
-    }
-    __builtin_nontemporal_store(w, (i32x2 *)out);
-  }
+  return v;
 }
 
 // The largest |v| of the row group's threads (T a wave, or all of a workgroup).
@@ -116,7 +94,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ptg_quantise_kernel(const Q
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int32_t j = (c * T + t) * 8;
-      if (j < a.n) store_codes(out + j, widen(mine.x[c]), r);
+      if (j < a.n) store_codes(out + j, quotients(widen(mine.x[c]), r), r.bad);
     }
   }
 }
@@ -134,7 +112,7 @@ __global__ __launch_bounds__(1024) void ptg_quantise_long_kernel(const QuantiseA
     const RowScale r = row_scale<TO>(group_top<1024>(top, lds[buf]));
     if (threadIdx.x == 0) a.scale[row] = r.scale;
 #pragma unroll 4
-    for (int32_t j = (int32_t)threadIdx.x * 8; j < a.n; j += 8192) store_codes(out + j, load8(x + j), r);
+    for (int32_t j = (int32_t)threadIdx.x * 8; j < a.n; j += 8192) store_codes(out + j, quotients(load8(x + j), r), r.bad);
   }
 }
 

@@ -242,14 +242,14 @@ def _activation(name) -> int:
 
 
 _STREAM = (LAYER_F32, LAYER_BF16)
-_ANY = (LAYER_F32, LAYER_BF16, LAYER_E4M3)
-_ONLY = {c: (c,) for c in (*_ANY, LAYER_I8)}  # the types allowed beside one that is given
+_ANY = (LAYER_F32, LAYER_BF16, LAYER_E4M3, LAYER_I8)
+_ONLY = {c: (c,) for c in _ANY}  # the types allowed beside one that is given
 
 
 def layer_rmsnorm(x, weight, out, *, residual=None, sum_out=None, scale=None, eps: float = 1e-6, stream=None) -> None:
     """layer_rmsnorm: out = s / sqrt(mean(s^2) + eps) * weight per row, s = x + residual (kept in sum_out, which
     may be x or residual). x, residual, sum_out: one dtype, bf16 or fp32. weight: bf16 or fp32, or None. out: fp32,
-    bf16, or float8_e4m3fn with `scale` (fp32, one value a row): s's norm is then about out * scale[:, None]."""
+    bf16, or float8_e4m3fn or int8 with `scale` (fp32, one value a row): s's norm is then about out * scale[:, None]."""
     shape, at = _first("x", x)
     m, n = shape
     px, ldx, ty = _matrix("x", x, shape, at, _STREAM)

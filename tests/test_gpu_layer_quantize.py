@@ -5,7 +5,7 @@ import torch
 
 import persistent_tiled_gemm_amd as ptg
 from oracle import layer_ref as ref
-from tests.layer_util import Out, normal, say
+from tests.layer_util import Out, normal, say, within
 
 pytestmark = pytest.mark.gpu
 
@@ -73,6 +73,58 @@ def test_empty_tiny_huge_and_non_finite_rows(dtype, t, n):
     x[9] = -0.0
     x[10] = 2.5
     check(x.to(t), dtype)
+
+
+def check_norm(x, residual=None, weight=None, sum_out=False):
+    m, n = x.shape
+    out, scale = Out(m, n, I8), torch.full((m,), -1.0, device="cuda")
+    kept = Out(m, n, x.dtype) if sum_out else None
+    ptg.layer_rmsnorm(x, weight, out.t, residual=residual, sum_out=kept.t if sum_out else None, scale=scale)
+    torch.cuda.synchronize()
+    out.check()
+    s, y = ref.rmsnorm(x, weight, residual)
+    top = y.abs().amax(dim=1)
+    want = torch.where(top == 0, torch.ones_like(top), (top / 127).clamp(min=2.0 ** -126))
+    within(scale, want, want * 100 * ref.U32, "scale")
+    v = y / want[:, None]
+    within(out.t.float(), v, ref.rmsnorm_codes_bound(v), "codes")
+    assert ((out.t.int().abs().amax(dim=1) == 127) | (scale == 1)).all()
+    if sum_out:
+        within(kept.t, s, ref.rounded(s, x.dtype, s.abs() * 2 * ref.U32), "sum")
+        kept.check()
+
+
+# the norm's row groups: their sizes change at n = 2048 and 8192, chunks per thread in between
+@pytest.mark.parametrize("m,n", [(1, 8), (3, 64), (5, 512), (7, 520), (4, 2048), (9, 2056), (2, 4096), (3, 5000), (1, 8192), (6, 8200), (2, 16384),
+                                 (2, 32768), (700, 1032)])
+@pytest.mark.parametrize("t", [BF16, F32])
+def test_norm_to_int8(m, n, t):
+    say("norm to int8", m, n, t)
+    w = (1 + 0.2 * normal(3, n, dtype=F32)).to(BF16)
+    check_norm(normal(1, m, n, scale=3.0, dtype=t, pad=8), normal(2, m, n, dtype=t), w, True)
+    check_norm(normal(1, m, n, scale=1e-3, dtype=t))
+
+
+def test_norm_to_int8_of_zeros_and_non_finite_rows():
+    x = normal(1, 5, 264, dtype=F32)
+    x[1] = 0.0
+    x[2, 7] = float("nan")
+    x[3, 8] = float("inf")
+    out, scale = torch.empty(5, 264, dtype=I8, device="cuda"), torch.empty(5, device="cuda")
+    ptg.layer_rmsnorm(x, None, out, scale=scale)
+    torch.cuda.synchronize()
+    assert scale[1] == 1.0 and torch.isnan(scale[2:4]).all() and torch.isfinite(scale[[0, 1, 4]]).all()
+    assert (out[1:4] == 0).all() and (out[[0, 4]].int().abs().amax(dim=1) == 127).all()
+
+
+def test_norm_to_int8_refuses():
+    x, out = normal(1, 4, 64), torch.empty(4, 64, dtype=I8, device="cuda")
+    with pytest.raises(ptg.PtgError) as e:
+        ptg.layer_rmsnorm(x, None, out)  # no scale
+    assert e.value.status == -1
+    with pytest.raises(ptg.PtgError) as e:
+        ptg.layer_rmsnorm(x, None, torch.empty_like(x), scale=torch.empty(4, device="cuda"))
+    assert e.value.status == -1
 
 
 def test_nothing_writes_nothing():

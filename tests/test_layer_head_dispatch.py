@@ -51,6 +51,9 @@ for n in (8, 520, 1032, 2056, 4104, 8200, 16392, 32776):
         for o in (2, 3):
             a = layer.QuantizeArgs(x=P, out=P, scale=P, m=4, n=n, ldx=n, ldo=n, type=t, out_type=o)
             assert lib.layer_quantize(ctypes.byref(a), None) == 0
+        if n <= 32768:
+            a = layer.RmsnormArgs(x=P, out=P, scale=P, m=4, n=n, ldx=n, ldo=n, type=t, out_type=3, eps=1e-6)
+            assert lib.layer_rmsnorm(ctypes.byref(a), None) == 0
 seen |= {{line.split()[0] for line in hip.stand_in_launches().decode().splitlines()}}
 result = dict(seen=sorted(seen), kernels=hip.stand_in_kernels().decode().split())
 """)
