@@ -1,6 +1,6 @@
-"""A pre-norm feed-forward layer out of the layer operators, trained a few steps in bf16 and then served in e4m3.
+"""A pre-norm feed-forward layer out of the layer operators, trained a few steps in bf16 and then served in 8 bits.
 
-    python examples/feed_forward.py [--tokens 512] [--hidden 1024] [--inner 4096] [--steps 20]
+    python examples/feed_forward.py [--tokens 512] [--hidden 1024] [--inner 4096] [--steps 20] [--serve e4m3|int8]
 
 Training (bf16, fp32 gradients and master weights):
 
@@ -9,8 +9,8 @@ Training (bf16, fp32 gradients and master weights):
     y    = a w2^T + s                  layer_linear, the residual stream in its epilogue
 
 and back through layer_linear_backward, layer_activation_backward and layer_rmsnorm_backward, which joins the stream's own
-gradient. Serving: the same layer with both weights quantised once to e4m3 rows; the norm writes the first product's operand
-and its row scales itself. Needs an MI355X.
+gradient. Serving: the same layer with both weights quantised once to e4m3 or int8 rows (layer_quantize); the norm writes the
+first product's operand and its row scales itself, layer_quantize the second's. Needs an MI355X.
 """
 
 from __future__ import annotations
@@ -23,8 +23,6 @@ import sys
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
-
-E4M3_MAX = 448.0
 
 
 class FeedForward:
@@ -85,19 +83,20 @@ class FeedForward:
 
 
 class Served:
-    """The layer with e4m3 weights, for one step's tokens."""
+    """The layer with 8-bit weights (e4m3 or int8), for one step's tokens."""
 
-    def __init__(self, trained: FeedForward, tokens: int):
+    def __init__(self, trained: FeedForward, tokens: int, dtype=None):
         torch = trained.torch
-        self.ptg, self.torch, self.plan, self.eps, self.w = trained.ptg, torch, trained.plan, trained.eps, trained.bf16
+        dtype = dtype or torch.float8_e4m3fn
+        self.ptg, self.plan, self.eps, self.w = trained.ptg, trained.plan, trained.eps, trained.bf16
         self.q = {}
         for name in ("w1", "w2"):  # laid out once
             w = trained.master[name]
-            scale = w.abs().amax(dim=1) / E4M3_MAX
-            self.q[name] = ((w / scale[:, None]).to(torch.float8_e4m3fn), scale)
+            self.q[name] = torch.empty_like(w, dtype=dtype), torch.empty(w.shape[0], device="cuda")
+            self.ptg.layer_quantize(w, *self.q[name])
         hidden, inner = self.w["w2"].shape
-        self.h8 = torch.empty(tokens, hidden, dtype=torch.float8_e4m3fn, device="cuda")
-        self.a8 = torch.empty(tokens, inner, dtype=torch.float8_e4m3fn, device="cuda")
+        self.h8 = torch.empty(tokens, hidden, dtype=dtype, device="cuda")
+        self.a8 = torch.empty(tokens, inner, dtype=dtype, device="cuda")
         self.h_scale, self.a_scale = torch.empty(tokens, device="cuda"), torch.empty(tokens, device="cuda")
         self.a = torch.empty(tokens, inner, dtype=torch.bfloat16, device="cuda")
 
@@ -107,10 +106,7 @@ class Served:
         p.layer_rmsnorm(x, w["gain"], self.h8, residual=residual, sum_out=residual, scale=self.h_scale, eps=self.eps)
         (w1, s1), (w2, s2) = self.q["w1"], self.q["w2"]
         p.layer_linear(self.h8, w1, self.a, self.plan, bias=w["b1"], activation="gelu_tanh", x_scale=self.h_scale, w_scale=s1)
-        # the second product's operand: e4m3 rows of the activations
-        amax = self.a.float().abs().amax(dim=1)
-        self.a_scale.copy_(self.torch.where(amax == 0, self.torch.ones_like(amax), amax / E4M3_MAX))
-        self.a8.copy_(self.a.float() / self.a_scale[:, None])
+        p.layer_quantize(self.a, self.a8, self.a_scale)
         p.layer_linear(self.a8, w2, out, self.plan, residual=residual, x_scale=self.a_scale, w_scale=s2)
         return out
 
@@ -121,6 +117,7 @@ def main(argv=None):
     ap.add_argument("--hidden", type=int, default=1024)
     ap.add_argument("--inner", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--serve", choices=("e4m3", "int8"), default="e4m3")
     a = ap.parse_args(argv)
     import torch
 
@@ -137,13 +134,13 @@ def main(argv=None):
     layer.ptg.layer_sync(layer.plan)
     print(f"training: mean squared error {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps")
 
-    served = Served(layer, 4)
+    served = Served(layer, 4, torch.int8 if a.serve == "int8" else torch.float8_e4m3fn)
     want = layer.forward(x, residual)[:4].float()
     out = torch.empty(4, a.hidden, dtype=torch.bfloat16, device="cuda")
     got = served.step(x[:4], residual[:4].clone(), out).float()
     layer.ptg.layer_sync(layer.plan)
     off = ((got - want).norm() / want.norm()).item()
-    print(f"serving in e4m3: {off:.4f} off the bf16 layer (2-norm, relative)")
+    print(f"serving in {a.serve}: {off:.4f} off the bf16 layer (2-norm, relative)")
     return losses, off
 
 
