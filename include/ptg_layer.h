@@ -21,6 +21,8 @@
  * dense; a weight is n x k as a linear layer keeps it. Device pointers only,
  * 16-byte aligned. Row lengths and strides are multiples of 8 elements (16 for
  * e4m3 and int8 operands of a product); the number of rows m is arbitrary, 0 included.
+ * Outputs and scratch share no memory with inputs or each other but where a function
+ * says so.
  * A stride is at least the row's length; with m <= 1, or rows of no elements, it is
  * not looked at.
  *
@@ -294,16 +296,18 @@ gemm_status layer_quantize(const layer_quantize_args *args, void *stream);
 
 /*
  * Softmax cross entropy of an output head, without its logits: with z = x . w^T
- * (m tokens, n entries of the vocabulary),
+ * (m tokens, n entries of the vocabulary, any number of them),
  *   lse_m = log sum_v exp z_mv,  loss_m = lse_m - z_m,label.
  * A negative label: the row is not counted, its loss is 0 (its lse is written all
  * the same). A label of n or more is a mistake that no call can see in time: its
  * loss is NaN, and so are its gradients. Logits, maxima and sums are fp32; they
  * are taken tile by tile, 8 bytes a row and block of the vocabulary reach memory.
- * loss may be NULL. lse holds other values while the call runs. A logit of NaN
+ * loss may be NULL. lse holds other values while the call runs and shares no memory with
+ * loss. A logit of NaN
  * gives the row NaN; w rows of -infinity work where the logit is -infinity.
- * Two launches (more where a workspace of 8 bytes a row and 64 entries does not
- * hold all rows). m == 0 enqueues nothing.
+ * Two launches, three where products are split along k (and in parts of the rows where the
+ * workspace does not hold 8 bytes a row and 128 entries for all of them). m == 0
+ * enqueues nothing.
  * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, loss and lse the same),
  * GEMM_E_SHAPE (also n == 0 with rows), GEMM_E_DEVICE, GEMM_E_HIP.
  */
@@ -331,8 +335,8 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *args, layer_cfg 
  * finite values there all the same (0 times NaN is NaN in dw).
  *
  * scratch: dz is made and used in pieces of the vocabulary, whole 256s of its
- * entries, as large as scratch_bytes allow: 2 m bytes an entry and, with more than
- * one piece and a bf16 dx, 4 m k bytes before them for dx's sum.
+ * entries, as large as scratch_bytes allow: 2 m bytes an entry (of whole 8s) and, with more
+ * than one piece and a bf16 dx, 4 m k bytes before them for dx's sum.
  * layer_cross_entropy_scratch gives the bytes for (at most) `pieces` pieces; the
  * fewer, the faster: each costs dx's sum once through memory. It is at the call's
  * disposal while the call runs, and any two calls may share it in turn.

@@ -586,7 +586,7 @@ gemm_status layer_quantize(const layer_quantize_args *a, void *stream) {
 
 gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, void *stream) {
   if (!a || !p) return GEMM_E_INVALID_ARG;
-  if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
+  if (bad_size(a->m, a->n, 1) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
       (a->m > 0 && a->n == 0))
     return GEMM_E_SHAPE;
   if (!aligned16(a->x) || !aligned16(a->w) || (reinterpret_cast<uintptr_t>(a->label) & 7u) || (reinterpret_cast<uintptr_t>(a->lse) & 3u) ||
@@ -647,9 +647,9 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, 
 }
 
 int64_t layer_cross_entropy_scratch(int64_t m, int64_t n, int64_t k, int32_t pieces) {
-  if (bad_size(m, n, 8) || bad_size(m, k, 8) || pieces < 1) return -1;
+  if (bad_size(m, n, 1) || bad_size(m, k, 8) || pieces < 1) return -1;
   // pieces of whole 256s of the vocabulary: no more of them than asked for
-  const int64_t piece = std::min(ceil_div(ceil_div(n, pieces), 256) * 256, n);
+  const int64_t piece = std::min(ceil_div(ceil_div(n, pieces), 256) * 256, ceil_div(n, 8) * 8);
   return 2 * m * piece + (piece < n ? 4 * m * k : 0);
 }
 
@@ -657,7 +657,7 @@ gemm_status layer_cross_entropy_backward(const layer_cross_entropy_grad_args *a,
   if (!a || !p) return GEMM_E_INVALID_ARG;
   if ((a->dx && !stream_type(a->dx_type)) || (a->dw && !stream_type(a->dw_type)) || a->accumulate < 0 || a->accumulate > 1)
     return GEMM_E_INVALID_ARG;
-  if (bad_size(a->m, a->n, 8) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
+  if (bad_size(a->m, a->n, 1) || bad_size(a->n, a->k, 8) || bad_stride(a->ldx, a->m, a->k, 8) || bad_stride(a->ldw, a->n, a->k, 8) ||
       (a->dx && bad_stride(a->lddx, a->m, a->k, 8)) || (a->dw && bad_stride(a->lddw, a->n, a->k, 8)) || (a->m > 0 && a->n == 0) ||
       a->scratch_bytes < 0)
     return GEMM_E_SHAPE;
@@ -672,8 +672,9 @@ gemm_status layer_cross_entropy_backward(const layer_cross_entropy_grad_args *a,
   if (st != GEMM_OK || (!any_dx && !any_dw)) return st;
   // The piece: as many whole 256s of the vocabulary as the scratch holds. With more than
   // one, dx is added up in fp32: in dx itself, or before the pieces in the scratch.
-  const int64_t all = 2 * a->m * a->n;
-  int64_t piece = a->n, sums = 0;
+  // dz's rows are of whole 8s; what is past the vocabulary is 0 there.
+  int64_t piece = ceil_div(a->n, 8) * 8, sums = 0;
+  const int64_t all = 2 * a->m * piece;
   if (a->m > 0 && a->scratch_bytes < all) {
     sums = any_dx && a->dx_type == LAYER_BF16 ? 4 * a->m * a->k : 0;
     piece = (a->scratch_bytes - sums) / (2 * a->m) / 256 * 256;
@@ -682,7 +683,6 @@ gemm_status layer_cross_entropy_backward(const layer_cross_entropy_grad_args *a,
   hipStream_t s = static_cast<hipStream_t>(stream);
   st = order_after_last_stream(p, s);
   if (st != GEMM_OK) return st;
-  if (a->m == 0) piece = a->n;  // dw = 0, in one go
   uint16_t *dz = a->m > 0 ? reinterpret_cast<uint16_t *>(static_cast<unsigned char *>(a->scratch) + sums) : nullptr;
   const int64_t ldx = stride_of(a->ldx, a->m, a->k), ldw = stride_of(a->ldw, a->n, a->k);
   const int64_t lddx = stride_of(a->lddx, a->m, a->k), lddw = stride_of(a->lddw, a->n, a->k);

@@ -85,23 +85,32 @@ struct LossOp {
     static_assert(CF::MB == 16 && CF::WN == loss_block(CF::BN_) && CF::NI % 2 == 0, "blocks");
     if (n_base >= N) return;  // a block past the vocabulary
     asm volatile("" : "+v"(lane));
+    if (n_base + CF::WN > N) {  // columns past the vocabulary: exp(-infinity) has no part, and dz is 0 there
+      int32_t left = N - n_base - (int32_t)(4u * (lane >> 4));
+#pragma unroll
+      for (int mi = 0; mi < CF::MI; ++mi) {
+#pragma unroll
+        for (int ni = 0; ni < CF::NI; ++ni) {
+          asm volatile("" : "+a"(acc[mi][ni]), "+v"(left));  // (no masks kept from block to block)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[mi][ni][e] = 16 * ni + e < left ? acc[mi][ni][e] : -INFINITY;
+          asm volatile("" : "+a"(acc[mi][ni]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     if constexpr (kGrad) grad<CF>(acc, rows, lane, m_base, n_base, M, N);
-    else stats<CF>(acc, rows, lane, m_base, n_base, M, N);
+    else stats<CF>(acc, rows, lane, m_base, n_base, M);
   }
 
-  // Two blocks of rows at a time (their exchanges between lanes overlap). Columns past the
-  // vocabulary, four at a time since it is a multiple of 8, are kept out by a limit of
-  // -infinity on their maximum and by an infinite offset: one operation a quad for each.
+  // Two blocks of rows at a time (their exchanges between lanes overlap).
   template <class CF, class Acc>
-  static __device__ __forceinline__ void stats(Acc &acc, const Row *rows, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M, int32_t N) {
+  static __device__ __forceinline__ void stats(Acc &acc, const Row *rows, uint32_t lane, int32_t m_base, int32_t n_base, int32_t M) {
     constexpr int MI = CF::MI, NI = CF::NI, G = 2;
     const LossTerms l = loss_terms();
     const uint32_t quarter = lane >> 4;
-    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * quarter), left = N - first;
+    const int32_t row = m_base + (int32_t)(lane & 15u), first = n_base + (int32_t)(4u * quarter);
     float2 *out = l.partial + (size_t)(n_base / CF::WN) * (size_t)M;
-    float limit[NI];
-#pragma unroll
-    for (int ni = 0; ni < NI; ++ni) limit[ni] = 16 * ni < left ? INFINITY : -INFINITY;
 #pragma unroll
     for (int g = 0; g < MI; g += G) {
 #pragma unroll
@@ -117,7 +126,7 @@ struct LossOp {
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) {
           const auto &z = acc[g + u][ni];
-          top[u] = fmaxf(top[u], fminf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), limit[ni]));
+          top[u] = fmaxf(top[u], fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
         }
       }
 #pragma unroll
@@ -129,11 +138,9 @@ struct LossOp {
         const float offset = offset_of(top[u]);
         float s = 0.0f;
 #pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          const float o = fmaxf(offset, -limit[ni]);
+        for (int ni = 0; ni < NI; ++ni)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[g + u][ni][e], kLog2E, -o));
-        }
+          for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[g + u][ni][e], kLog2E, -offset));
         sum[u] = put_right(s, top[u], offset);
         if (__ballot(at[u] >= 0 && at[u] < CF::WN)) {  // few tiles hold a label of theirs
           float picked = 0.0f;
@@ -259,9 +266,11 @@ __global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksAr
   int32_t m_t, n_t;
   decode_super_tile(a.first + (int32_t)tile, a.tiles_m, a.tiles_n, a.super_rows, m_t, n_t);
   const int32_t m = m_t * EDGE + (int32_t)r, n = n_t * EDGE + (int32_t)(8u * q);
-  const bool in = m < a.m && n < a.n;  // (n is a multiple of 8 everywhere)
+  const bool in = m < a.m && n < a.n;
   f32x8 z = {};
   if (in) z = chunk_sum<EDGE, false>(a.ws, tile, r, q, a.chunks);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = n + e < a.n ? z[e] : -INFINITY;  // (see finish)
   if constexpr (FORM == kFormLogitGrad) {
     if (!in) return;
     const RowGrad g = row_grad(a.loss.label[m], a.loss.lse[m], a.loss.weight ? a.loss.weight[m] : 1.0f, a.loss.first, a.loss.entries);

@@ -150,14 +150,14 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
       float top = -INFINITY, sum = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (first < a.n && label == first + q) loss.picked[m] = acc[t][q];
-        top = first < a.n ? fmaxf(top, acc[t][q]) : top;
+        if (first + q < a.n && label == first + q) loss.picked[m] = acc[t][q];
+        top = first + q < a.n ? fmaxf(top, acc[t][q]) : top;
       }
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       const float offset = offset_of(top);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sum += first < a.n ? __builtin_amdgcn_exp2f(fmaf(acc[t][q], kLog2E, -offset)) : 0.0f;
+      for (int q = 0; q < 4; ++q) sum += first + q < a.n ? __builtin_amdgcn_exp2f(fmaf(acc[t][q], kLog2E, -offset)) : 0.0f;
       sum = put_right(sum, top, offset);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);

@@ -89,10 +89,23 @@ def test_loss_sizes(plan, m, n, k):
     check_forward(plan, m, n, k, pad=8)
 
 
+# vocabularies of any length: ends inside a lane's four columns, its eight, a tile
+ODD = [(1, 1, 8), (3, 3, 40), (7, 9, 264), (12, 1001, 136), (24, 16385, 1032), (40, 8197, 2056), (70, 1, 64), (80, 129, 264), (100, 255, 72),
+       (150, 511, 520), (300, 257, 136), (260, 1027, 2056), (600, 3086, 264), (1000, 5003, 128)]
+
+
+@pytest.mark.parametrize("m,n,k", ODD)
+def test_any_vocabulary(plan, m, n, k):
+    say("any vocabulary", m, n, k)
+    check_backward(plan, m, n, k, weighted=True, scaled=True, pad=8)
+    if n > 256:
+        check_backward(plan, m, n, k, 2, F32, F32, accumulate=True)
+
+
 # w large enough that few rows' x goes through LDS: one share of k and several, a share that ends inside a segment, a ragged
 # last block of w
 @pytest.mark.parametrize("m,n,k", [(8, 33032, 1032), (11, 8200, 4104), (16, 2056, 16400), (17, 16392, 1040), (24, 4104, 4112), (32, 2056, 8208),
-                                   (33, 8200, 2064), (48, 1032, 32784), (64, 16392, 1296), (63, 4104, 8200)])
+                                   (33, 8200, 2064), (48, 1032, 32784), (9, 8195, 4104), (30, 2049, 8200), (50, 4102, 4112), (64, 16392, 1296), (63, 4104, 8200)])
 def test_loss_of_some_rows_of_a_large_weight(plan, m, n, k):
     say("cross entropy, some rows", m, n, k)
     check_forward(plan, m, n, k, pad=24)

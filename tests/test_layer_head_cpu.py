@@ -87,7 +87,7 @@ GRAD = ("layer.CrossEntropyGradArgs(**(dict(x=P, w=P, label=P, lse=P, weight=P, 
         "n=64, k=32, ldx=32, ldw=32, lddx=32, lddw=32, dx_type=1, dw_type=1) | kw))")
 BOTH = [(dict(x=None), INVALID), (dict(w=None), INVALID), (dict(label=None), INVALID), (dict(lse=None), INVALID), (dict(x=P + 8), INVALID),
         (dict(w=P + 2), INVALID), (dict(label=P + 4), INVALID), (dict(lse=P + 2), INVALID), (dict(m=-1), SHAPE), (dict(n=0), SHAPE),
-        (dict(n=60), SHAPE), (dict(k=28), SHAPE), (dict(n=(1 << 20) + 8), SHAPE), (dict(k=(1 << 20) + 8), SHAPE), (dict(ldx=24), SHAPE),
+        (dict(n=-1), SHAPE), (dict(k=28), SHAPE), (dict(n=(1 << 20) + 1), SHAPE), (dict(k=(1 << 20) + 8), SHAPE), (dict(ldx=24), SHAPE),
         (dict(ldw=36), SHAPE), (dict(m=(1 << 30) + 1), SHAPE)]
 
 
@@ -105,7 +105,7 @@ def test_cross_entropy_refuses(stand_in):
     assert got == [[s, 0] for _, s in cases]  # refused, and nothing launched
     ok = [dict(m=0, x=None, w=None, label=None, lse=None), dict(m=0, n=0)]
     assert statuses(stand_in, "layer_cross_entropy", LOSS, ok) == [[0, 0]] * 2
-    got = statuses(stand_in, "layer_cross_entropy", LOSS, [dict(), dict(loss=None), dict(k=0, x=None, w=None), dict(m=1, ldx=3)])
+    got = statuses(stand_in, "layer_cross_entropy", LOSS, [dict(), dict(loss=None), dict(k=0, x=None, w=None), dict(m=1, ldx=3), dict(n=1), dict(n=61)])
     assert all(s == 0 and n > 0 for s, n in got)
 
 
@@ -115,14 +115,16 @@ def test_cross_entropy_backward_refuses(stand_in):
                     (dict(accumulate=2), INVALID), (dict(accumulate=-1), INVALID), (dict(lddx=24), SHAPE), (dict(lddw=28), SHAPE),
                     (dict(scratch_bytes=-1), SHAPE), (dict(scratch_bytes=511), SHAPE), (dict(scratch_bytes=0), SHAPE),
                     # a piece of 256, but no room for dx's sum; the sum, but no piece
-                    (dict(n=1024, scratch_bytes=2048), SHAPE), (dict(n=1024, scratch_bytes=2048 + 511), SHAPE)]
+                    (dict(n=1024, scratch_bytes=2048), SHAPE), (dict(n=1024, scratch_bytes=2048 + 511), SHAPE),
+                    # dz's rows are of whole 8s
+                    (dict(n=61, scratch_bytes=2 * 4 * 61), SHAPE), (dict(n=61, scratch_bytes=511), SHAPE)]
     got = statuses(stand_in, "layer_cross_entropy_backward", GRAD, [c[0] for c in cases])
     assert got == [[s, 0] for _, s in cases]
     ok = [dict(m=0, x=None, w=None, label=None, lse=None, dw=None, scratch=None, scratch_bytes=0), dict(m=0, accumulate=1, scratch=None),
           dict(dx=None, dw=None), dict(k=0)]
     assert statuses(stand_in, "layer_cross_entropy_backward", GRAD, ok) == [[0, 0]] * 4
     runs = [dict(), dict(weight=None, dloss=None), dict(n=1024, scratch_bytes=2048 + 512), dict(n=1024, dx_type=0, scratch_bytes=2048),
-            dict(n=1024, dx=None, scratch_bytes=2048), dict(m=0, scratch=None, scratch_bytes=0, dx=None)]
+            dict(n=1024, dx=None, scratch_bytes=2048), dict(m=0, scratch=None, scratch_bytes=0, dx=None), dict(n=61), dict(n=1), dict(n=1021, scratch_bytes=2048 + 512)]
     got = statuses(stand_in, "layer_cross_entropy_backward", GRAD, runs)
     assert all(s == 0 and n > 0 for s, n in got)
 
@@ -133,15 +135,16 @@ def test_int8_product_refuses_what_its_sums_do_not_hold(stand_in):
     assert [s for s, _ in statuses(stand_in, "layer_linear", line, [c[0] for c in cases])] == [s for _, s in cases]
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (1000, 50264, 2056), (4096, 131072, 4096), (7, 1 << 20, 64), (0, 64, 64)])
+@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (1000, 50264, 2056), (4096, 131072, 4096), (7, 1 << 20, 64), (0, 64, 64), (3, 1, 8), (300, 50257, 768), (5, 1021, 64)])
 def test_scratch_sizes(m, n, k):
+    whole = -(-n // 8) * 8
     for pieces in (1, 2, 3, 7, 64, 100000):
         size = ptg.layer_cross_entropy_scratch(m, n, k, pieces)
-        sums = 0 if size == 2 * m * n else 4 * m * k
-        piece = n if m == 0 else (size - sums) // (2 * m)
+        sums = 0 if size == 2 * m * whole else 4 * m * k
+        piece = whole if m == 0 else (size - sums) // (2 * m)
         assert -(-n // piece) <= pieces or piece == 256 or pieces > n // 256
-        assert piece == n or piece % 256 == 0
-    for bad in ((-1, 64, 64, 1), (4, 60, 64, 1), (4, 64, 60, 1), (4, 64, 64, 0)):
+        assert piece == whole or piece % 256 == 0
+    for bad in ((-1, 64, 64, 1), (4, -1, 64, 1), (4, (1 << 20) + 1, 64, 1), (4, 64, 60, 1), (4, 64, 64, 0)):
         with pytest.raises(ValueError):
             ptg.layer_cross_entropy_scratch(*bad)
 
