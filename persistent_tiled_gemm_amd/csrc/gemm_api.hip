@@ -260,14 +260,14 @@ void plan_units(const gemm_plan *p, bool grouped, int32_t mode, int64_t tiles, i
   *items = tiles - r + r * S;
 }
 
-hipError_t launch_form(int edge, int form, int mode, const KernelArgs &args, const ptg::ProductOpArgs &op, const ptg::LossTerms &loss, int grid,
-                       hipStream_t s) {
+hipError_t launch_form(int edge, int form, int mode, bool alone, const KernelArgs &args, const ptg::ProductOpArgs &op, const ptg::LossTerms &loss,
+                       int grid, hipStream_t s) {
   switch (form) {
-    case ptg::kFormNTI8: return ptg::launch_product_i8(edge, mode, args, op, grid, s);
+    case ptg::kFormNTI8: return ptg::launch_product_i8(edge, mode, alone, args, op, grid, s);
     case ptg::kFormNNScaled:
-    case ptg::kFormTNScaled: return ptg::launch_product_scaled(edge, form, mode, args, op, grid, s);
+    case ptg::kFormTNScaled: return ptg::launch_product_scaled(edge, form, mode, alone, args, op, grid, s);
     case ptg::kFormLoss:
-    case ptg::kFormLogitGrad: return ptg::launch_product_loss(edge, form, mode, args, op, loss, grid, s);
+    case ptg::kFormLogitGrad: return ptg::launch_product_loss(edge, form, mode, alone, args, op, loss, grid, s);
     default: return ptg::launch_product(edge, form, mode, args, op, grid, s);
   }
 }
@@ -347,7 +347,7 @@ gemm_status launch(gemm_plan *p, int32_t mode, bool grouped, KernelArgs &args, i
     args.self_clean = 0;
   }
   args.log = p->d_log;
-  e = product ? launch_form(p->desc.bm, form, mode, args, *product, operands->loss, (int)grid, s)
+  e = product ? launch_form(p->desc.bm, form, mode, items <= p->cu_count, args, *product, operands->loss, (int)grid, s)
               : ptg::launch_gemm(p->desc.bm, mode, grouped, p->desc.b_layout == 1, args, (int)grid, p->dyn_lds, s);
   if (e != hipSuccess) return hip_fail(p, e, "kernel launch");
   if (!captured) ++p->runs;

@@ -141,34 +141,37 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // 62, in 8 chunks: 20; 1000 x 4104 x 2056 (rows off the lines), 264 of 128: 58, the
 // last eight in 6 chunks: 47, 68 of 256 in 3 chunks: 55 (chosen: the last eight in 13
 // chunks, whose fit is 40 and whose time 49).
-// int8 and the loss forms take the bf16 figures (a k-step of theirs is 128 int8: 0.26 to
-// 0.33, and 0.45 to 0.85 as more CUs work) with the fill, drain and writes of a CU's
-// further units, 5 and 12, counted: with half the k-steps of bf16 they decide (int8 4096 x
-// 4096 x 1024: 128 without them, 48.9 us; 256, 30.7). Over 36 products of them the choice was
-// within 3% of the best of all edges and splits in 30.
+// The forms of super-tiles (int8, loss, scaled) take the bf16 figures (a k-step of int8 is 64
+// values deep and as long) with the fill, drain and writes of a CU's further units, 5 and
+// 12, counted: with half the k-steps of bf16 they decide (int8 4096 x 4096 x 1024: 128 without
+// them, 48.9 us; 256, 30.7). Their 128 x 128 tiles run two a CU where there are more units than
+// CUs (ProductOp): 0.40 to 0.44 for a k-step of both as the units grow from one to two for each
+// CU, then 0.48 for each two of a CU's units and 0.28 for an odd one.
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN || form == ptg::kFormTNScaled;
   const bool nn = form == ptg::kFormNN || form == ptg::kFormNNScaled;
   const int64_t units = ptg::form_units(form), nk = ceil_div(a.k / units, 32), line = 32 * units;
   const bool off_line = !tn && ((a.m > 1 && a.lda % line != 0) || (!nn && a.ldb % line != 0));
   const double slow128 = off_line ? (e8 ? 1.1 : 1.33) : 1.0, slow256 = off_line ? (e8 ? 1.1 : nn ? 1.05 : 1.13) : 1.0;
-  const bool refill = ptg::form_is_super(form);
+  const bool refill = ptg::form_is_super(form), shared = refill && !tn;
   TileChoice best = {256, 1, 0, 1e300};
   for (const int edge : {128, 256}) {
     const int64_t T = ceil_div(a.m, edge) * ceil_div(a.n, edge);
     const int64_t slots = edge == 256 ? cus : 2 * cus;  // chunks the workspace holds
+    auto pairs = [](int64_t units) { return 0.48 * (double)(units / 2) + 0.28 * (double)(units % 2); };
     // the time of `units` tiles or chunks of `steps` k-steps
     auto run = [&](int64_t units, int64_t steps) {
       const double load = (double)units / (double)cus, rounds = (double)ceil_div(units, cus);
       double step;
       if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.18 * load * load) : (e8 ? 1.12 : 0.66) * rounds);
+      else if (shared) step = slow128 * (load <= 1.0 ? 0.28 : load <= 2.0 ? 0.36 + 0.04 * load : pairs(ceil_div(units, cus)));
       else if (tn) step = load <= 1.0 ? 0.23 : std::max(0.44, 0.23 * load);
       else step = slow128 * (e8 ? 0.41 : 0.28) * rounds;
       return (double)steps * step;
     };
     const int64_t resident = cus * ptg::product_workgroups(edge, form);
     auto fixed = [&](int64_t units) {
-      const double again = refill ? (edge == 256 ? 12.0 : 5.0) * (double)(ceil_div(units, resident) - 1) : 0.0;
+      const double again = refill ? (edge == 256 ? 12.0 : 5.0) * (double)(ceil_div(units, shared ? cus : resident) - 1) : 0.0;
       return (edge == 256 ? 18.0 : 8.0) - (units <= resident ? 2.0 : 0.0) + again;
     };
     const double join = edge == 256 ? 0.06 : 0.02;
@@ -606,7 +609,8 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, 
   int64_t tiles = 0;
   const bool shared = ptg::rows_shared_preferred(k, LAYER_BF16, p->cu_count);
   if (shared || ptg::rows_preferred(k, LAYER_BF16)) {
-    const int64_t sums = shared ? ptg::rows_shared_floats(k, LAYER_BF16, p->cu_count, &tiles) : ptg::rows_partial_floats(k, LAYER_BF16, p->cu_count, &tiles);
+    const int64_t sums = shared ? ptg::rows_shared_floats(k, LAYER_BF16, p->cu_count, &tiles)
+                                : ptg::rows_partial_floats(k, LAYER_BF16, p->cu_count, &tiles);
     const int64_t parts = ceil_div(sums, 2) * 2;
     const int64_t blocks = ceil_div(a->n, shared ? ptg::rows_shared_loss_block(k, p->cu_count) : ptg::rows_loss_block(k, p->cu_count));
     if (parts + 2 * blocks * a->m <= p->ws_floats && tiles <= kArrivals) {

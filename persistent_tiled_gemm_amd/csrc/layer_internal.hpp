@@ -147,16 +147,16 @@ struct ProductOpArgs {
   EpilogueArgs ep;
   int32_t lda, ldb;
 };
-// Workgroups of the tiled product that a CU holds at once.
-constexpr int product_workgroups(int tile_edge, int form) {
-  return tile_edge == 128 && (form == kFormTN || form == kFormTNScaled) ? 2 : 1;
-}
+// Workgroups of the tiled product that a CU holds at once: by its LDS stages, and by form (at most).
+constexpr int stages_workgroups(int tile_edge, int stages) { return tile_edge == 128 && stages == 4 ? 2 : 1; }
+constexpr int product_workgroups(int tile_edge, int form) { return tile_edge == 128 && (form == kFormTN || form_is_super(form)) ? 2 : 1; }
 // mode: kDynamic or kNonPersistent
 hipError_t launch_product(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
-// The same for the int8 form, the scaled forms and the loss forms.
-hipError_t launch_product_i8(int tile_edge, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
-hipError_t launch_product_scaled(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
-hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
+// The same for the int8 form, the scaled forms and the loss forms. alone: no more units than CUs.
+hipError_t launch_product_i8(int tile_edge, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s);
+hipError_t launch_product_scaled(int tile_edge, int form, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, int grid,
+                                 hipStream_t s);
+hipError_t launch_product_loss(int tile_edge, int form, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
                                int grid, hipStream_t s);
 // Adds the chunks of the tiles [first, first + tiles) and finishes them.
 hipError_t launch_product_reduce(int tile_edge, int form, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t first,

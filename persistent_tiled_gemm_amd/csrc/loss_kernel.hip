@@ -47,12 +47,12 @@ __device__ __forceinline__ RowGrad row_grad(int64_t label, float lse, float weig
 __device__ __forceinline__ float probability(float z, const RowGrad &r) { return __builtin_amdgcn_exp2f(fmaf(z, kLog2E, -r.offset)); }
 __device__ __forceinline__ float times_factor(float factor, float v) { return factor == 0.0f ? 0.0f : factor * v; }
 
-template <int FORM>
+template <int FORM, int STAGES>
 struct LossOp {
   using Args = ProductOpArgs;
   static constexpr bool AT = false, BT = true, E8 = false, I8 = false, kPlain = false, kWide = true, kDirect = true, kSuper = true;
   static constexpr bool kGrad = FORM == kFormLogitGrad;
-  template <int EDGE> using Tile = ProductOp<kFormNT>::Tile<EDGE>;
+  template <int EDGE> using Tile = typename ProductOp<kFormNT, STAGES>::template Tile<EDGE>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
 
@@ -246,9 +246,9 @@ struct LossOp {
   }
 };
 
-template <int EDGE, int FORM, int MODE>
-__global__ __launch_bounds__(256, 1) void ptg_loss_kernel(const LossKernelArgs a) {
-  gemm_body<EDGE, EDGE, MODE, false, LossOp<FORM>>(a.gemm, a.op);
+template <int EDGE, int FORM, int STAGES, int MODE>
+__global__ __launch_bounds__(256, stages_workgroups(EDGE, STAGES)) void ptg_loss_kernel(const LossKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, LossOp<FORM, STAGES>>(a.gemm, a.op);
 }
 
 // The tiles that were split along k: their chunks' sums, added in chunk order, then what
@@ -379,20 +379,22 @@ hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, co
   return tile_edge == 256 ? reduce_edge<256>(form, a, tiles, s) : reduce_edge<128>(form, a, tiles, s);
 }
 
-template <int EDGE, int FORM>
-static hipError_t launch_form(int mode, const LossKernelArgs &a, int grid, hipStream_t s) {
-  const dim3 g((uint32_t)grid), b(256);
-  if (mode == kDynamic) hipLaunchKernelGGL((ptg_loss_kernel<EDGE, FORM, kDynamic>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((ptg_loss_kernel<EDGE, FORM, kNonPersistent>), g, b, 0, s, a);
+template <int EDGE, int FORM, int STAGES, int MODE>
+static hipError_t launch_one(const LossKernelArgs &a, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((ptg_loss_kernel<EDGE, FORM, STAGES, MODE>), dim3((uint32_t)grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
+template <int FORM>
+static hipError_t launch_form(int tile_edge, int mode, bool alone, const LossKernelArgs &a, int grid, hipStream_t s) {
+  if (tile_edge == 256) return mode == kDynamic ? launch_one<256, FORM, 4, kDynamic>(a, grid, s) : launch_one<256, FORM, 4, kNonPersistent>(a, grid, s);
+  if (alone) return launch_one<128, FORM, 8, kNonPersistent>(a, grid, s);
+  return mode == kDynamic ? launch_one<128, FORM, 4, kDynamic>(a, grid, s) : launch_one<128, FORM, 4, kNonPersistent>(a, grid, s);
+}
 
-hipError_t launch_product_loss(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
+hipError_t launch_product_loss(int tile_edge, int form, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, const LossTerms &loss,
                                int grid, hipStream_t s) {
   const LossKernelArgs a = {args, op, loss};
-  if (tile_edge == 256)
-    return form == kFormLoss ? launch_form<256, kFormLoss>(mode, a, grid, s) : launch_form<256, kFormLogitGrad>(mode, a, grid, s);
-  return form == kFormLoss ? launch_form<128, kFormLoss>(mode, a, grid, s) : launch_form<128, kFormLogitGrad>(mode, a, grid, s);
+  return form == kFormLoss ? launch_form<kFormLoss>(tile_edge, mode, alone, a, grid, s) : launch_form<kFormLogitGrad>(tile_edge, mode, alone, a, grid, s);
 }
 
 }  // namespace ptg

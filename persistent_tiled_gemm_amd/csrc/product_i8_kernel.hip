@@ -6,9 +6,9 @@
 
 namespace ptg {
 
-template <int EDGE, int MODE>
-__global__ __launch_bounds__(256, product_workgroups(EDGE, kFormNTI8)) void ptg_product_i8_kernel(const ProductKernelArgs a) {
-  gemm_body<EDGE, EDGE, MODE, false, ProductOp<kFormNTI8>>(a.gemm, a.op);
+template <int EDGE, int STAGES, int MODE>
+__global__ __launch_bounds__(256, stages_workgroups(EDGE, STAGES)) void ptg_product_i8_kernel(const ProductKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, ProductOp<kFormNTI8, STAGES>>(a.gemm, a.op);
 }
 
 template <int EDGE>
@@ -16,25 +16,25 @@ __global__ __launch_bounds__(256) void ptg_product_i8_reduce_kernel(const Reduce
   reduce_tiles<EDGE, kScalesRowCol, true, true>(a);
 }
 
-hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first, int32_t tiles, int32_t chunks,
-                            hipStream_t s) {
+hipError_t launch_reduce_i8(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first,
+                            int32_t tiles, int32_t chunks, hipStream_t s) {
   const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks, (m + tile_edge - 1) / tile_edge, super_rows};
   if (tile_edge == 256) hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<256>, dim3(reduce_grid<256>(tiles)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(ptg_product_i8_reduce_kernel<128>, dim3(reduce_grid<128>(tiles)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <int EDGE>
-static hipError_t launch_edge(int mode, const ProductKernelArgs &a, int grid, hipStream_t s) {
-  const dim3 g((uint32_t)grid), b(256);
-  if (mode == kDynamic) hipLaunchKernelGGL((ptg_product_i8_kernel<EDGE, kDynamic>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((ptg_product_i8_kernel<EDGE, kNonPersistent>), g, b, 0, s, a);
+template <int EDGE, int STAGES, int MODE>
+static hipError_t launch_one(const ProductKernelArgs &a, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((ptg_product_i8_kernel<EDGE, STAGES, MODE>), dim3((uint32_t)grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_product_i8(int tile_edge, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+hipError_t launch_product_i8(int tile_edge, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
   const ProductKernelArgs a = {args, op};
-  return tile_edge == 256 ? launch_edge<256>(mode, a, grid, s) : launch_edge<128>(mode, a, grid, s);
+  if (tile_edge == 256) return mode == kDynamic ? launch_one<256, 4, kDynamic>(a, grid, s) : launch_one<256, 4, kNonPersistent>(a, grid, s);
+  if (alone) return launch_one<128, 8, kNonPersistent>(a, grid, s);
+  return mode == kDynamic ? launch_one<128, 4, kDynamic>(a, grid, s) : launch_one<128, 4, kNonPersistent>(a, grid, s);
 }
 
 }  // namespace ptg

@@ -119,7 +119,7 @@ __device__ __forceinline__ void finish_rows(const EpilogueArgs &e, int64_t m, in
   }
 }
 
-template <int FORM>
+template <int FORM, int STAGES = FORM == kFormTN || FORM == kFormTNScaled ? 4 : 8>
 struct ProductOp {
   using Args = ProductOpArgs;
   static constexpr bool AT = FORM == kFormTN || FORM == kFormTNScaled, E8 = FORM == kFormNTE4m3, I8 = FORM == kFormNTI8;
@@ -133,8 +133,12 @@ struct ProductOp {
   // their loads spread over the step; NN 734 -> 700; 1000 x 4104 x 2056 61 -> 47); a
   // pair's loads then have one to two steps to land in a ring of four stages, enough
   // for the 256 x 256 tile's steps but not for the shorter ones of 128 x 128, which
-  // get eight (and one workgroup a CU).
-  template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16, EDGE == 128 && !AT ? 8 : 4>;
+  // get eight (and one workgroup a CU). The forms of super-tiles take eight where every
+  // unit has a CU to itself, and otherwise four and two workgroups a CU, each of which
+  // fills and finishes its tile under the other's MFMAs (int8 2048 x 4096 x 2048, 512 tiles: 22.3
+  // us against 35.7; 1000 x 4104 x 2064, 264 tiles: 22.7 and 31.1 with the last eight split;
+  // 1024 x 4096 x 4096, 256 tiles: 29.3 with four stages, 26.5 with eight).
+  template <int EDGE> using Tile = Cfg<EDGE, EDGE, 2, 2, 16, EDGE == 128 ? STAGES : 4>;
   static __device__ __forceinline__ int32_t lda(const KernelProblem &, const Args &op) { return op.lda; }
   static __device__ __forceinline__ int32_t ldb(const KernelProblem &, const Args &op) { return op.ldb; }
 

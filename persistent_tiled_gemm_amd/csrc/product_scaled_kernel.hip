@@ -5,9 +5,9 @@
 
 namespace ptg {
 
-template <int EDGE, int FORM, int MODE>
-__global__ __launch_bounds__(256, product_workgroups(EDGE, FORM)) void ptg_product_scaled_kernel(const ProductKernelArgs a) {
-  gemm_body<EDGE, EDGE, MODE, false, ProductOp<FORM>>(a.gemm, a.op);
+template <int EDGE, int FORM, int STAGES, int MODE>
+__global__ __launch_bounds__(256, stages_workgroups(EDGE, STAGES)) void ptg_product_scaled_kernel(const ProductKernelArgs a) {
+  gemm_body<EDGE, EDGE, MODE, false, ProductOp<FORM, STAGES>>(a.gemm, a.op);
 }
 
 template <int EDGE>
@@ -15,27 +15,30 @@ __global__ __launch_bounds__(256) void ptg_product_scaled_reduce_kernel(const Re
   reduce_tiles<EDGE, kScalesOne, false, true>(a);
 }
 
-hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first, int32_t tiles, int32_t chunks,
-                                hipStream_t s) {
+hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const float *ws, int32_t m, int32_t n, int32_t super_rows, int32_t first,
+                                int32_t tiles, int32_t chunks, hipStream_t s) {
   const ReduceArgs a = {op.ep, ws, m, n, (n + tile_edge - 1) / tile_edge, first, chunks, (m + tile_edge - 1) / tile_edge, super_rows};
   if (tile_edge == 256) hipLaunchKernelGGL(ptg_product_scaled_reduce_kernel<256>, dim3(reduce_grid<256>(tiles)), dim3(256), 0, s, a);
   else hipLaunchKernelGGL(ptg_product_scaled_reduce_kernel<128>, dim3(reduce_grid<128>(tiles)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <int EDGE, int FORM>
-static hipError_t launch_form(int mode, const ProductKernelArgs &a, int grid, hipStream_t s) {
-  const dim3 g((uint32_t)grid), b(256);
-  if (mode == kDynamic) hipLaunchKernelGGL((ptg_product_scaled_kernel<EDGE, FORM, kDynamic>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((ptg_product_scaled_kernel<EDGE, FORM, kNonPersistent>), g, b, 0, s, a);
+template <int EDGE, int FORM, int STAGES, int MODE>
+static hipError_t launch_one(const ProductKernelArgs &a, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((ptg_product_scaled_kernel<EDGE, FORM, STAGES, MODE>), dim3((uint32_t)grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
+template <int EDGE, int FORM>
+static hipError_t launch_form(int mode, const ProductKernelArgs &a, int grid, hipStream_t s) {
+  return mode == kDynamic ? launch_one<EDGE, FORM, 4, kDynamic>(a, grid, s) : launch_one<EDGE, FORM, 4, kNonPersistent>(a, grid, s);
+}
 
-hipError_t launch_product_scaled(int tile_edge, int form, int mode, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
+hipError_t launch_product_scaled(int tile_edge, int form, int mode, bool alone, const KernelArgs &args, const ProductOpArgs &op, int grid, hipStream_t s) {
   const ProductKernelArgs a = {args, op};
   if (tile_edge == 256)
     return form == kFormNNScaled ? launch_form<256, kFormNNScaled>(mode, a, grid, s) : launch_form<256, kFormTNScaled>(mode, a, grid, s);
-  return form == kFormNNScaled ? launch_form<128, kFormNNScaled>(mode, a, grid, s) : launch_form<128, kFormTNScaled>(mode, a, grid, s);
+  if (form == kFormTNScaled) return launch_form<128, kFormTNScaled>(mode, a, grid, s);
+  return alone ? launch_one<128, kFormNNScaled, 8, kNonPersistent>(a, grid, s) : launch_form<128, kFormNNScaled>(mode, a, grid, s);
 }
 
 }  // namespace ptg

@@ -10,14 +10,14 @@ from tests.test_product_isa import compile_to_asm, loops
 
 pytestmark = isa.pytestmark
 
-# source, kernels as (name and template arguments before the mode)
+# source, kernels as (name and template arguments before the LDS stages and the mode)
 KERNELS = {
     "product_i8_kernel.hip": [("ptg_product_i8_kernel", "Li{edge}E")],
     "product_scaled_kernel.hip": [("ptg_product_scaled_kernel", "Li{edge}ELi5E"), ("ptg_product_scaled_kernel", "Li{edge}ELi6E")],
     "loss_kernel.hip": [("ptg_loss_kernel", "Li{edge}ELi7E"), ("ptg_loss_kernel", "Li{edge}ELi8E")],
 }
-CASES = [(source, name, args, edge, mode) for source, kernels in KERNELS.items() for name, args in kernels for edge in (256, 128)
-         for mode in (2, 0)]
+CASES = [(source, name, args, edge, stages, mode) for source, kernels in KERNELS.items() for name, args in kernels
+         for edge, stages, mode in ((256, 4, 2), (256, 4, 0), (128, 4, 2), (128, 4, 0), (128, 8, 0)) if stages == 4 or "Li6E" not in args]
 
 
 @pytest.fixture(scope="module")
@@ -26,16 +26,16 @@ def asm(tmp_path_factory):
     return {source: compile_to_asm(tmp, source) for source in [*KERNELS, "quantise_kernel.hip", "rows_shared_kernel.hip"]}
 
 
-def kernel_text(text, name, args, edge, mode):
-    i = text.index(f"\n_ZN3ptg{len(name)}{name}I{args.format(edge=edge)}Li{mode}EEE")
+def kernel_text(text, name, args, edge, stages, mode):
+    i = text.index(f"\n_ZN3ptg{len(name)}{name}I{args.format(edge=edge)}Li{stages}ELi{mode}EEE")
     i = text.index(":", i)
     return text[i:text.index(".Lfunc_end", i)]
 
 
-@pytest.mark.parametrize("source,name,args,edge,mode", CASES)
-def test_main_loop_is_one_block_without_copies(asm, source, name, args, edge, mode):
+@pytest.mark.parametrize("source,name,args,edge,stages,mode", CASES)
+def test_main_loop_is_one_block_without_copies(asm, source, name, args, edge, stages, mode):
     step = 64 if edge == 256 else 16  # MFMAs a k-step
-    text = kernel_text(asm[source], name, args, edge, mode)
+    text = kernel_text(asm[source], name, args, edge, stages, mode)
     bodies = loops(text)
     counts = [sum(x.startswith("v_mfma") for x in b) for b in bodies]
     assert sorted(set(counts)) == [2 * step, 4 * step] and counts.count(4 * step) == (2 if mode == 2 else 1), counts
@@ -50,10 +50,10 @@ def test_main_loop_is_one_block_without_copies(asm, source, name, args, edge, mo
             assert sum(x.startswith("v_") and not x.startswith("v_mfma") for x in body) <= 8
 
 
-@pytest.mark.parametrize("source,name,args,edge,mode", CASES)
-def test_mfma_hazard_distances(asm, source, name, args, edge, mode):
+@pytest.mark.parametrize("source,name,args,edge,stages,mode", CASES)
+def test_mfma_hazard_distances(asm, source, name, args, edge, stages, mode):
     """An MFMA result reaches any other reader only after the wait states the longest MFMA needs."""
-    f = isa.instructions(kernel_text(asm[source], name, args, edge, mode))
+    f = isa.instructions(kernel_text(asm[source], name, args, edge, stages, mode))
     first = next(n for n, x in enumerate(f) if x.startswith("v_mfma"))
     last_mfma, pos, result = {}, 0, None
     for x in f[first - 64:]:
@@ -82,11 +82,17 @@ def test_no_kernel_uses_scratch(asm, source):
     assert sizes and not [k for k, s in sizes if int(s) != 0]
 
 
-def test_small_scaled_tiles_leave_room_for_their_neighbours(asm):
-    """TN's 128 x 128 tiles run two workgroups a CU: at most 256 registers (vector and accumulator) a lane."""
-    sizes = re.findall(r"\.amdhsa_kernel _ZN3ptg25ptg_product_scaled_kernelILi128ELi6E\S+.*?\.amdhsa_next_free_vgpr (\d+)",
-                       asm["product_scaled_kernel.hip"], re.S)
-    assert len(sizes) == 2 and all(int(s) <= 256 for s in sizes)
+def test_small_tiles_leave_room_for_their_neighbours(asm):
+    """128 x 128 tiles in four stages run two workgroups a CU: at most 256 registers (vector and accumulator) a lane, and half
+    the LDS."""
+    for source, kernels in KERNELS.items():
+        for name, args in kernels:
+            start = f"_ZN3ptg{len(name)}{name}I{args.format(edge=128)}Li4E"
+            found = re.findall(r"\.amdhsa_kernel " + start + r"\S+(.*?)\.end_amdhsa_kernel", asm[source], re.S)
+            assert len(found) == 2, start
+            for text in found:
+                assert int(re.search(r"\.amdhsa_next_free_vgpr (\d+)", text).group(1)) <= 256
+                assert int(re.search(r"\.amdhsa_group_segment_fixed_size (\d+)", text).group(1)) <= 80 * 1024
 
 
 def test_large_tiles_fit_the_lds_of_a_cu(asm):
