@@ -146,7 +146,10 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // 12, counted: with half the k-steps of bf16 they decide (int8 4096 x 4096 x 1024: 128 without
 // them, 48.9 us; 256, 30.7). Their 128 x 128 tiles run two a CU where there are more units than
 // CUs (ProductOp): 0.40 to 0.44 for a k-step of both as the units grow from one to two for each
-// CU, then 0.48 for each two of a CU's units and 0.28 for an odd one.
+// CU, then 0.48 for each two of a CU's units and 0.28 for an odd one. TN's take 0.44 for each
+// two, and 2 to fill and drain two more. Over 58 products of these forms the time was within
+// 2% of the best of all edges and splits at the mean, up to 16% off for four (777 x 10240 x 1032's
+// dw: 128 as the figures of TN above have it, 38; 256, 33, chosen now).
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
   const bool e8 = form == ptg::kFormNTE4m3, tn = form == ptg::kFormTN || form == ptg::kFormTNScaled;
   const bool nn = form == ptg::kFormNN || form == ptg::kFormNNScaled;
@@ -165,13 +168,14 @@ TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
       double step;
       if (edge == 256) step = slow256 * (load <= 1.0 ? (e8 ? 0.9 + 0.22 * load * load : 0.48 + 0.18 * load * load) : (e8 ? 1.12 : 0.66) * rounds);
       else if (shared) step = slow128 * (load <= 1.0 ? 0.28 : load <= 2.0 ? 0.36 + 0.04 * load : pairs(ceil_div(units, cus)));
-      else if (tn) step = load <= 1.0 ? 0.23 : std::max(0.44, 0.23 * load);
+      else if (tn) step = load <= 1.0 ? 0.23 : refill ? 0.44 * (double)ceil_div(units, 2 * cus) : std::max(0.44, 0.23 * load);
       else step = slow128 * (e8 ? 0.41 : 0.28) * rounds;
       return (double)steps * step;
     };
     const int64_t resident = cus * ptg::product_workgroups(edge, form);
     auto fixed = [&](int64_t units) {
-      const double again = refill ? (edge == 256 ? 12.0 : 5.0) * (double)(ceil_div(units, shared ? cus : resident) - 1) : 0.0;
+      const double each = edge == 256 ? 12.0 : shared ? 5.0 : 2.0;  // (TN's: of two workgroups together)
+      const double again = refill ? each * (double)(ceil_div(units, shared ? cus : resident) - 1) : 0.0;
       return (edge == 256 ? 18.0 : 8.0) - (units <= resident ? 2.0 : 0.0) + again;
     };
     const double join = edge == 256 ? 0.06 : 0.02;

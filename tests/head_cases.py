@@ -114,11 +114,11 @@ CASES = [
     ("tiles 256 logit gradients dynamic; tiles 128 NN one a CU, all split", "dx", 136, 89904, 120),
     ("tiles 256 logit gradients one wave; tiles 128 NN dynamic, last wave split", "dx", 1358, 6432, 6128),
     ("tiles 128 logit gradients dynamic; tiles 128 TN dynamic", "dw", 1, 71528, 72),
-    ("tiles 128 logit gradients one a CU, split; tiles 256 TN one wave", "dw", 390, 2448, 6352),
+    ("tiles 128 logit gradients one a CU, split; tiles 256 TN one wave", "dw", 638, 2408, 3736),
     ("tiles 128 logit gradients one a CU; tiles 128 TN one wave", "dw", 2, 80, 64),
     ("tiles 128 logit gradients one a CU; tiles 128 TN one wave, all split", "dw", 735, 72, 96),
-    ("tiles 128 logit gradients one wave, split; tiles 256 TN dynamic", "dw", 514, 4288, 7296),
     ("tiles 256 logit gradients dynamic, split; tiles 128 TN dynamic", "dw", 170, 67664, 664),
+    ("tiles 256 logit gradients one wave, split; tiles 256 TN dynamic", "dw", 1256, 4072, 7624),
+    ("tiles 256 logit gradients one wave, split; tiles 256 TN dynamic, last wave split", "dw", 2227, 2488, 7720),
     ("tiles 256 logit gradients one wave, split; tiles 256 TN one wave, all split", "dw", 4357, 672, 5496),
-    ("tiles 256 logit gradients one wave; tiles 256 TN dynamic, last wave split", "dw", 2604, 4048, 8240),
 ]
