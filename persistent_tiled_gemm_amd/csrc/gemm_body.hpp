@@ -327,6 +327,7 @@ __device__ __forceinline__ uint32_t claim_next(const KernelArgs &a, uint32_t xcc
 // rows is asked for at the tile's set-up and waits in LDS, two tiles' worth. (finish needs no
 // LDS else, so the next tile's first loads could go out before it: measured, the loss's
 // tiles then took 1 to 4% longer.)
+//
 // The plain product: fp32 C, row strides as long as the rows. BT: B is given as
 // N x K row-major (C = A . B^T); its stage then holds BN rows x 32 k like A's, and
 // its fragments are read like A's.

@@ -2,6 +2,11 @@
 // 16 x 16 x 64 int8 MFMA, which multiplies twice as many values in the same time and
 // adds them in 32-bit integers: sums are exact (k is limited so that they fit) and are
 // rounded once, on their way into the epilogue.
+//
+// Bound by power and MFMA issue where there are tiles enough (8192^3 with a residual 444 us,
+// 2476 TOP/s; bare 407 to 448, by the bits of the operands, and the vendor library's 520); few
+// tiles by their fill, drain and epilogue (1000 x 4104 x 2064: 23 us bare, 36 with bias, gelu,
+// its kept argument and a residual).
 #include "product_op.hpp"
 
 namespace ptg {

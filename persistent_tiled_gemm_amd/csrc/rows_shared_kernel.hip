@@ -7,8 +7,10 @@
 // all the copies of x take at 5.8 TB/s. Here a workgroup owns 16 rows of w a wave and
 // one share of k (of S): it brings x's share to LDS once for all its waves, and each
 // wave then streams its own rows of w over the whole share, with nothing else in its
-// queue. (8192^2: 24 rows 22.0 -> 17.9 us, 64 rows 27.2 -> 20.9; 16384 x 4096: 31.7 -> 20.2.) No wave's sums meet another's; the shares of k meet in the plan's workspace, as
-// in rows_kernel.hip.
+// queue. (8192^2: 24 rows 22.0 -> 17.9 us, 64 rows 27.2 -> 20.9; 16384 x 4096: 31.7 -> 20.2.)
+// No wave's sums meet another's; the shares of k meet in the plan's workspace, as in
+// rows_kernel.hip. Bound by latency at few rows (24 rows: 67 MB of w, 11.6 us at the rate of a
+// plain read): x's way to LDS comes before the first product, the meeting after the last.
 //
 // LDS: 256-byte segments, segment by segment, x's rows one after the other in each; 16-byte
 // chunk c of row r sits in slot c ^ (r mod 16), so that 16 rows' reads of one chunk are
