@@ -305,9 +305,10 @@ __global__ __launch_bounds__(256) void ptg_loss_chunks_kernel(const LossChunksAr
 }
 
 // The blocks of a row joined: R rows a workgroup, whose threads take a slice of the blocks
-// each, eight at a time with all their loads under way, and meet in a tree; the order is
-// fixed. Sixteen rows fill a 128-byte line. One block after the other, each waiting for
-// the one before, took 57 us for 4096 rows of 1024 blocks and 12.6 for 4 rows of 2048.
+// each, eight at a time with all their loads under way, and meet in a tree of lanes, then of
+// waves; the order is fixed. Sixteen rows fill a 128-byte line. Bound by latency: 4 rows of 2048
+// blocks 3.6 us, 4096 rows of 1024 blocks 8.2 (one block after the other, each waiting for
+// the one before, took 12.6 and 57).
 struct LossJoinArgs {
   const float2 *partial;
   const int64_t *label;
@@ -317,10 +318,13 @@ struct LossJoinArgs {
 };
 template <int R>
 __global__ __launch_bounds__(512) void ptg_loss_join_kernel(const LossJoinArgs a) {
-  constexpr int S = 512 / R, U = 8;
-  __shared__ float2 lds[S][R];
+  constexpr int S = 512 / R, U = 8, kWaves = 8;
+  __shared__ float2 lds[kWaves][R];
   const int32_t r = (int32_t)threadIdx.x % R, slice = (int32_t)threadIdx.x / R;
   const int32_t m = (int32_t)blockIdx.x * R + r;
+  const bool ends = slice == 0 && m < a.m;  // writes the row's results
+  const int64_t label = ends ? a.label[m] : -1;
+  const float picked = ends ? a.lse[m] : 0.0f;
   float top = -INFINITY, sum = 0.0f;
   if (m < a.m) {
     for (int32_t b0 = slice; b0 < a.blocks; b0 += U * S) {
@@ -339,22 +343,21 @@ __global__ __launch_bounds__(512) void ptg_loss_join_kernel(const LossJoinArgs a
       top = t;
     }
   }
-  lds[slice][r] = make_float2(top, sum);
 #pragma unroll
-  for (int half = S / 2; half > 0; half >>= 1) {
-    __syncthreads();
-    if (slice < half) {
-      const float2 q = lds[slice + half][r];
-      const float t = fmaxf(top, q.x);
-      sum = rescaled(sum, top, t) + rescaled(q.y, q.x, t);
-      top = t;
-      lds[slice][r] = make_float2(top, sum);
-    }
+  for (int o = R; o < 64; o <<= 1) {
+    const float from = __shfl_xor(top, o, 64), other = __shfl_xor(sum, o, 64), t = fmaxf(top, from);
+    sum = rescaled(sum, top, t) + rescaled(other, from, t);
+    top = t;
   }
-  if (slice != 0 || m >= a.m) return;
+  if ((threadIdx.x & 63u) < (uint32_t)R) lds[threadIdx.x >> 6][r] = make_float2(top, sum);
+  __syncthreads();
+  if (!ends) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, lds[w][r].x);
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += rescaled(lds[w][r].y, lds[w][r].x, top);
   const float lse = top + logf(sum);
-  const int64_t label = a.label[m];
-  const float picked = a.lse[m];
   a.lse[m] = lse;
   if (a.loss) a.loss[m] = label < 0 ? 0.0f : label >= a.entries ? __uint_as_float(0x7fc00000u) : lse - picked;
 }
