@@ -302,12 +302,12 @@ gemm_status layer_quantize(const layer_quantize_args *args, void *stream);
  * the same). A label of n or more is a mistake that no call can see in time: its
  * loss is NaN, and so are its gradients. Logits, maxima and sums are fp32; they
  * are taken tile by tile, 8 bytes a row and block of the vocabulary reach memory.
- * loss may be NULL. lse holds other values while the call runs and shares no memory with
- * loss. A logit of NaN
- * gives the row NaN; w rows of -infinity work where the logit is -infinity.
- * Two launches, three where products are split along k (and in parts of the rows where the
- * workspace does not hold 8 bytes a row and 128 entries for all of them). m == 0
- * enqueues nothing.
+ * loss may be NULL. lse holds other values while the call runs and shares no
+ * memory with loss. A logit of NaN gives the row NaN; w rows of -infinity work
+ * where the logit is -infinity.
+ * Two launches, three where products are split along k (and in parts of the rows
+ * where the workspace does not hold 8 bytes a row and 128 entries for all of
+ * them). m == 0 enqueues nothing.
  * Errors: GEMM_E_INVALID_ARG (a NULL or misaligned pointer, loss and lse the same),
  * GEMM_E_SHAPE (also n == 0 with rows), GEMM_E_DEVICE, GEMM_E_HIP.
  */

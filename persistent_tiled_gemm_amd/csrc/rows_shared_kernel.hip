@@ -208,13 +208,15 @@ __global__ __launch_bounds__(64 * WAVES) void ptg_rows_shared_loss_kernel(const 
 
 // The shape of a call: 16-row blocks of x, the waves of a workgroup (16 rows of w each) and
 // the shares of k: as many as bring the workgroups to the CUs' number, and as x needs to
-// fit. Up to 32 rows four waves with four segments under way; more take eight with two,
-// so that fewer workgroups hold copies of x (int8 8192^2, 64 rows: four 24.2 us, eight 20.9).
+// fit. Up to 32 rows and 128 MiB of w four waves with four segments under way; more of
+// either take eight with two, so that fewer workgroups hold copies of x (int8 8192^2, 64 rows:
+// four 24.2 us, eight 20.9; 32768 x 8192, 24 rows: 63.9 and 54.5; 16384 x 4096, 32 rows: 16.2 and
+// 17.3; the loss of 16384 x 8192, 24 rows: 66.8 and 58.6, of 16384 x 1024, 20 rows: 13.0 and 14.0).
 struct SharedShape { int mt, waves; int64_t tiles, split; };
 static SharedShape shared_shape(const ProductArgs &p, int type, int cu_count) {
   SharedShape f;
   f.mt = p.m <= 16 ? 1 : p.m <= 32 ? 2 : 4;
-  f.waves = f.mt < 4 ? 4 : 8;
+  f.waves = f.mt == 4 || (int64_t)p.n * p.k * (type == kTypeI8 ? 1 : 2) >= (int64_t)128 << 20 ? 8 : 4;
   f.tiles = (p.n + 16 * f.waves - 1) / (16 * f.waves);
   const int64_t segs = ((int64_t)p.k * (type == kTypeI8 ? 1 : 2) + 255) / 256, fits = kSharedBytes / (f.mt * 16 * 256);
   f.split = std::max<int64_t>({1, std::min<int64_t>({cu_count / f.tiles, segs, 16}), (segs + fits - 1) / fits});
@@ -231,17 +233,18 @@ int64_t rows_shared_floats(const ProductArgs &p, int type, int cu_count, int64_t
 // elements of w (8192^2: 4 rows 16.5 us here and 16.1 there, 8 rows 16.4 and 16.6, 24 rows
 // 17.9 and 22.0), from 32 rows on with 16 Mi (4096^2: 24 rows 9.4 and 8.8, 48 rows 10.9 and
 // 11.4). Smaller w runs in the few-row kernel at every m (2048^2, 64 rows: 9.6 and 7.5).
-// The cross entropy's bf16: from 8 rows on with 32 Mi elements (131072 x 2048: 4 rows 111 and
-// 109, 8 rows 112 and 119) and rows of 1024 (100000 x 512, 8 rows: 37 and 30); from 17 on with
-// 16 Mi (4096^2, 24 rows: 16.0 and 18.1) up to where the tiles are as fast, whose x is read
-// less often (24 rows: 8192 x 4096 21.7 here and 28.8 as tiles, 16384 x 8192 67 and 73, 32768 x
-// 4096 68 and 62, 50264 x 2056 83 and 75).
+// The cross entropy's bf16, with rows of 1024 (100000 x 512, 8 rows: 37 and 30): from 2 rows on
+// with 64 Mi elements (131072 x 2048: 1 row 100 and 99, 3 rows 101 and 105; 32768 x 4096, 4 rows:
+// 52.3 and 57.3), from 8 on with 32 Mi; from 17 on with 16 Mi (4096^2, 24 rows: 16.0 and 18.1)
+// up to where the tiles are as fast, whose x is read less often (24 rows: 8192 x 4096 20.8 here
+// and 28.8 as tiles, 16384 x 8192 58.6 and 73, 32768 x 4096 57 and 52, 50264 x 2056, 32 rows: 79
+// and 42).
 bool rows_shared_preferred(const ProductArgs &p, int type, int cu_count) {
   const int64_t size = (int64_t)p.n * p.k, mi = (int64_t)1 << 20;
   if (p.m > kRowsMost || size < 16 * mi || shared_shape(p, type, cu_count).split > 16) return false;
   if (type == kTypeI8) return p.m >= (size < 32 * mi ? 32 : 8);
   if (p.k < 1024) return false;
-  if (p.m <= 16) return p.m >= 8 && size >= 32 * mi;
+  if (p.m <= 16) return size >= 64 * mi ? p.m >= 2 : p.m >= 8 && size >= 32 * mi;
   return p.n <= 32768 && (size < 128 * mi || p.n <= 16384);
 }
 
@@ -264,8 +267,10 @@ hipError_t launch_rows_shared(const ProductArgs &p, float *partial, uint32_t *ar
   const SharedShape f = shared_shape(p, kTypeI8, cu_count);
   const RowsArgs a = rows_args(p, partial, arrivals);
   const dim3 grid((uint32_t)f.tiles, (uint32_t)f.split), block(64 * f.waves);
-  if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<1, 4, 4>), grid, block, 0, s, a);
-  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<2, 4, 4>), grid, block, 0, s, a);
+  if (f.mt == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<1, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<1, 8, 2>), grid, block, 0, s, a);
+  else if (f.mt == 2 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<2, 4, 4>), grid, block, 0, s, a);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<2, 8, 2>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((ptg_rows_shared_i8_kernel<4, 8, 2>), grid, block, 0, s, a);
   return hipGetLastError();
 }
@@ -276,8 +281,10 @@ hipError_t launch_rows_shared_loss(const ProductArgs &p, float *partial, uint32_
   const SharedShape f = shared_shape(p, kTypeBf16, cu_count);
   const RowsArgs a = rows_args(p, partial, arrivals);
   const dim3 grid((uint32_t)f.tiles, (uint32_t)f.split), block(64 * f.waves);
-  if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<1, 4, 4>), grid, block, 0, s, a, p.loss);
-  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<2, 4, 4>), grid, block, 0, s, a, p.loss);
+  if (f.mt == 1 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<1, 4, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 1) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<1, 8, 2>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 2 && f.waves == 4) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<2, 4, 4>), grid, block, 0, s, a, p.loss);
+  else if (f.mt == 2) hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<2, 8, 2>), grid, block, 0, s, a, p.loss);
   else hipLaunchKernelGGL((ptg_rows_shared_loss_kernel<4, 8, 2>), grid, block, 0, s, a, p.loss);
   return hipGetLastError();
 }

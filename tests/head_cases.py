@@ -72,8 +72,10 @@ CASES = [
     ("tiles 256 int8 one wave, all split", "i8", 6371, 168, 16208),
     ("x in LDS i8 1 4 4", "i8", 10, 16448, 2048),
     ("x in LDS i8 1 4 4, k shared", "i8", 11, 3296, 10208),
+    ("x in LDS i8 1 8 2, k shared", "i8", 9, 13264, 10240),
     ("x in LDS i8 2 4 4", "i8", 17, 13632, 2480),
     ("x in LDS i8 2 4 4, k shared", "i8", 32, 4120, 4080),
+    ("x in LDS i8 2 8 2, k shared", "i8", 17, 10952, 12704),
     ("x in LDS i8 4 8 2", "i8", 62, 16440, 1088),
     ("x in LDS i8 4 8 2, k shared", "i8", 33, 2968, 5712),
     ("rows loss 1 1 4 4; join 2", "loss", 2, 16808, 88),
@@ -96,8 +98,11 @@ CASES = [
     ("tiles 256 logits one wave; join 16", "loss", 166, 34048, 128),
     ("x in LDS loss 1 4 4, k shared; join 2", "loss", 11, 4736, 7808),
     ("x in LDS loss 1 4 4; join 2", "loss", 14, 16328, 2144),
+    ("x in LDS loss 1 8 2, k shared; join 2", "loss", 6, 9728, 6984),
+    ("x in LDS loss 1 8 2; join 2", "loss", 2, 20872, 3240),
     ("x in LDS loss 2 4 4, k shared; join 16", "loss", 21, 3136, 5376),
     ("x in LDS loss 2 4 4; join 16", "loss", 19, 9200, 1928),
+    ("x in LDS loss 2 8 2, k shared; join 16", "loss", 17, 16720, 4208),
     ("x in LDS loss 4 8 2, k shared; join 16", "loss", 33, 3144, 5392),
     ("x in LDS loss 4 8 2; join 16", "loss", 42, 17280, 1024),
     ("tiles 128 logit gradients dynamic, split; tiles 128 NN one a CU, all split", "dx", 9, 66168, 496),
