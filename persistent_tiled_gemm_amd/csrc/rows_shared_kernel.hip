@@ -75,7 +75,10 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
   const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)ldw);
   const bool w_in = n0 + (int32_t)row < a.n;
   const uint32_t w_row = row * ldw;  // byte offset of the lane's row
-  f32x4 acc[MT] = {};  // (int8: the bits of integers)
+  // bf16: a sum for every second or fourth step, so that a chain of fp32 additions is no longer than
+  // in rows_kernel.hip, where the waves split k (one sum: a fifth more error at k = 4096)
+  constexpr int kSums = I8 ? 1 : MT == 4 ? 2 : 4;
+  f32x4 sums[MT][kSums] = {};  // (int8: the bits of integers)
   i32x4 w[DEPTH][4];
   auto seg_of = [&](uint32_t g) -> uint32_t { return g + rot < count ? g + rot : g + rot - count; };
   auto load = [&](int d, uint32_t g) {
@@ -95,7 +98,7 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         const i32x4 x = *(const i32x4 *)(seg + (off ^ (uint32_t)(64 * u)) + t * 16 * 256);
-        acc[t] = mfma_step<I8>(w[d][u], x, acc[t]);
+        sums[t][u % kSums] = mfma_step<I8>(w[d][u], x, sums[t][u % kSums]);
       }
   };
   if (count > 0) {
@@ -111,6 +114,16 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
         load(d, g + (uint32_t)(d + DEPTH));
       }
     }
+  }
+
+  f32x4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+#pragma unroll
+    for (int h = kSums / 2; h > 0; h /= 2)
+#pragma unroll
+      for (int q = 0; q < h; ++q) sums[t][q] = add_parts<I8>(sums[t][q], sums[t][q + h]);
+    acc[t] = sums[t][0];
   }
 
   // ---- the shares of k meet: each part through to memory, a relaxed count, and the last
