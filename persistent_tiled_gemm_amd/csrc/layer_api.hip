@@ -147,7 +147,7 @@ struct TileChoice { int edge; int32_t split; int64_t base; double us; };
 // them, 48.9 us; 256, 30.7). Their 128 x 128 tiles run two a CU where there are more units than
 // CUs (ProductOp): 0.40 to 0.44 for a k-step of both as the units grow from one to two for each
 // CU, then 0.48 for each two of a CU's units and 0.28 for an odd one. TN's take 0.44 for each
-// two, and 2 to fill and drain two more. Over 58 products of these forms the time was within
+// two, and 2 to fill and drain two more. Over 71 products of these forms the time was within
 // 2% of the best of all edges and splits at the mean, up to 16% off for four (777 x 10240 x 1032's
 // dw: 128 as the figures of TN above have it, 38; 256, 33, chosen now).
 TileChoice choose_tiles(const ptg::ProductArgs &a, int form, int64_t cus) {
