@@ -71,7 +71,8 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
 
   // ---- w: DEPTH segments of the wave's rows under way. Segments past the share are asked
   // for out of range (zeros, no traffic), so that every turn of the loop is alike and waits for
-  // the oldest segment alone.
+  // the oldest segment alone. They are not multiplied: LDS holds no zeros of x for them, and 0
+  // times an infinity is NaN.
   const __amdgpu_buffer_rsrc_t wr = make_rsrc((const unsigned char *)a.w + (size_t)n0 * (size_t)ldw);
   const bool w_in = n0 + (int32_t)row < a.n;
   const uint32_t w_row = row * ldw;  // byte offset of the lane's row
@@ -92,7 +93,7 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
   };
   const uint32_t off = row * 256u + ((group ^ row) << 4);  // of the lane's chunk in a segment, first step
   auto multiply = [&](int d, uint32_t g) {
-    const unsigned char *seg = xs + seg_of(min(g, count - 1u)) * (uint32_t)(kRows * 256);
+    const unsigned char *seg = xs + seg_of(g) * (uint32_t)(kRows * 256);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -107,13 +108,17 @@ __device__ __forceinline__ void rows_shared(const RowsArgs &a, const LossTerms &
     // x has landed once no more loads are under way than those
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(DEPTH * 4) : "memory");
     wg_barrier();
-    for (uint32_t g = 0; g < count; g += DEPTH) {
+    uint32_t g = 0;
+    for (; g + DEPTH <= count; g += DEPTH) {
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
         multiply(d, g + (uint32_t)d);
         load(d, g + (uint32_t)(d + DEPTH));
       }
     }
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d)
+      if (g + (uint32_t)d < count) multiply(d, g + (uint32_t)d);
   }
 
   f32x4 acc[MT];
