@@ -65,3 +65,20 @@ def test_an_infinity_in_x(plan, m, n, k):
                 v[(t[r] + 1) % n, at] = 1.0  # another one's is
         exact = check(plan, y, v, t, f"{m} {n} {k} from {first}")
         assert not torch.isfinite(exact[0][rows]).any() and torch.isfinite(exact[0][[r for r in range(m) if r % 3 == 1]]).all()
+
+
+@pytest.mark.parametrize("m,n,k", PATHS)
+def test_an_infinite_logit_takes_all(plan, m, n, k):
+    """Entries of the vocabulary with an infinite weight: +infinity for the rows that it meets with a positive value, -infinity for
+    the others; two in one block of columns and one far from them."""
+    say("an infinite logit", m, n, k)
+    x, w = normal(1, m, k), normal(2, n, k, scale=2.0 / k ** 0.5)
+    label = torch.randint(0, n, (m,), generator=torch.Generator().manual_seed(3)).cuda()
+    x[:, 0] = torch.where(torch.arange(m, device="cuda") % 4 < 2, 1.0, -1.0).to(BF16)
+    x[:, k - 1] = torch.where(torch.arange(m, device="cuda") % 4 == 1, 1.0, -1.0).to(BF16)
+    w[:, 0], w[:, k - 1] = 0.5, -0.25
+    w[5, 0], w[9, 0], w[n - 1, k - 1] = INF, INF, INF
+    label[0], label[m // 2], label[m - 1] = 5, 9, n - 1
+    exact = check(plan, x, w, label, f"{m} {n} {k}")
+    rows = torch.arange(m) % 4
+    assert (exact[0][rows < 2] == INF).all() and torch.isfinite(exact[0][rows >= 2]).all()
