@@ -33,7 +33,9 @@ struct layer_plan {
 
 namespace {
 
-constexpr int64_t kArrivals = 4096;  // tiles whose k is shared: CUs / 2 at most (rows_shape), checked at each call
+// Tiles whose k is shared: CUs / 2 at most by rows_shape, and any number with x in LDS (shared_shape also shares a k that
+// does not fit there). Checked at each call: what has more of them runs another way.
+constexpr int64_t kArrivals = 4096;
 
 gemm_status hip_fail(layer_plan *p, hipError_t e, const char *what) {
   if (p) std::snprintf(p->last_error, sizeof(p->last_error), "%s: %s", what, hipGetErrorString(e));
@@ -611,6 +613,9 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *a, layer_cfg p, 
   k.loss.entries = a->n;
   hipError_t e;
   int64_t tiles = 0;
+  // Few rows. Where x in LDS is preferred but its parts outgrow the workspace or the arrival counts (w of 5 Gi elements and
+  // more), the tiles are next, not the other few-row kernel: 16 x 1048576 x 8192 2807 us as tiles (6.1 TB/s) and 3495 there,
+  // 8 x 400000 x 16384 2263 and 2687.
   const bool shared = ptg::rows_shared_preferred(k, LAYER_BF16, p->cu_count);
   if (shared || ptg::rows_preferred(k, LAYER_BF16)) {
     const int64_t sums = shared ? ptg::rows_shared_floats(k, LAYER_BF16, p->cu_count, &tiles)

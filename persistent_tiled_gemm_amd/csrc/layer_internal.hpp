@@ -167,7 +167,7 @@ hipError_t launch_reduce_scaled(int tile_edge, const ProductOpArgs &op, const fl
                                 int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
 hipError_t launch_reduce_loss(int tile_edge, int form, const LossTerms &loss, const float *ws, int32_t m, int32_t n, int32_t super_rows,
                               int32_t first, int32_t tiles, int32_t chunks, hipStream_t s);
-// Columns of a block that leaves one partial maximum and sum: the tiles' and the few-row kernel's.
+// Columns of a block of the tiles that leaves one partial maximum and sum (the few-row kernels': rows_loss_block, rows_shared_loss_block).
 constexpr int32_t loss_block(int tile_edge) { return tile_edge / 2; }
 // lse and loss of m rows from `blocks` partial maxima and sums each; lse holds the labels' logits before.
 hipError_t launch_loss_join(const float2 *partial, int32_t blocks, const int64_t *label, int64_t entries, float *lse, float *loss, int32_t m,

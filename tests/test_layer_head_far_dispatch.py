@@ -11,8 +11,8 @@ def stand_in(tmp_path_factory):
     return hip_stand_in.built(tmp_path_factory.mktemp("stand_in"))
 
 
-def test_the_compared_calls_are_what_they_say(stand_in):
-    cases = head_far_cases.CASES
+@pytest.mark.parametrize("cases", [head_far_cases.CASES, head_far_cases.OUTGROWN], ids=["compared", "outgrown"])
+def test_the_calls_are_what_they_say(stand_in, cases):
     got = hip_stand_in.run(stand_in, head_cases.WHAT_RUNS + f"result = [what_runs(*c) for c in {[c[1:] for c in cases]!r}]")
     assert {f"{c[1:]}": g for c, g in zip(cases, got)} == {f"{c[1:]}": c[0] for c in cases}
 
