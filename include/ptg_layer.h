@@ -332,7 +332,10 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *args, layer_cfg 
  * one fp32 value on the device (NULL: 1), e.g. the 1 / count of a mean; it is applied
  * in fp32 after the products. dx and dw: fp32 or bf16, NULL: not wanted. Rows that
  * are not counted, or weigh 0, have dz = 0 whatever their logits are; x must hold
- * finite values there all the same (0 times NaN is NaN in dw).
+ * finite values there all the same (0 times NaN is NaN in dw). In the same way an
+ * entry that a row of -infinity in w masks has dz = 0, and dw takes such a w, but
+ * dx needs a finite one: 0 times -infinity is NaN, in the infinite columns of every
+ * row of dx.
  *
  * scratch: dz is made and used in pieces of the vocabulary, whole 256s of its
  * entries, as large as scratch_bytes allow: 2 m bytes an entry (of whole 8s) and, with more

@@ -405,8 +405,9 @@ def layer_cross_entropy_backward(x, w, label, lse, scratch, plan: LayerPlan, *, 
                                  accumulate: bool = False, stream=None) -> None:
     """layer_cross_entropy_backward: the gradient of dloss * sum(weight * loss) at the forward pass's lse: dx (m x k) and dw
     (n x k; added to dw with accumulate), each bf16 or fp32 and optional. weight: fp32, one value a row, or None (ones);
-    dloss: one fp32 value on the device, or None (1). scratch: a contiguous device tensor of any dtype; the vocabulary is
-    taken in pieces that fit its bytes (layer_cross_entropy_scratch)."""
+    dloss: one fp32 value on the device, or None (1). x is finite, and so is w where dx is wanted (a w that masks entries with
+    -infinity gives NaN there). scratch: a contiguous device tensor of any dtype; the vocabulary is taken in pieces that fit its
+    bytes (layer_cross_entropy_scratch)."""
     if dx is None and dw is None:
         raise ValueError("layer_cross_entropy_backward needs dx or dw")
     m, n, k, at, px, ldx, pw, ldw = _head(x, w, plan)
