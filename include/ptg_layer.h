@@ -345,7 +345,10 @@ gemm_status layer_cross_entropy(const layer_cross_entropy_args *args, layer_cfg 
  * disposal while the call runs, and any two calls may share it in turn.
  * Three launches a piece, six where products are split along k. With m == 0 dw is
  * zeroed (unless accumulate is set). No result depends on the order in which
- * workgroups run; the pieces' size changes the order of dx's sum.
+ * workgroups run. The pieces' size may change the order of the sums over k, over the
+ * tokens and over the vocabulary, and with it the last bits of dz, dw and dx; the room
+ * for a bf16 dx's sum is not the pieces', so dw alone and dw beside such a dx may
+ * differ in them.
  * Errors: as layer_cross_entropy; GEMM_E_SHAPE where scratch_bytes hold no piece.
  */
 typedef struct layer_cross_entropy_grad_args {

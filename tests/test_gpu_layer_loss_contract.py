@@ -47,3 +47,26 @@ def test_a_vocabulary_masked_in_w(plan, m, n, k, pieces):
     within(dw.t.cpu()[kept], want_dw, dw_off, "dw")
     within(dx.t.cpu()[:, 1:], want_dx[:, 1:], dx_off[:, 1:], "dx")
     assert torch.isnan(dx.t[:, 0]).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(150, 2056, 264), (777, 10248, 520)])
+@pytest.mark.parametrize("dx_t", [BF16, F32])
+def test_dw_alone_and_beside_dx(plan, m, n, k, dx_t):
+    """One scratch for all three calls. The sum of a bf16 dx takes some of it, so that the pieces may be others and with them
+    the order of sums: each result is within the bounds. An fp32 dx takes none: the same pieces, the same bits."""
+    say("dw beside dx", m, n, k, dx_t)
+    x, w, label = head(m, n, k)
+    lse = forward(plan, x, w, label)[0][1: m + 1].clone()
+    room = scratch(m, n, k, 2)
+    both, alone = (Out(m, k, dx_t), Out(n, k, F32)), (Out(m, k, dx_t), Out(n, k, F32))
+    ptg.layer_cross_entropy_backward(x, w, label, lse, room, plan, dx=both[0].t, dw=both[1].t)
+    ptg.layer_cross_entropy_backward(x, w, label, lse, room, plan, dx=alone[0].t)
+    ptg.layer_cross_entropy_backward(x, w, label, lse, room, plan, dw=alone[1].t)
+    torch.cuda.synchronize()
+    want = ref.cross_entropy_backward_bounds(x, w, label, lse, dx_t, F32)
+    for name, exact, a, b in zip(("dx", "dw"), want, both, alone):
+        for t in (a, b):
+            t.check()
+            within(t.t, *exact, name)
+        if dx_t == F32 or name == "dx":
+            assert torch.equal(a.t, b.t), name
