@@ -17,9 +17,9 @@
 // unpredicted token, -1 + p, is exact to p.
 //
 // Bound by power and MFMA issue, as the product is, where there are tiles enough: 4096 x
-// 131072 x 4096, loss 2.94 ms (1495 TFLOP/s; the vendor library's logits alone 3.04), the
-// gradient's logits 390 us of 1140 for each 16384 entries. Few tiles fill and drain: 1000 x
-// 50264 x 2056, 788 tiles of 33 two-step loads, 201 us with w in the last-level cache and 235
+// 131072 x 4096, loss 2.97 ms (1481 TFLOP/s; the vendor library's logits alone 3.06), the
+// gradient's logits 399 us of 1162 for each 16384 entries. Few tiles fill and drain: 1000 x
+// 50264 x 2056, 788 tiles of 33 two-step loads, 201 us with w in the last-level cache and 236
 // from memory; 777 x 10240 x 1032's dz, 160 tiles, 41 us.
 #include "loss_device.hpp"
 #include "product_op.hpp"

@@ -3,10 +3,11 @@
 // adds them in 32-bit integers: sums are exact (k is limited so that they fit) and are
 // rounded once, on their way into the epilogue.
 //
-// Bound by power and MFMA issue where there are tiles enough (8192^3 with a residual 444 us,
-// 2476 TOP/s; bare 407 to 448, by the bits of the operands, and the vendor library's 520); few
-// tiles by their fill, drain and epilogue (1000 x 4104 x 2064: 23 us bare, 36 with bias, gelu,
-// its kept argument and a residual).
+// 8192^3 with a residual takes 446 us (2465 TOP/s; bare 391 to 446, by the bits of the operands,
+// and the vendor library's 519 to 538): some 350 by power and MFMA issue, and some 100 (75 bare)
+// of fill, drain and epilogue, four tiles a CU with nothing beside them (k = 2048 and 4096: 176
+// and 260 us, bare 152 and 229). Few tiles are bound by those (1000 x 4104 x 2064: 23 us bare, 36
+// with bias, gelu, its kept argument and a residual).
 #include "product_op.hpp"
 
 namespace ptg {
